@@ -3,7 +3,7 @@
  *
  * What it computes: Y = X . dequant(Wq, scales, zeros)^T with low-bit weights
  * (int4 / uint4 + zero points, FP4 e2m1 with UE8M0 block scales, FP8 e4m3 with
- * channel scales) and f16 / bf16 / FP8 e4m3 activations, as a dense layer and as
+ * channel scales, int8 with channel scales) and f16 / bf16 / FP8 e4m3 / int8 activations, as a dense layer and as
  * an MoE grouped GEMM over routed tokens.  Sources: the web pages on the Humming
  * quantized-GEMM library -- "Humming" (README), "Key Features" and "Support Matrix"
  * (weight, activation and scale types; dense and MoE GEMM); "Humming: Fast,
@@ -59,13 +59,14 @@ typedef enum {
 enum { QG_W_INT4 = 1,      /* symmetric int4 in [-8, 7], two's-complement nibbles            */
        QG_W_UINT4 = 2,     /* uint4 in [0, 15]; with has_zero, value (u - z) * s              */
        QG_W_FP4_E2M1 = 3,  /* OCP FP4 e2m1 codes                                              */
-       QG_W_FP8_E4M3 = 4   /* OCP FP8 e4m3 ("fn") codes                                       */ };
+       QG_W_FP8_E4M3 = 4,  /* OCP FP8 e4m3 ("fn") codes                                       */
+       QG_W_INT8 = 5       /* int8 in [-128, 127]                                             */ };
 /* Scale types. */
 enum { QG_S_F16 = 1, QG_S_BF16 = 2, QG_S_F32 = 3, QG_S_UE8M0 = 4 };
-/* Activation types.  FP8 activations come with one float32 scale per row (token); FP4
+/* Activation types.  FP8 and int8 activations come with one float32 scale per row (token); FP4
  * activations (MXFP4: packed e2m1 codes, even K in the low nibble) with one UE8M0 exponent
  * byte per 32 consecutive K of a row. */
-enum { QG_A_F16 = 1, QG_A_BF16 = 2, QG_A_FP8_E4M3 = 3, QG_A_FP4_E2M1 = 4 };
+enum { QG_A_F16 = 1, QG_A_BF16 = 2, QG_A_FP8_E4M3 = 3, QG_A_FP4_E2M1 = 4, QG_A_INT8 = 5 };
 /* Output types. */
 enum { QG_O_F16 = 1, QG_O_BF16 = 2 };
 /* Compute options. */
@@ -75,7 +76,9 @@ enum { QG_C_NATIVE = 0,    /* multiply in the activation's type                 
         * "Precision and deployment considerations": no Stream-K-style split and the same
         * MMA type across batch sizes).  Every row count then runs the MFMA kernel without a
         * split over K, so each output row is bitwise the same whatever M (or T) and the other
-        * rows are; slower at small M.  MoE block sizes below 128 are rejected. */
+        * rows are; slower at small M.  MoE block sizes below 128 are rejected.  int8
+        * layers are batch-invariant with and without it (exact integer sums): for them it
+        * changes nothing and every MoE block size stays. */
        QG_C_BATCH_INVARIANT = 4 };
 
 /*
@@ -93,6 +96,8 @@ enum { QG_C_NATIVE = 0,    /* multiply in the activation's type                 
  *   e4m3 weights, f32 block scales (group_k == 128: one scale per 128 output channels x
  *       128 K, scales [E][N/128][K/128], n % 128 == 0), e4m3 activations with one f32
  *       scale per (row, 128-wide K group)                              [block-scaled W8A8]
+ *   int8 weights, f32 channel scales (group_k == 0), int8 activations, k < 2^17: the sum over
+ *       k is exact in 32-bit integers, y = out(float(sum) * scale[n] * x_scale[m])  [int8 W8A8]
  */
 typedef struct {
   int32_t w_type;       /* QG_W_*                                                      */
@@ -146,6 +151,7 @@ size_t qg_prepared_bytes(const qg_layer_desc* desc);
  *            int4/uint4  uint32 [E][N][K/8]  (element k at bits 4*(k%8), low nibble first)
  *            e2m1        uint8  [E][N][K/2]  (even k in the low nibble)
  *            e4m3        uint8  [E][N][K]
+ *            int8        int8   [E][N][K]
  *   scales device, [E][N][G] of the scale type (G = K/group_k, or 1 per channel);
  *          block-scaled e4m3: float32 [E][N/128][K/128]
  *   zeros  device, uint8 [E][N][G] holding 0..15 when has_zero, else NULL
@@ -166,7 +172,7 @@ qg_status qg_prepare(const qg_layer_desc* desc, const void* w, const void* scale
  * workspace holds what such a split (or the W4A8 route below, this library's own
  * reading) needs between launches.
  *   - dense shapes whose output tiles fill at most half the GPU split K over
- *     workgroups: ksplit * m * N * 4 bytes of fp32 partial sums (required:
+ *     workgroups: ksplit * m * N * 4 bytes of fp32 (int8: int32) partial sums (required:
  *     QG_ERR_WORKSPACE without it);
  *   - grouped (MoE) products need none.
  */
@@ -178,9 +184,9 @@ size_t qg_workspace_bytes(const qg_prepared* p, int64_t m_or_tokens, int32_t top
  * product of the inputs with the transposed (dequantized) weight.  "Humming" (wiki
  * article), "Device and workload selection": the kernel configuration follows the range
  * of M, switching where compute starts to outweigh the weight traffic.
- *   x        device [M][K] of a_type (f16/bf16 values or e4m3 codes), or packed e2m1 codes
+ *   x        device [M][K] of a_type (f16/bf16 values, e4m3 codes or int8), or packed e2m1 codes
  *            uint8 [M][K/2] for FP4 activations
- *   x_scale  device, else NULL: float32 per-token scales for e4m3 activations, [M], or
+ *   x_scale  device, else NULL: float32 per-token scales for e4m3 and int8 activations, [M], or
  *            [M][K/128] for block-scaled layers; uint8 UE8M0 exponents [M][K/32] for FP4
  *            activations (X[m, k] = e2m1(code) * 2^(x_scale[m][k/32] - 127))
  *   y        device [M][N] of out_type, written in full (fp32 accumulation, RNE)
@@ -272,7 +278,7 @@ qg_status qg_moe_grouped_map(int32_t layout, const int32_t* offsets_or_counts, i
  * dimension; "Device and workload selection": in the indexed organization the kernel
  * reads each expert's input rows through the routing indices (here sorted_ids).
  *   x        device [T][K] of a_type (FP4: uint8 [T][K/2]);  x_scale device float32 [T] for
- *            e4m3 ([T][K/128] for block-scaled layers), uint8 [T][K/32] for FP4, else NULL
+ *            e4m3 and int8 ([T][K/128] for block-scaled layers), uint8 [T][K/32] for FP4, else NULL
  *   sorted_ids / expert_ids / num_post_pad  from qg_moe_align with the same block_m
  *   block_m  4, 16, 32 or 64 (weight-streaming kernel) or 128, 256 (MFMA kernel; 256 not
  *            for e4m3 or int4->e4m3 weights); FP4 activations: 16, 32, 64 or 128;
@@ -290,6 +296,7 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
  * benchmark paragraph; "Humming" wiki article, "Reported performance") and do not say
  * what joins them; this library's reading is the usual SwiGLU feed-forward layer:
  *
+ *   0. qg_moe_route, where the router's logits are given rather than ids and weights;
  *   1. qg_moe_align, then qg_moe_gemm with the gate/up layer (N = 2*I): Y1 [T*topk][2I];
  *   2. qg_moe_swiglu: act = silu(gate) * up per (token, slot) row -> [T*topk][I];
  *   3. the down product is qg_moe_gemm itself with the down layer (K = I), called with
@@ -312,9 +319,11 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
  *             QG_A_FP4_E2M1: each row quantized for the next product's MXFP4 activations: act
  *             rounded to bfloat16 (nearest even), then exactly qg_quantize_e2m1_rows of those
  *             rows; out = packed e2m1 codes uint8 [rows][inter/2] (16-byte aligned)
- *   out_scale device float32 [rows] for QG_A_FP8_E4M3, uint8 [rows][inter/32] UE8M0 exponents
+ *             QG_A_INT8: each row quantized for the next product's int8 activations, act in
+ *             float32 under the rule of qg_quantize_int8_rows; out = int8 [rows][inter]
+ *   out_scale device float32 [rows] for QG_A_FP8_E4M3 and QG_A_INT8, uint8 [rows][inter/32] UE8M0 exponents
  *             for QG_A_FP4_E2M1, else ignored (may be NULL)
- * inter % 8 == 0 (and inter <= 8192 for QG_A_FP8_E4M3, inter % 32 == 0 for QG_A_FP4_E2M1),
+ * inter % 8 == 0 (and inter <= 8192 for QG_A_FP8_E4M3, <= 32768 for QG_A_INT8, inter % 32 == 0 for QG_A_FP4_E2M1),
  * else QG_ERR_UNSUPPORTED.  Rows of
  * slots the gate/up product did not write give unspecified values, which nothing reads.
  */
@@ -332,6 +341,61 @@ qg_status qg_moe_swiglu(const void* gate_up, int64_t rows, int64_t inter, int32_
  */
 qg_status qg_quantize_e4m3_rows(const void* x, int64_t rows, int64_t k, int32_t in_type, uint8_t* codes, float* scale,
                                 void* stream);
+
+/*
+ * qg_quantize_int8_rows: per-token int8 quantization of 16-bit activations, the input of the int8
+ * W8A8 products.  For each row r < rows of x (device [rows][k], in_type QG_A_F16 / QG_A_BF16,
+ * finite):
+ *   scale[r] = max_i |x[r][i]| / 127 in float32 (1 where that is 0, as for an all-zero row),
+ *   codes[r][i] = x[r][i] / scale[r] in float32, rounded to the nearest integer, ties to even,
+ *                 clamped to [-127, 127].
+ *   codes  device int8 [rows][k] (8-byte aligned);  scale  device float32 [rows]
+ * k % 8 == 0 and k <= 32768, else QG_ERR_UNSUPPORTED.
+ */
+qg_status qg_quantize_int8_rows(const void* x, int64_t rows, int64_t k, int32_t in_type, int8_t* codes, float* scale,
+                                void* stream);
+
+/*
+ * qg_moe_route: from router logits to the experts and weights of every token, the topk_ids and
+ * weights that qg_moe_align, qg_moe_gemm and qg_moe_combine take.  For token t with logits
+ * l[e] = logits[t * row_stride + e], e < E:
+ *   - an expert is eligible unless its logit is NaN or -inf (+inf counts as the largest finite
+ *     float32); with a bias, unless its bias is NaN or -inf either;
+ *   - score s[e] = exp(l[e]) / sum of exp(l) over the experts whose logit is eligible
+ *     (QG_R_SOFTMAX), or 1 / (1 + exp(-l[e])) (QG_R_SIGMOID);
+ *   - choice value c[e] = s[e] + bias[e] with a bias; without one experts compare by their logits
+ *     (the order of their scores);
+ *   - num_groups > 1: the experts form num_groups runs of E / num_groups; a group's value is its
+ *     best choice value (group_top 1) or the sum of its two best (group_top 2; without a bias the
+ *     sum of scores; the one there is where a group has one eligible expert); experts outside the
+ *     topk_groups best groups are not eligible;
+ *   - topk_ids[t][j] = the eligible expert of the j-th largest choice value; equal values, of groups
+ *     too, go to the lowest index; -1 where fewer than topk experts are eligible (the other entry
+ *     points drop such slots);
+ *   - topk_weights[t][j] = s[topk_ids[t][j]] (0 for -1), divided by the sum of the token's chosen
+ *     scores where renormalize is 1 (all 0 where that sum is 0), times weight_scale.
+ * Scores, choice values and sums are held in 64 bits and each weight is rounded to float32 once.
+ *   logits       device [T] rows of E of in_type (QG_L_*), row_stride >= E elements apart, aligned
+ *                to their element
+ *   bias         device float32 [E], or NULL
+ *   topk_ids     device int32 [T][topk];  topk_weights  device float32 [T][topk]; both written in full
+ * E <= 512, topk <= 64, num_groups <= 64, else QG_ERR_UNSUPPORTED; num_groups divides E,
+ * topk_groups <= num_groups and topk <= topk_groups * E / num_groups, else QG_ERR_INVALID_ARG.
+ */
+enum { QG_R_SOFTMAX = 1, QG_R_SIGMOID = 2 };
+enum { QG_L_F16 = 1, QG_L_BF16 = 2, QG_L_F32 = 3 };
+typedef struct {
+  int32_t scoring;      /* QG_R_*                                              */
+  int32_t num_experts;  /* E                                                   */
+  int32_t topk;         /* experts per token                                   */
+  int32_t num_groups;   /* 1: no groups                                        */
+  int32_t topk_groups;  /* groups kept (1 with num_groups == 1)                */
+  int32_t group_top;    /* choice values that make a group's value: 1 or 2     */
+  int32_t renormalize;  /* 1: the chosen scores are divided by their sum       */
+  float weight_scale;   /* factor of every weight                              */
+} qg_route_desc;
+qg_status qg_moe_route(const qg_route_desc* desc, const void* logits, int32_t in_type, int64_t row_stride,
+                       const float* bias, int64_t tokens, int32_t* topk_ids, float* topk_weights, void* stream);
 
 /*
  * qg_quantize_e2m1_rows: MXFP4 quantization of 16-bit activations, the input of the W4A4

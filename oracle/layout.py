@@ -11,7 +11,7 @@ from its specification (not from the library's code):
 Regions, each starting at a 256-byte aligned offset: W, then S, then Z (if zero points).
 
 W: 16-byte units indexed [e][nb = n/16][ku = k/KU][c = n%16], KU = 32 for 4-bit
-   formats and 16 for e4m3; unit byte offset = ((e*NB + nb)*KUN + ku)*256 + c*16.
+   formats and 16 for e4m3 and int8; unit byte offset = ((e*NB + nb)*KUN + ku)*256 + c*16.
    4-bit unit: four little-endian u32 words; word j holds elements k = ku*32 + 8j + i,
    i = 0..7, nibble position p holding element i = ORDER[p]:
      "pair"    [0, 2, 4, 6, 1, 3, 5, 7]  int4/uint4 with f16/bf16 activations
@@ -19,7 +19,7 @@ W: 16-byte units indexed [e][nb = n/16][ku = k/KU][c = n%16], KU = 32 for 4-bit
      "natural" [0, 1, 2, 3, 4, 5, 6, 7]  e2m1
    Nibble value: uint4 -> u; int4 with f16/bf16 activations -> c ^ 8 (biased to q + 8);
    int4 for the e4m3 conversion -> c (two's complement); e2m1 -> c.
-   e4m3 unit: 16 bytes, element k = ku*16 + i at byte i.
+   e4m3 or int8 unit: 16 bytes, element k = ku*16 + i at byte i.
 S: elements [e][nb][g][c] = scale[e][nb*16 + c][g] in the scale type's own bytes
    (2 for f16/bf16, 4 for f32, 1 for UE8M0); channel scales have G = 1.  Block scales of
    e4m3 weights (one per G x G block of output channels x K): [e][n/G][g] as given.
@@ -50,7 +50,7 @@ def order_for(w_type: str, a_type: str) -> str | None:
 
 
 def sizes(w_type, s_type, n, k, group, experts, has_zero):
-    bits = 8 if w_type == "e4m3" else 4
+    bits = 8 if w_type in ("e4m3", "int8") else 4
     g = 1 if group == 0 else k // group
     wb = experts * n * k * bits // 8
     block = w_type == "e4m3" and group > 0          # block scales [e][n/G][k/G], stored as given
@@ -81,9 +81,9 @@ def repack(layer) -> np.ndarray:
     sz = sizes(layer.w_type, layer.s_type, n, k, layer.group, e_, has_zero)
     out = np.zeros(sz["total"], dtype=np.uint8)
     nb = n // 16
-    if layer.w_type == "e4m3":
+    if layer.w_type in ("e4m3", "int8"):
         kun = k // 16
-        codes = np.asarray(layer.w, dtype=np.uint8).reshape(e_, nb, 16, kun, 16)   # e, nb, c, ku, i
+        codes = np.ascontiguousarray(layer.w).view(np.uint8).reshape(e_, nb, 16, kun, 16)   # e, nb, c, ku, i
         units = codes.transpose(0, 1, 3, 2, 4)                                      # e, nb, ku, c, i
         out[:sz["w_bytes"]] = units.reshape(-1)
     else:
@@ -123,10 +123,11 @@ def unpack(buf, w_type, a_type, s_type, n, k, group, experts, has_zero):
     sz = sizes(w_type, s_type, n, k, group, experts, has_zero)
     nb = n // 16
     wbytes = buf[:sz["w_bytes"]]
-    if w_type == "e4m3":
+    if w_type in ("e4m3", "int8"):
         kun = k // 16
         u = wbytes.reshape(experts, nb, kun, 16, 16).transpose(0, 1, 3, 2, 4)
         w = np.ascontiguousarray(u).reshape(experts, n, k)
+        w = w.view(np.int8) if w_type == "int8" else w
     else:
         order = ORDERS[order_for(w_type, a_type)]
         kun = k // 32

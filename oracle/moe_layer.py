@@ -54,6 +54,14 @@ def swiglu_e4m3(gate_up):
     return act, codes, scale
 
 
+def swiglu_int8(gate_up):
+    """SwiGLU in float64, rounded to float32, then quantized per row to int8.  Returns (float64
+    activation [R, I], codes int8 [R, I], scale float32 [R])."""
+    act = swiglu(gate_up)
+    codes, scale = Q.absmax_int8_rows(act.astype(np.float32))
+    return act, codes, scale
+
+
 def swiglu_mxfp4(gate_up):
     """SwiGLU, rounded to bfloat16 (the 16-bit SwiGLU output), then MXFP4-quantized per 32-block
     of each row (the W4A4 down product's activations).  Returns (codes uint8 [R, I/2],

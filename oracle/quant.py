@@ -66,6 +66,16 @@ def absmax_rows(x):
     return round_to_e4m3(q.astype(np.float64)), scale
 
 
+def absmax_int8_rows(x):
+    """Per-row absmax int8: scale = max|row| / 127 in float32 (1 where that is 0), code = the quotient
+    in float32, rounded half to even, clamped to [-127, 127].  Returns (codes int8, scale float32)."""
+    x32 = np.asarray(x, dtype=np.float32)
+    scale = (np.max(np.abs(x32), axis=1) / np.float32(127.0)).astype(np.float32)
+    scale[scale == 0] = np.float32(1.0)
+    q = np.rint((x32 / scale[:, None]).astype(np.float32))
+    return np.clip(q, -127, 127).astype(np.int8), scale
+
+
 # the 8 non-negative e2m1 values, codes 0..7 in ascending order
 _E2M1 = decode_e2m1(np.arange(8))
 

@@ -21,7 +21,7 @@ Passages followed:
 Readings where the pages are silent (each listed in the design notes):
 * zero points are integers in the code domain: w = (u - z) * s;
 * symmetric int4 keeps -8;
-* activations are what the kernel reads: f16/bf16 values, or sx[m] * e4m3(code) (with block
+* activations are what the kernel reads: f16/bf16 values, or sx[m] * e4m3(code) or sx[m] * int8 (with block
   scales sx[m, k / 128] * e4m3(code)), or MXFP4 activations 2^(b[m, k / 32] - 127) * e2m1(code)
   (one UE8M0 exponent per 32 consecutive K of a row, as for MXFP4 weights);
 * block scales ("Humming" wiki article, "Quantization representation": a scale shared across
@@ -41,7 +41,7 @@ def dequant_codes(layer_w, layer_s, layer_z, w_type: str, s_type: str, group: in
     """Dequantize ONE expert's weights to float64 [N, K].
 
     layer_w: packed codes for one expert (uint32 [N, K/8] for int4/uint4, uint8 [N, K/2] for e2m1,
-    uint8 [N, K] for e4m3); layer_s: [N, G]; layer_z: [N, G] uint8 or None.
+    uint8 [N, K] for e4m3, int8 [N, K] for int8); layer_s: [N, G]; layer_z: [N, G] uint8 or None.
     """
     if w_type in ("int4", "uint4"):
         codes = F.unpack_u32_nibbles(layer_w)
@@ -50,6 +50,8 @@ def dequant_codes(layer_w, layer_s, layer_z, w_type: str, s_type: str, group: in
         vals = F.decode_e2m1(F.unpack_u8_nibbles(layer_w))
     elif w_type == "e4m3":
         vals = F.decode_e4m3(layer_w)
+    elif w_type == "int8":
+        vals = np.asarray(layer_w, dtype=np.int8).astype(np.float64)
     else:
         raise ValueError(w_type)
     n = vals.shape[0]
@@ -98,7 +100,7 @@ def activations(acts, a_type: str) -> np.ndarray:
     if a_type == "e2m1":
         sx = F.decode_ue8m0(acts.x_scale)        # [M, K / 32]
         return x * np.repeat(sx, 32, axis=1)
-    if a_type == "e4m3":
+    if a_type in ("e4m3", "int8"):
         sx = np.asarray(acts.x_scale, dtype=np.float32).astype(np.float64)
         if sx.ndim == 2:                       # one scale per (row, group of K / G columns)
             x = x * np.repeat(sx, x.shape[1] // sx.shape[1], axis=1)

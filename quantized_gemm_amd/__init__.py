@@ -5,8 +5,8 @@ stream supplies the hipStream_t, and every step of the computation runs in the
 library's HIP kernels.  The entry points mirror include/qg.h one to one:
 ``prepared_bytes``, ``prepare``, ``workspace_bytes``, ``gemm``, ``moe_block_m``,
 ``moe_capacity``, ``moe_align``, ``moe_grouped_map``, ``moe_gemm``, ``moe_swiglu``,
-``moe_combine``, ``quantize_e4m3_rows``, ``quantize_e2m1_rows``, ``dequant``, ``status_str``,
-``version`` and the measurement helpers ``ceiling_read`` and ``ceiling_mfma``.
+``moe_combine``, ``moe_route``, ``quantize_e4m3_rows``, ``quantize_int8_rows``,
+``quantize_e2m1_rows``, ``dequant``, ``status_str``, ``version`` and the measurement helpers ``ceiling_read`` and ``ceiling_mfma``.
 
 There is no fallback: if libqg.so is missing or cannot be loaded, every call raises.
 """
@@ -19,18 +19,21 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqg.so")
 
 # Enumerations (values as in include/qg.h).
-W_INT4, W_UINT4, W_FP4_E2M1, W_FP8_E4M3 = 1, 2, 3, 4
+W_INT4, W_UINT4, W_FP4_E2M1, W_FP8_E4M3, W_INT8 = 1, 2, 3, 4, 5
 S_F16, S_BF16, S_F32, S_UE8M0 = 1, 2, 3, 4
-A_F16, A_BF16, A_FP8_E4M3, A_FP4_E2M1 = 1, 2, 3, 4
+A_F16, A_BF16, A_FP8_E4M3, A_FP4_E2M1, A_INT8 = 1, 2, 3, 4, 5
 O_F16, O_BF16 = 1, 2
 C_NATIVE, C_W_TO_FP8, C_BATCH_INVARIANT = 0, 1, 4
 MOE_CONTIGUOUS, MOE_MASKED = 1, 2
+R_SOFTMAX, R_SIGMOID = 1, 2
+L_F16, L_BF16, L_F32 = 1, 2, 3
 
 STATUS = {0: "QG_OK", 1: "QG_ERR_INVALID_ARG", 2: "QG_ERR_UNSUPPORTED", 3: "QG_ERR_ARCH_MISMATCH",
           4: "QG_ERR_NOT_PREPARED", 5: "QG_ERR_WORKSPACE", 6: "QG_ERR_CAPACITY", 7: "QG_ERR_HIP"}
 EXPORTS = ["qg_prepared_bytes", "qg_prepare", "qg_workspace_bytes", "qg_gemm", "qg_moe_block_m", "qg_moe_capacity",
            "qg_moe_align", "qg_moe_grouped_map", "qg_moe_gemm", "qg_moe_swiglu", "qg_moe_combine",
-           "qg_quantize_e4m3_rows", "qg_quantize_e2m1_rows", "qg_dequant", "qg_ceiling_read", "qg_ceiling_mfma", "qg_ceiling_lds",
+           "qg_quantize_e4m3_rows", "qg_quantize_int8_rows", "qg_quantize_e2m1_rows", "qg_moe_route", "qg_dequant",
+           "qg_ceiling_read", "qg_ceiling_mfma", "qg_ceiling_lds",
            "qg_gemm_noalloc", "qg_noalloc_scratch_bytes",
            "qg_status_str", "qg_version"]
 
@@ -46,6 +49,12 @@ class LayerDesc(ctypes.Structure):
                 ("has_zero", ctypes.c_int32), ("a_type", ctypes.c_int32), ("compute", ctypes.c_int32),
                 ("out_type", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("n", ctypes.c_int64),
                 ("k", ctypes.c_int64)]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("weight_scale", ctypes.c_float)]
 
 
 class Prepared(ctypes.Structure):
@@ -87,6 +96,9 @@ def lib():
         L.qg_quantize_e4m3_rows.argtypes = [vp, i64, i64, i32, vp, vp, vp]
         L.qg_quantize_e2m1_rows.argtypes, L.qg_quantize_e2m1_rows.restype = [vp, i64, i64, i32, vp, vp, vp], i32
         L.qg_quantize_e4m3_rows.restype = i32
+        L.qg_quantize_int8_rows.argtypes, L.qg_quantize_int8_rows.restype = [vp, i64, i64, i32, vp, vp, vp], i32
+        L.qg_moe_route.argtypes = [ctypes.POINTER(RouteDesc), vp, i32, i64, vp, i64, vp, vp, vp]
+        L.qg_moe_route.restype = i32
         L.qg_dequant.argtypes, L.qg_dequant.restype = [pp, i32, vp, vp], i32
         u64 = ctypes.c_uint64
         L.qg_gemm_noalloc.argtypes, L.qg_gemm_noalloc.restype = [pp, vp, vp, vp, i64, vp], i32
@@ -233,7 +245,7 @@ def moe_gemm_call(p: Prepared, x, x_scale, sorted_ids, expert_ids, num_post_pad,
 
 
 def moe_swiglu(gate_up, rows: int, inter: int, in_type: int, out_type: int, out, out_scale=None, stream=None):
-    """act = silu(gate) * up per row (gate = first ``inter`` columns); f16/bf16, per-row e4m3 or MXFP4 output."""
+    """act = silu(gate) * up per row (gate = first ``inter`` columns); f16/bf16, per-row e4m3 or int8, or MXFP4 output."""
     st = lib().qg_moe_swiglu(_ptr(gate_up), rows, inter, in_type, out_type, _ptr(out), _ptr(out_scale),
                              _stream(stream))
     _check(st, "qg_moe_swiglu")
@@ -251,6 +263,26 @@ def quantize_e4m3_rows(x, rows: int, k: int, in_type: int, codes, scale, stream=
     """Per-token absmax e4m3 quantization of 16-bit rows: codes [rows][k] uint8, scale [rows] float32."""
     st = lib().qg_quantize_e4m3_rows(_ptr(x), rows, k, in_type, _ptr(codes), _ptr(scale), _stream(stream))
     _check(st, "qg_quantize_e4m3_rows")
+
+
+def quantize_int8_rows(x, rows: int, k: int, in_type: int, codes, scale, stream=None):
+    """Per-token absmax int8 quantization of 16-bit rows: codes [rows][k] int8, scale [rows] float32."""
+    st = lib().qg_quantize_int8_rows(_ptr(x), rows, k, in_type, _ptr(codes), _ptr(scale), _stream(stream))
+    _check(st, "qg_quantize_int8_rows")
+
+
+def make_route_desc(scoring, num_experts, topk, num_groups=1, topk_groups=1, group_top=1, renormalize=False,
+                    weight_scale=1.0) -> RouteDesc:
+    return RouteDesc(scoring, num_experts, topk, num_groups, topk_groups, group_top, int(renormalize), weight_scale)
+
+
+def moe_route(desc: RouteDesc, logits, in_type: int, tokens: int, topk_ids, topk_weights, bias=None,
+              row_stride: int | None = None, stream=None):
+    """Router logits [tokens] rows of E (``row_stride`` elements apart, default E) -> topk_ids int32 and
+    topk_weights float32, both [tokens][topk], for moe_align, moe_gemm and moe_combine."""
+    st = lib().qg_moe_route(ctypes.byref(desc), _ptr(logits), in_type, desc.num_experts if row_stride is None else row_stride,
+                            _ptr(bias), tokens, _ptr(topk_ids), _ptr(topk_weights), _stream(stream))
+    _check(st, "qg_moe_route")
 
 
 def quantize_e2m1_rows(x, rows: int, k: int, in_type: int, codes, scales, stream=None):

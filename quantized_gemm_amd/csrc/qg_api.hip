@@ -83,9 +83,9 @@ qg_status check_desc(const qg_layer_desc* dd, PathInfo* pi) {
   const int binv = (dv.compute & QG_C_BATCH_INVARIANT) != 0;
   dv.compute &= ~QG_C_BATCH_INVARIANT;
   const qg_layer_desc* d = &dv;
-  if (d->w_type < QG_W_INT4 || d->w_type > QG_W_FP8_E4M3) return QG_ERR_INVALID_ARG;
+  if (d->w_type < QG_W_INT4 || d->w_type > QG_W_INT8) return QG_ERR_INVALID_ARG;
   if (d->s_type < QG_S_F16 || d->s_type > QG_S_UE8M0) return QG_ERR_INVALID_ARG;
-  if (d->a_type < QG_A_F16 || d->a_type > QG_A_FP4_E2M1) return QG_ERR_INVALID_ARG;
+  if (d->a_type < QG_A_F16 || d->a_type > QG_A_INT8) return QG_ERR_INVALID_ARG;
   if (d->out_type != QG_O_F16 && d->out_type != QG_O_BF16) return QG_ERR_INVALID_ARG;
   if (d->compute != QG_C_NATIVE && d->compute != QG_C_W_TO_FP8) return QG_ERR_INVALID_ARG;
   if (d->has_zero != 0 && d->has_zero != 1) return QG_ERR_INVALID_ARG;
@@ -123,6 +123,8 @@ qg_status check_desc(const qg_layer_desc* dd, PathInfo* pi) {
     if (act16) {
       if (d->out_type != (d->a_type == QG_A_F16 ? QG_O_F16 : QG_O_BF16)) return QG_ERR_UNSUPPORTED;
       p.af = d->a_type == QG_A_F16 ? A_F16 : A_BF16;
+    } else if (d->a_type == QG_A_INT8) {
+      return QG_ERR_UNSUPPORTED;
     } else if (d->a_type == QG_A_FP4_E2M1) {
       p.af = A_FP4;   // W4A4 MXFP4: both operands and both exponents go to the scaled fp4 MFMA
     } else {
@@ -130,6 +132,13 @@ qg_status check_desc(const qg_layer_desc* dd, PathInfo* pi) {
     }
     p.wp_small = WP_FP4; p.order = 0; p.w4 = 1; p.st = S_UE8M0;
     p.dq_wp = WP_FP4;
+  } else if (d->w_type == QG_W_INT8) {
+    if (d->a_type != QG_A_INT8 || d->compute != QG_C_NATIVE || d->has_zero || d->group_k != 0 || d->s_type != QG_S_F32)
+      return QG_ERR_UNSUPPORTED;
+    // |sum| <= k * 128 * 128 has to stay below 2^31 for the 32-bit sums to be exact
+    if (d->k >= (1 << 17)) return QG_ERR_UNSUPPORTED;
+    p.wp_small = WP_INT8; p.w4 = 0; p.af = A_INT8; p.st = S_F32;
+    p.dq_wp = WP_INT8;
   } else {  // e4m3: channel scales (group 0) or 128 x 128 block scales (group 128)
     if (d->a_type != QG_A_FP8_E4M3 || d->compute != QG_C_NATIVE || d->has_zero ||
         (d->group_k != 0 && d->group_k != 128) || d->s_type != QG_S_F32)
@@ -139,16 +148,23 @@ qg_status check_desc(const qg_layer_desc* dd, PathInfo* pi) {
     p.dq_wp = WP_FP8;
   }
   p.wp_mfma = p.wp_small == WP_INT4Q_MAGIC ? WP_INT4Q_FP8 : p.wp_small;
-  p.binv = binv;
+  // exact integer sums, whatever kernel and split adds them, and one order of the scales: int8
+  // products are batch-invariant on every path, so the flag leaves their selector alone
+  p.binv = binv && d->w_type != QG_W_INT8;
   if (pi) *pi = p;
   return QG_OK;
 }
 
 struct Sizes { int64_t wb, sb, zb, off_s, off_z, total, groups; };
 
+// Layers of one byte per weight.
+bool byte_weights(const qg_layer_desc* d) { return d->w_type == QG_W_FP8_E4M3 || d->w_type == QG_W_INT8; }
+// Activations that come with scales.
+bool scaled_acts(const qg_layer_desc* d) { return d->a_type != QG_A_F16 && d->a_type != QG_A_BF16; }
+
 Sizes sizes_of(const qg_layer_desc* d) {
   Sizes s{};
-  const int bits = d->w_type == QG_W_FP8_E4M3 ? 8 : 4;
+  const int bits = byte_weights(d) ? 8 : 4;
   s.groups = d->group_k == 0 ? 1 : d->k / d->group_k;
   s.wb = d->n * d->k * bits / 8;                     // per expert
   s.sb = d->n * s.groups * scale_bytes(d->s_type);   // per expert
@@ -189,10 +205,9 @@ qg_status launched() {
 
 // ---- M-bucket selector --------------------------------------------------------------
 // Weight-streaming family: a workgroup of 2 column blocks x 4 K parts (4-bit weights)
-// or 1 x 8 (e4m3 weights) waves; rows in blocks of 4 / 16 / 32 / 64 (mt = 0 / 1 / 2 / 4).
-StreamTile stream_tile(int64_t rows, int64_t n, int w_type) {
+// or 1 x 8 (e4m3 or int8 weights) waves; rows in blocks of 4 / 16 / 32 / 64 (mt = 0 / 1 / 2 / 4).
+StreamTile stream_tile(int64_t rows, int64_t n, bool w8) {
   StreamTile t{};
-  const bool w8 = w_type == QG_W_FP8_E4M3;
   t.ncb = w8 ? 1 : 2;
   t.kq = w8 ? 8 : 4;
   t.mt = rows <= 4 ? 0 : (rows <= 16 ? 1 : (rows <= 32 ? 2 : 4));
@@ -215,7 +230,7 @@ constexpr int64_t kStreamMaxRows = 64;
 constexpr int kMaxSplit = 8;
 int split_for(int64_t tiles, int64_t k, int group, const PathInfo& pi) {
   if (pi.binv || tiles * 2 > kCUs) return 1;
-  const int64_t bk = pi.af == A_FP8 ? 128 : 64;   // K per step: fp8 MFMAs take 128
+  const int64_t bk = pi.af == A_FP8 || pi.af == A_INT8 ? 128 : 64;   // K per step: 128 bytes
   const int64_t steps = k / bk;
   int sp = 1;
   while (sp < kMaxSplit && tiles * sp * 2 <= kCUs && steps % (sp * 2) == 0 && steps / (sp * 2) >= 8 &&
@@ -247,7 +262,7 @@ MfmaTile mfma_tile(int64_t rows, int64_t n, int64_t k, int group, const PathInfo
   // at 33 / 64 rows 25.1 / 27.3 -> 20.1 / 23.7 us, slower at 96 / 128 rows), and up to 128
   // rows for e4m3 and e2m1 x e4m3 weights (W4A8 MXFP4 at 96 / 128 rows 25.6 / 29.8 -> 19.8 /
   // 21.2 us, block-scaled W8A8 27.8 / 29.3 -> 25.3 / 26.4 us).
-  const int64_t rows64 = pi.af == A_FP8 && pi.wp_mfma != WP_INT4Q_FP8 ? 128 : 64;
+  const int64_t rows64 = (pi.af == A_FP8 && pi.wp_mfma != WP_INT4Q_FP8) || pi.af == A_INT8 ? 128 : 64;
   if (t.bm == 128 && rows <= rows64 && pi.af != A_FP4 && !pi.binv) {
     const int64_t tiles64 = ((rows + 63) / 64) * ntiles;
     const int sp64 = split_for(tiles64, k, group, pi);
@@ -409,7 +424,7 @@ int w4a4_dense_rows(int64_t m, int64_t n, bool binv) {
 // below 2^31 bytes (one expert's weights, all scales, the activations).
 bool fits_rsrc(const qg_prepared* p, int64_t x_rows) {
   const int64_t lim = (int64_t)1 << 31;
-  const int64_t row_bytes = p->desc.a_type == QG_A_FP8_E4M3 ? p->desc.k
+  const int64_t row_bytes = p->desc.a_type == QG_A_FP8_E4M3 || p->desc.a_type == QG_A_INT8 ? p->desc.k
                             : p->desc.a_type == QG_A_FP4_E2M1 ? p->desc.k / 2 : p->desc.k * 2;
   return (int64_t)p->w_expert_bytes < lim && (int64_t)(p->s_expert_bytes * p->desc.num_experts) < lim &&
          (int64_t)(p->z_expert_bytes * p->desc.num_experts) < lim && x_rows * row_bytes < lim;
@@ -424,7 +439,7 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
   if (m < 0) return QG_ERR_INVALID_ARG;
   if (m == 0) return QG_OK;
   if (!x || !y || !aligned16(x) || !aligned16(y)) return QG_ERR_INVALID_ARG;
-  if ((p->desc.a_type == QG_A_FP8_E4M3 || p->desc.a_type == QG_A_FP4_E2M1) && !x_scale) return QG_ERR_INVALID_ARG;
+  if (scaled_acts(&p->desc) && !x_scale) return QG_ERR_INVALID_ARG;
   if (m > (1 << 24) || !fits_rsrc(p, m)) return QG_ERR_UNSUPPORTED;
   s = check_arch();
   if (s != QG_OK) return s;
@@ -487,11 +502,12 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
     if (!launch_mfma_gemm(a, t, pi.wp_mfma, pi.af, pi.of, pi.st, p->desc.has_zero != 0, false, (hipStream_t)stream))
       return QG_ERR_UNSUPPORTED;
     if (t.ksplit > 1 &&
-        !launch_split_reduce(a, pi.wp_mfma == WP_FP8, pi.af == A_FP8, pi.of, (hipStream_t)stream))
+        !launch_split_reduce(a, pi.wp_mfma == WP_FP8 || pi.wp_mfma == WP_INT8, pi.af == A_FP8 || pi.af == A_INT8, pi.of,
+                             (hipStream_t)stream, pi.wp_mfma == WP_INT8))
       return QG_ERR_UNSUPPORTED;
     return launched();
   }
-  StreamTile t = stream_tile(m, p->desc.n, p->desc.w_type);
+  StreamTile t = stream_tile(m, p->desc.n, byte_weights(&p->desc));
   const int sp = stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
   if (sp > 1) {
     const size_t need = dense_workspace(p, pi, m);
@@ -507,8 +523,9 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
   if (!launch_stream_gemm(a, t, pi.wp_small, pi.af, pi.of, pi.st, p->desc.has_zero != 0, false, (hipStream_t)stream))
     return QG_ERR_UNSUPPORTED;
   // block-scaled partials are scaled already; the others take their scales in the reduction
-  if (sp > 1 && !launch_split_reduce(a, pi.wp_small == WP_FP8, pi.af == A_FP8 && !is_block(pi), pi.of,
-                                     (hipStream_t)stream))
+  if (sp > 1 && !launch_split_reduce(a, pi.wp_small == WP_FP8 || pi.wp_small == WP_INT8,
+                                     (pi.af == A_FP8 && !is_block(pi)) || pi.af == A_INT8, pi.of, (hipStream_t)stream,
+                                     pi.wp_small == WP_INT8))
     return QG_ERR_UNSUPPORTED;
   return launched();
 }
@@ -539,7 +556,7 @@ int32_t qg_moe_block_m(const qg_prepared* p, int64_t tokens, int32_t topk) {
   if (busy <= 4) return 4;
   if (is_block(pi) && busy <= 64) return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
   if (mean <= 16) return 16;
-  if (mean <= 24 && pi.af != A_FP8) return 32;
+  if (mean <= 24 && pi.af != A_FP8 && pi.af != A_INT8) return 32;
   // 256-row blocks halve the weight conversion per FLOP and add padding rows: int4 weights
   // converted to e4m3 take them from a mean of 128 rows (E = 64 top-6 skewed, K = 4096: a mean
   // of 144 / 192 / 256 / 512 / 768 rows 240 / 319 / 386 / 663 / 943 -> 221 / 293 / 343 / 568 /
@@ -612,7 +629,7 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
   if (tokens == 0) return QG_OK;
   if (!x || !y || !sorted_ids || !expert_ids || !num_post_pad || !aligned16(x) || !aligned16(y))
     return QG_ERR_INVALID_ARG;
-  if ((p->desc.a_type == QG_A_FP8_E4M3 || p->desc.a_type == QG_A_FP4_E2M1) && !x_scale) return QG_ERR_INVALID_ARG;
+  if (scaled_acts(&p->desc) && !x_scale) return QG_ERR_INVALID_ARG;
   if (block_m != 4 && block_m != 16 && block_m != 32 && block_m != 64 && block_m != 128 && block_m != 256)
     return QG_ERR_UNSUPPORTED;
   if (pi.af == A_FP4 && (block_m == 4 || block_m == 256)) return QG_ERR_UNSUPPORTED;
@@ -653,8 +670,8 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
       return QG_ERR_UNSUPPORTED;
     return launched();
   }
-  StreamTile t = stream_tile(block_m, p->desc.n, p->desc.w_type);
-  if (p->desc.w_type != QG_W_FP8_E4M3) {   // 128 columns per workgroup (see launch_mt)
+  StreamTile t = stream_tile(block_m, p->desc.n, byte_weights(&p->desc));
+  if (!byte_weights(&p->desc)) {   // 128 columns per workgroup (see launch_mt)
     t.ncb = 8;
     t.kq = 1;
     t.grid_x = (unsigned)((p->desc.n / 16 + 7) / 8);
@@ -671,22 +688,24 @@ qg_status qg_moe_swiglu(const void* gate_up, int64_t rows, int64_t inter, int32_
                         void* out_scale, void* stream) {
   if (rows < 0 || inter <= 0) return QG_ERR_INVALID_ARG;
   if (in_type != QG_O_F16 && in_type != QG_O_BF16) return QG_ERR_INVALID_ARG;
-  if (out_type != QG_A_F16 && out_type != QG_A_BF16 && out_type != QG_A_FP8_E4M3 && out_type != QG_A_FP4_E2M1)
+  if (out_type != QG_A_F16 && out_type != QG_A_BF16 && out_type != QG_A_FP8_E4M3 && out_type != QG_A_FP4_E2M1 &&
+      out_type != QG_A_INT8)
     return QG_ERR_INVALID_ARG;
   if (inter % 8 != 0) return QG_ERR_UNSUPPORTED;
   if (out_type == QG_A_FP8_E4M3 && inter > 8192) return QG_ERR_UNSUPPORTED;
   if (out_type == QG_A_FP4_E2M1 && inter % 32 != 0) return QG_ERR_UNSUPPORTED;
+  if (out_type == QG_A_INT8 && inter > kInt8RowMax) return QG_ERR_UNSUPPORTED;
   if (rows > ((int64_t)1 << 31) - 1 || rows * inter > ((int64_t)1 << 40)) return QG_ERR_UNSUPPORTED;
   if (rows == 0) return QG_OK;
   if (!gate_up || !out || !aligned16(gate_up) || !aligned16(out)) return QG_ERR_INVALID_ARG;
-  if (out_type == QG_A_FP8_E4M3 && (!out_scale || ((uintptr_t)out_scale & 3u) != 0)) return QG_ERR_INVALID_ARG;
+  if ((out_type == QG_A_FP8_E4M3 || out_type == QG_A_INT8) && (!out_scale || ((uintptr_t)out_scale & 3u) != 0)) return QG_ERR_INVALID_ARG;
   if (out_type == QG_A_FP4_E2M1 && !out_scale) return QG_ERR_INVALID_ARG;
   qg_status s = check_arch();
   if (s != QG_OK) return s;
   const int in_t = in_type == QG_O_F16 ? O_F16 : O_BF16;
-  const int out_t = out_type == QG_A_FP8_E4M3 ? A_FP8
+  const int out_t = out_type == QG_A_INT8 ? A_INT8 : out_type == QG_A_FP8_E4M3 ? A_FP8
                     : out_type == QG_A_FP4_E2M1 ? A_FP4 : (out_type == QG_A_F16 ? A_F16 : A_BF16);
-  const bool scaled = out_type == QG_A_FP8_E4M3 || out_type == QG_A_FP4_E2M1;
+  const bool scaled = out_type != QG_A_F16 && out_type != QG_A_BF16;
   if (!launch_swiglu(gate_up, rows, inter, in_t, out_t, out, scaled ? out_scale : nullptr, (hipStream_t)stream))
     return QG_ERR_UNSUPPORTED;
   return launched();
@@ -705,6 +724,55 @@ qg_status qg_quantize_e4m3_rows(const void* x, int64_t rows, int64_t k, int32_t 
   if (s != QG_OK) return s;
   if (!launch_quant_rows_e4m3(x, rows, k, in_type == QG_A_F16 ? O_F16 : O_BF16, codes, scale, (hipStream_t)stream))
     return QG_ERR_UNSUPPORTED;
+  return launched();
+}
+
+qg_status qg_quantize_int8_rows(const void* x, int64_t rows, int64_t k, int32_t in_type, int8_t* codes, float* scale,
+                                void* stream) {
+  if (rows < 0 || k <= 0) return QG_ERR_INVALID_ARG;
+  if (in_type != QG_A_F16 && in_type != QG_A_BF16) return QG_ERR_INVALID_ARG;
+  if (k % 8 != 0 || k > kInt8RowMax) return QG_ERR_UNSUPPORTED;
+  if (rows > ((int64_t)1 << 31) - 1) return QG_ERR_UNSUPPORTED;
+  if (rows == 0) return QG_OK;
+  if (!x || !codes || !scale || !aligned16(x) || ((uintptr_t)codes & 7u) != 0 || ((uintptr_t)scale & 3u) != 0)
+    return QG_ERR_INVALID_ARG;
+  qg_status s = check_arch();
+  if (s != QG_OK) return s;
+  if (!launch_quant_rows_int8(x, rows, k, in_type == QG_A_F16 ? O_F16 : O_BF16, false, codes, scale, (hipStream_t)stream))
+    return QG_ERR_UNSUPPORTED;
+  return launched();
+}
+
+qg_status qg_moe_route(const qg_route_desc* d, const void* logits, int32_t in_type, int64_t row_stride, const float* bias,
+                       int64_t tokens, int32_t* topk_ids, float* topk_weights, void* stream) {
+  if (!d || tokens < 0) return QG_ERR_INVALID_ARG;
+  if (d->scoring != QG_R_SOFTMAX && d->scoring != QG_R_SIGMOID) return QG_ERR_INVALID_ARG;
+  if (in_type != QG_L_F16 && in_type != QG_L_BF16 && in_type != QG_L_F32) return QG_ERR_INVALID_ARG;
+  if (d->num_experts <= 0 || d->topk <= 0 || d->num_groups <= 0 || d->topk_groups <= 0) return QG_ERR_INVALID_ARG;
+  if (d->topk > d->num_experts || d->topk_groups > d->num_groups || d->num_experts % d->num_groups != 0)
+    return QG_ERR_INVALID_ARG;
+  if (d->topk > d->topk_groups * (d->num_experts / d->num_groups)) return QG_ERR_INVALID_ARG;
+  if (d->group_top != 1 && d->group_top != 2) return QG_ERR_INVALID_ARG;
+  if (d->renormalize != 0 && d->renormalize != 1) return QG_ERR_INVALID_ARG;
+  if (row_stride < d->num_experts) return QG_ERR_INVALID_ARG;
+  if (d->num_experts > 512 || d->topk > 64 || d->num_groups > 64) return QG_ERR_UNSUPPORTED;
+  if (tokens * d->topk > ((int64_t)1 << 30) || tokens > ((int64_t)1 << 30) || row_stride > ((int64_t)1 << 30))
+    return QG_ERR_UNSUPPORTED;
+  if (tokens == 0) return QG_OK;
+  const uintptr_t esz = in_type == QG_L_F32 ? 4 : 2;
+  if (!logits || !topk_ids || !topk_weights || (uintptr_t)logits % esz != 0 || ((uintptr_t)topk_ids & 3u) != 0 ||
+      ((uintptr_t)topk_weights & 3u) != 0 || ((uintptr_t)bias & 3u) != 0)
+    return QG_ERR_INVALID_ARG;
+  qg_status s = check_arch();
+  if (s != QG_OK) return s;
+  RouteArgs a{};
+  a.logits = logits; a.bias = bias; a.ids = topk_ids; a.weights = topk_weights;
+  a.tokens = tokens; a.stride = row_stride;
+  a.experts = d->num_experts; a.topk = d->topk;
+  a.groups = d->num_groups; a.topk_groups = d->topk_groups; a.group_top = d->group_top;
+  a.softmax = d->scoring == QG_R_SOFTMAX; a.renorm = d->renormalize; a.scale = d->weight_scale;
+  const int in_t = in_type == QG_L_F32 ? S_F32 : in_type == QG_L_BF16 ? S_BF16 : S_F16;
+  if (!launch_moe_route(a, in_t, (hipStream_t)stream)) return QG_ERR_UNSUPPORTED;
   return launched();
 }
 

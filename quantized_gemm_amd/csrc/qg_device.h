@@ -4,7 +4,7 @@
 // Prepared layout (format version 1; the offline transform of "Humming: Fast, Flexible
 // Kernels for Quantized Inference", standard-format paragraph, which reorders weights,
 // scales and zero points into the order the kernel reads them):
-//   W: 16-byte units [e][n/16][k/KU][n%16], KU = 32 (4-bit) or 16 (e4m3).  A 4-bit unit is
+//   W: 16-byte units [e][n/16][k/KU][n%16], KU = 32 (4-bit) or 16 (e4m3, int8).  A 4-bit unit is
 //      four u32 words; word j holds k = 8j..8j+7 of the unit, nibble position p holding
 //      element ORDER[p]:  PAIR {0,2,4,6,1,3,5,7} (int4/uint4 with f16/bf16 activations;
 //      int4 stored biased, q + 8), QUAD {0,4,1,5,2,6,3,7} (int4 for the e4m3 conversion,
@@ -24,12 +24,14 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // Formats (template tags) ---------------------------------------------------------
-enum : int { A_F16 = 1, A_BF16 = 2, A_FP8 = 3, A_FP4 = 4 };
+enum : int { A_F16 = 1, A_BF16 = 2, A_FP8 = 3, A_FP4 = 4, A_INT8 = 5 };
 enum : int { O_F16 = 1, O_BF16 = 2 };
 enum : int { S_F16 = 1, S_BF16 = 2, S_F32 = 3, S_UE8M0 = 4 };
 // Weight paths of the kernels.
@@ -39,7 +41,8 @@ enum : int {
   WP_FP4 = 3,          // e2m1 -> bf16/f16 with the UE8M0 block scale folded in
   WP_FP8 = 4,          // e4m3 used as is, fp8 MFMA
   WP_INT4Q_FP8 = 5,    // int4 (QUAD) -> e4m3 by table, fp8 MFMA, group scale per 128-k MFMA
-  WP_FP8_BLOCK = 6     // e4m3 with 128 x 128 block scales x e4m3 with (row, 128-k) scales, promoted per step
+  WP_FP8_BLOCK = 6,    // e4m3 with 128 x 128 block scales x e4m3 with (row, 128-k) scales, promoted per step
+  WP_INT8 = 7          // int8 used as is, i8 MFMA into 32-bit integers
 };
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
@@ -85,6 +88,16 @@ template <int OF>
 __device__ __forceinline__ uint16_t f32_to_out(float v) {
   if constexpr (OF == O_BF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
   else return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// An int8 product's sum -> output: float(sum) * sw * sx, each step rounded to float32, then to the
+// output type.  The empty asm keeps the last product from being folded into the conversion (which
+// would round once, in some kernels and not in others): every path gives the same bits.
+template <int OF>
+__device__ __forceinline__ uint16_t scaled_out(int sum, float sw, float sx) {
+  float v = (float)sum * sw * sx;
+  asm("" : "+v"(v));
+  return f32_to_out<OF>(v);
 }
 
 // ---- 4-bit unpack ------------------------------------------------------------------
@@ -191,6 +204,15 @@ __device__ __forceinline__ f32x4 mfma16x16x128_fp8(i32x8 a, i32x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
 }
 
+// int8 x int8, 16 bytes of K per lane; both operands take any common order of K.  The sums are
+// exact integers.
+__device__ __forceinline__ i32x4 mfma16x16x64_i8(u32x4 a, u32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ i32x16 mfma32x32x32_i8(i32x4 a, i32x4 b, i32x16 c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+}
+
 // e4m3 activations x e2m1 weights (format code 4) with the weights' UE8M0 block scale:
 // each lane passes the biased exponent of the 32 K it holds of its column (sb); the
 // activation operand's scale is neutral.  The e2m1 operand uses the low 4 dwords of b.
@@ -293,6 +315,7 @@ __device__ __forceinline__ u32x4 bload16_stream(__amdgpu_buffer_rsrc_t r, int of
 // An empty asm that takes a 32x32 accumulator in VGPRs: the value must be computed
 // before this point (device-only, so that no host pass sees a 512-bit register operand).
 __device__ __forceinline__ void keep_in_vgprs(const f32x16& v) { asm volatile("" ::"v"(v)); }
+__device__ __forceinline__ void keep_in_vgprs(const i32x16& v) { asm volatile("" ::"v"(v)); }
 
 // 16 bytes per lane from a buffer straight into LDS: lane l writes lds + 16 l (lds is
 // wave-uniform); an out-of-range offset stores zeros.  Kept out of kernel templates: used

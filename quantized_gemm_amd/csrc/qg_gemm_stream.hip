@@ -7,6 +7,7 @@ bool stream_int4(const StreamArgs&, const StreamTile&, int, int, int, int, bool,
 bool stream_int4q(const StreamArgs&, const StreamTile&, int, int, int, int, bool, bool, hipStream_t);
 bool stream_fp4(const StreamArgs&, const StreamTile&, int, int, int, int, bool, bool, hipStream_t);
 bool stream_fp8(const StreamArgs&, const StreamTile&, int, int, int, int, bool, bool, hipStream_t);
+bool stream_int8(const StreamArgs&, const StreamTile&, int, int, int, int, bool, bool, hipStream_t);
 
 bool launch_stream_gemm(const StreamArgs& a, const StreamTile& t, int wp, int af, int of, int stype, bool zero,
                         bool moe, hipStream_t st) {
@@ -14,11 +15,13 @@ bool launch_stream_gemm(const StreamArgs& a, const StreamTile& t, int wp, int af
   if (stream_int4q(a, t, wp, af, of, stype, zero, moe, st)) return true;
   if (stream_fp4(a, t, wp, af, of, stype, zero, moe, st)) return true;
   if (stream_fp8(a, t, wp, af, of, stype, zero, moe, st)) return true;
+  if (stream_int8(a, t, wp, af, of, stype, zero, moe, st)) return true;
   return false;
 }
 
 bool mfma_int4(const MfmaArgs&, const MfmaTile&, int, int, int, int, bool, bool, hipStream_t);
 bool mfma_fp4(const MfmaArgs&, const MfmaTile&, int, int, int, int, bool, bool, hipStream_t);
+bool mfma_int8(const MfmaArgs&, const MfmaTile&, int, int, int, int, bool, bool, hipStream_t);
 bool mfma_fp8(const MfmaArgs&, const MfmaTile&, int, int, int, int, bool, bool, hipStream_t);
 bool mfma_w4a8(const MfmaArgs&, const MfmaTile&, int, int, int, int, bool, bool, hipStream_t);
 bool mfma_fp8_block(const MfmaArgs&, const MfmaTile&, int, int, int, int, bool, bool, hipStream_t);
@@ -27,6 +30,7 @@ bool launch_mfma_gemm(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int 
                       hipStream_t st) {
   if (mfma_int4(a, t, wp, af, of, stype, zero, moe, st)) return true;
   if (mfma_fp4(a, t, wp, af, of, stype, zero, moe, st)) return true;
+  if (mfma_int8(a, t, wp, af, of, stype, zero, moe, st)) return true;
   if (mfma_fp8(a, t, wp, af, of, stype, zero, moe, st)) return true;
   if (mfma_w4a8(a, t, wp, af, of, stype, zero, moe, st)) return true;
   if (mfma_fp8_block(a, t, wp, af, of, stype, zero, moe, st)) return true;

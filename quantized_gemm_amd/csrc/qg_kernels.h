@@ -12,7 +12,7 @@ struct StreamArgs {
   const void* s;             // prepared S region
   const uint32_t* z;         // prepared Z region or null
   const void* x;             // activations [rows][k]
-  const float* x_scale;      // per-row scales for e4m3 activations
+  const float* x_scale;      // per-row scales for e4m3 and int8 activations
   void* y;                   // output [rows][n]
   int64_t m;                 // dense rows
   int64_t x_rows;            // rows of x (dense: m, MoE: tokens)
@@ -23,7 +23,7 @@ struct StreamArgs {
   const int32_t* expert_ids;
   const int32_t* num_post_pad;
   int topk, sentinel;
-  float* part;               // split K: fp32 partial sums [ksplit][m][n] (workspace)
+  float* part;               // split K: fp32 (int8 products: int32) partial sums [ksplit][m][n] (workspace)
   int ksplit;                // K slices (1: none)
 };
 
@@ -44,8 +44,9 @@ bool launch_mfma_gemm(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int 
                       hipStream_t st);
 
 // Sum of the split-K partials a.part[ksplit][m][n] into a.y, with the e4m3 per-channel
-// (w_scale, fp8 weights) and per-token (a.x_scale, e4m3 activations) scales.
-bool launch_split_reduce(const MfmaArgs& a, bool w_scale, bool x_scale, int of, hipStream_t st);
+// (w_scale, fp8 weights) and per-token (a.x_scale, e4m3 activations) scales.  whole: the partials
+// are 32-bit integers (int8 products; both scales).
+bool launch_split_reduce(const MfmaArgs& a, bool w_scale, bool x_scale, int of, hipStream_t st, bool whole = false);
 
 bool launch_stream_gemm(const StreamArgs& a, const StreamTile& t, int wp, int af, int of, int stype, bool zero,
                         bool moe, hipStream_t st);
@@ -55,7 +56,7 @@ struct RepackArgs {
   const void* w; const void* s; const uint8_t* z;
   uint8_t* out_w; uint8_t* out_s; uint32_t* out_z;
   int experts, n, k, groups;
-  int w4;                    // 1: 4-bit codes, 0: e4m3 bytes
+  int w4;                    // 1: 4-bit codes, 0: e4m3 or int8 bytes
   int order;                 // 0 natural, 1 pair, 2 quad
   int bias8;                 // xor every nibble with 8
   int s_bytes;               // bytes per scale element
@@ -70,13 +71,28 @@ struct DequantArgs {
 void launch_dequant(const DequantArgs& a, hipStream_t st);
 
 // MoE layer steps around the grouped products (qg_moe_layer.hip).  in_t / dtype: O_F16 or
-// O_BF16; out_t: A_F16, A_BF16, A_FP8 (out_scale: float32, one scale per row) or A_FP4
+// O_BF16; out_t: A_F16, A_BF16, A_FP8 or A_INT8 (out_scale: float32, one scale per row) or A_FP4
 // (out: packed e2m1 codes, out_scale: uint8 UE8M0 exponent per 32 outputs).
 bool launch_swiglu(const void* gu, int64_t rows, int64_t inter, int in_t, int out_t, void* out, void* out_scale,
                    hipStream_t st);
 // Per-row absmax e4m3 quantization of 16-bit rows (in_t O_F16 / O_BF16), k <= 8192, k % 8 == 0.
 bool launch_quant_rows_e4m3(const void* x, int64_t rows, int64_t k, int in_t, void* codes, float* scale,
                             hipStream_t st);
+// Per-row absmax int8 quantization of 16-bit rows, or of the SwiGLU of [gate | up] rows (silu);
+// k <= kInt8RowMax, k % 8 == 0.
+constexpr int64_t kInt8RowMax = 1024 * 4 * 8;
+bool launch_quant_rows_int8(const void* x, int64_t rows, int64_t k, int in_t, bool silu, int8_t* codes, float* scale,
+                            hipStream_t st);
+// Routing (qg_moe_route.hip): one row of logits per token, in_t S_F16 / S_BF16 / S_F32.
+struct RouteArgs {
+  const void* logits; const float* bias;
+  int32_t* ids; float* weights;
+  int64_t tokens, stride;
+  int experts, topk, groups, topk_groups, group_top;
+  int softmax, renorm;
+  float scale;
+};
+bool launch_moe_route(const RouteArgs& a, int in_t, hipStream_t st);
 // W4A4 MXFP4 (qg_w4a4.hip): e2m1 x e2m1 with UE8M0 exponents on both sides.  bm = rows per
 // workgroup (16, 32, 64 or 128; MoE: the align block); dense: grid over a.m, MoE: grid_y blocks.
 int w4a4_cols(int bm);

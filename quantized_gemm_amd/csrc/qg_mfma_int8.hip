@@ -1,0 +1,15 @@
+// MFMA-bound GEMM instantiations: int8 weights with int8 activations.
+#include "qg_mfma_kernel.h"
+
+namespace qg {
+
+bool mfma_int8(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int of, int stype, bool zero, bool moe,
+               hipStream_t st) {
+  if (wp == WP_INT8 && af == A_INT8 && of == O_BF16 && stype == S_F32 && zero == false)
+    return launch_mfma_variant<WP_INT8, A_INT8, O_BF16, S_F32, false>(a, t, moe, st);
+  if (wp == WP_INT8 && af == A_INT8 && of == O_F16 && stype == S_F32 && zero == false)
+    return launch_mfma_variant<WP_INT8, A_INT8, O_F16, S_F32, false>(a, t, moe, st);
+  return false;
+}
+
+}  // namespace qg

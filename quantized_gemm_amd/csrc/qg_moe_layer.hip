@@ -12,6 +12,8 @@
 //    [0, E), float32 in slot order, one rounding at the end.
 //  * Per-token e4m3 quantization of 16-bit activations (the input of a W4A8 product), the
 //    same row quantizer without the SwiGLU.
+//  * The same pair for int8 activations: scale = max|row| / 127 (1 where that is 0), code =
+//    round to nearest even of row / scale.
 //
 // All three are HBM-bound streams: 16-byte loads and stores, 8 elements per thread-piece,
 // consecutive lanes on consecutive pieces of a row.  The per-row e4m3 quantization reduces a
@@ -195,6 +197,65 @@ __global__ __launch_bounds__(256) void swiglu_e4m3_wave_kernel(const uint16_t* _
   }
 }
 
+// int8 rows, as they are or as SwiGLU of [gate | up]: one row per NT threads (NT = 64: a wave per
+// row, four rows per workgroup), each keeping up to P pieces of 8 values in registers between the
+// maximum and the codes, so that the row is read once.  The quotient is rounded to float32 and
+// then to an integer, as the definition says; for a row of 16-bit values it decides every code
+// but those of exact halves as exact arithmetic does.
+template <int IN, bool SILU, int NT, int P>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rows_int8_kernel(const uint16_t* __restrict__ x, int64_t rows,
+                                                                       int64_t k, int8_t* __restrict__ codes,
+                                                                       float* __restrict__ scale) {
+  constexpr int RPB = NT < 256 ? 256 / NT : 1;             // rows per workgroup
+  const int tid = threadIdx.x % NT;
+  const int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / NT;
+  if (r >= rows) return;                                   // NT = 64: whole waves leave together
+  const int64_t per_row = k >> 3;
+  const uint16_t* row = x + r * (SILU ? 2 : 1) * k;
+  float v[P][8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t c8 = tid + NT * i;
+    if (c8 < per_row) {
+      if constexpr (SILU) swiglu8<IN>(row, k, c8, v[i]);
+      else unpack8<IN>(ldg16(row + 8 * c8), v[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[i][e]));
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+  if constexpr (NT > 64) {
+    __shared__ float s_wmax[NT / 64];
+    if ((tid & 63) == 0) s_wmax[tid >> 6] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) amax = fmaxf(amax, s_wmax[w]);
+  }
+  float sc = amax / 127.0f;                                // correctly rounded division
+  if (sc == 0.0f) sc = 1.0f;
+  if (tid == 0) scale[r] = sc;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int64_t c8 = tid + NT * i;
+    if (c8 < per_row) {
+      u32x2 o;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float q = fminf(fmaxf(__builtin_rintf(v[i][4 * h + e] / sc), -127.0f), 127.0f);
+          w |= ((uint32_t)(int)q & 0xFFu) << (8 * e);
+        }
+        o[h] = w;
+      }
+      *(u32x2*)(codes + r * k + 8 * c8) = o;
+    }
+  }
+}
+
 // One thread per 8 outputs of a token.  Slots go in groups of 8 with every row load of a
 // group in flight at once: a dropped slot's row exists (it is only unwritten), so it is read
 // like the others and discarded with a select, never multiplied (it may hold NaN).
@@ -256,9 +317,37 @@ static bool launch_rows_e4m3(const uint16_t* g, int64_t rows, int64_t inter, int
   return true;
 }
 
+template <int IN, bool SILU, int NT, int P>
+static void launch_rows_int8_one(const uint16_t* x, int64_t rows, int64_t k, int8_t* codes, float* scale, hipStream_t st) {
+  constexpr int RPB = NT < 256 ? 256 / NT : 1;
+  hipLaunchKernelGGL((rows_int8_kernel<IN, SILU, NT, P>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT * RPB), 0, st, x,
+                     rows, k, codes, scale);
+}
+
+// A wave per row up to 2048 values, 256 threads up to 8192, 1024 up to kInt8RowMax.
+template <int IN, bool SILU>
+static bool launch_rows_int8(const uint16_t* x, int64_t rows, int64_t k, int8_t* codes, float* scale, hipStream_t st) {
+  if (k <= 64 * 4 * 8) launch_rows_int8_one<IN, SILU, 64, 4>(x, rows, k, codes, scale, st);
+  else if (k <= 256 * 4 * 8) launch_rows_int8_one<IN, SILU, 256, 4>(x, rows, k, codes, scale, st);
+  else if (k <= kInt8RowMax) launch_rows_int8_one<IN, SILU, 1024, 4>(x, rows, k, codes, scale, st);
+  else return false;
+  return true;
+}
+
+bool launch_quant_rows_int8(const void* x, int64_t rows, int64_t k, int in_t, bool silu, int8_t* codes, float* scale,
+                            hipStream_t st) {
+  const uint16_t* g = (const uint16_t*)x;
+  if (in_t == O_BF16) return silu ? launch_rows_int8<O_BF16, true>(g, rows, k, codes, scale, st)
+                                  : launch_rows_int8<O_BF16, false>(g, rows, k, codes, scale, st);
+  if (in_t == O_F16) return silu ? launch_rows_int8<O_F16, true>(g, rows, k, codes, scale, st)
+                                 : launch_rows_int8<O_F16, false>(g, rows, k, codes, scale, st);
+  return false;
+}
+
 bool launch_swiglu(const void* gu, int64_t rows, int64_t inter, int in_t, int out_t, void* out, void* out_scale,
                    hipStream_t st) {
   const uint16_t* g = (const uint16_t*)gu;
+  if (out_t == A_INT8) return launch_quant_rows_int8(gu, rows, inter, in_t, true, (int8_t*)out, (float*)out_scale, st);
   if (out_t == A_FP8) return launch_rows_e4m3<true>(g, rows, inter, in_t, out, (float*)out_scale, st);
   if (out_t == A_FP4) {
     const dim3 grid4((unsigned)((rows * (inter >> 5) + 255) / 256));

@@ -122,10 +122,11 @@ void launch_repack(const RepackArgs& a, hipStream_t st) {
 }
 
 // ---- read-back through the kernels' own unpack routines ---------------------------
-// One thread per (n, 32-k unit) (4-bit) or (n, 16-k unit) (e4m3).
+// One thread per (n, 32-k unit) (4-bit) or (n, 16-k unit) (e4m3, int8).
 template <int WP, int AF, int ST>
 __global__ void dequant_kernel(DequantArgs a) {
-  const int64_t kun = (WP == WP_FP8) ? (a.k >> 4) : (a.k >> 5);
+  constexpr bool BYTES = WP == WP_FP8 || WP == WP_INT8;
+  const int64_t kun = BYTES ? (a.k >> 4) : (a.k >> 5);
   const int64_t total = (int64_t)a.n * kun;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= total) return;
@@ -133,7 +134,7 @@ __global__ void dequant_kernel(DequantArgs a) {
   const int64_t ku = i % kun;
   const int nb = (int)(n >> 4), c = (int)(n & 15);
   const u32x4 v = *(const u32x4*)(a.w + ((((int64_t)nb * kun + ku) * 16 + c) << 4));
-  float* out = a.out + n * a.k + ku * ((WP == WP_FP8) ? 16 : 32);
+  float* out = a.out + n * a.k + ku * (BYTES ? 16 : 32);
   if constexpr (WP == WP_FP8) {
     const float sw = ((const float*)a.s)[n];
 #pragma unroll
@@ -145,6 +146,13 @@ __global__ void dequant_kernel(DequantArgs a) {
       out[4 * j + 2] = f1[0] * sw;
       out[4 * j + 3] = f1[1] * sw;
     }
+    return;
+  } else if constexpr (WP == WP_INT8) {
+    const float sw = ((const float*)a.s)[n];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) out[4 * j + q] = (float)(int8_t)(v[j] >> (8 * q)) * sw;
     return;
   } else {
     const int64_t k0 = ku * 32;
@@ -206,7 +214,7 @@ __global__ void dequant_kernel(DequantArgs a) {
 }
 
 void launch_dequant(const DequantArgs& a, hipStream_t st) {
-  const int64_t kun = (a.wp == WP_FP8) ? (a.k >> 4) : (a.k >> 5);
+  const int64_t kun = (a.wp == WP_FP8 || a.wp == WP_INT8) ? (a.k >> 4) : (a.k >> 5);
   const int64_t total = (int64_t)a.n * kun;
   dim3 grid((unsigned)((total + 255) / 256)), block(256);
 #define QG_DQ(WP_, AF_, ST_) \
@@ -222,6 +230,7 @@ void launch_dequant(const DequantArgs& a, hipStream_t st) {
   QG_DQ(WP_FP4, A_BF16, S_UE8M0)
   QG_DQ(WP_FP4, A_F16, S_UE8M0)
   QG_DQ(WP_FP8, A_FP8, S_F32)
+  QG_DQ(WP_INT8, A_INT8, S_F32)
 #undef QG_DQ
 }
 

@@ -14,6 +14,7 @@ Storage formats produced (all row-major numpy arrays):
   int4 is stored as the two's-complement nibble.
 * e2m1 weights: ``uint8 [E, N, K/2]``; even k in the low nibble.
 * e4m3 (OCP "fn" flavour) weights / activations: ``uint8`` codes.
+* int8 weights / activations: ``int8`` values.
 * f16 / bf16 values: ``uint16`` bit patterns.
 * UE8M0 scales: ``uint8`` biased exponents.
 * zero points: ``uint8 [E, N, K/G]`` holding 0..15.
@@ -126,8 +127,8 @@ def router_weights(logits: np.ndarray, ids: np.ndarray) -> np.ndarray:
 class Layer:
     """One quantized layer in storage form plus its activations."""
     name: str
-    w_type: str            # "int4" | "uint4" | "e2m1" | "e4m3"
-    a_type: str            # "f16" | "bf16" | "e4m3" | "e2m1"
+    w_type: str            # "int4" | "uint4" | "e2m1" | "e4m3" | "int8"
+    a_type: str            # "f16" | "bf16" | "e4m3" | "e2m1" | "int8"
     s_type: str            # "f16" | "bf16" | "f32" | "ue8m0"
     out_type: str          # "f16" | "bf16"
     n: int
@@ -143,8 +144,8 @@ class Layer:
 
 @dataclass
 class Acts:
-    x: np.ndarray                  # uint16 bits [M, K] (f16/bf16), uint8 e4m3 codes [M, K] or packed e2m1 [M, K/2]
-    x_scale: np.ndarray | None     # float32 [M] (or [M, K/128]) for e4m3, uint8 UE8M0 [M, K/32] for e2m1
+    x: np.ndarray                  # uint16 bits [M, K] (f16/bf16), uint8 e4m3 codes [M, K], packed e2m1 [M, K/2], int8 [M, K]
+    x_scale: np.ndarray | None     # float32 [M] (or [M, K/128]) for e4m3, float32 [M] for int8, uint8 UE8M0 [M, K/32] for e2m1
     topk_ids: np.ndarray | None    # int32 [T, topk] for MoE
     topk_weights: np.ndarray | None = None   # float32 [T, topk]: router probabilities of the chosen experts
 
@@ -185,6 +186,40 @@ def dense_w8a8_fp8(m: int = 1, n: int = 7168, k: int = 7168, seed: int = 0):
     layer = Layer("dense_w8a8_fp8", "e4m3", "e4m3", "f32", "bf16", n, k, 0, 1,
                   wq.reshape(1, n, k), sw.reshape(1, n, 1), None)
     return layer, Acts(xq, sx, None)
+
+
+def absmax_int8_rows(x: np.ndarray):
+    """Per-row absmax quantization to int8: scale = max|row| / 127 in float32 (1 for an all-zero row),
+    code = x / scale rounded half to even.  Returns (codes int8 [R, C], scale float32 [R])."""
+    x = np.asarray(x, dtype=np.float32)
+    amax = np.max(np.abs(x), axis=1)
+    scale = np.where(amax == 0, np.float32(1.0), amax / np.float32(127.0)).astype(np.float32)
+    return np.clip(np.rint(x / scale[:, None]), -127, 127).astype(np.int8), scale
+
+
+def dense_w8a8_int8(m: int = 1, n: int = 7168, k: int = 7168, out: str = "bf16", seed: int = 0):
+    """Dense int8 W8A8: per-token absmax int8 activations, per-channel absmax int8 weights (N(0, 0.02))."""
+    rng = _rng(seed)
+    xq, sx = absmax_int8_rows(rng.standard_normal((m, k), dtype=np.float32))
+    wf = (rng.standard_normal((n, k), dtype=np.float32) * np.float32(0.02)).astype(np.float32)
+    wq, sw = absmax_int8_rows(wf)
+    layer = Layer("dense_w8a8_int8", "int8", "int8", "f32", out, n, k, 0, 1, wq.reshape(1, n, k), sw.reshape(1, n, 1), None)
+    return layer, Acts(xq, sx, None)
+
+
+def moe_w8a8_int8(t: int = 64, experts: int = 64, topk: int = 6, n: int = 2816, k: int = 4096, out: str = "bf16",
+                  seed: int = 0):
+    """MoE int8 W8A8: per-token absmax int8 activations, per-(expert, channel) absmax int8 weights
+    (N(0, 0.02)), softmax top-k routing of N(0,1) logits."""
+    rng = _rng(seed)
+    xq, sx = absmax_int8_rows(rng.standard_normal((t, k), dtype=np.float32))
+    wf = (rng.standard_normal((experts * n, k), dtype=np.float32) * np.float32(0.02)).astype(np.float32)
+    wq, sw = absmax_int8_rows(wf)
+    logits = rng.standard_normal((t, experts), dtype=np.float32)
+    ids = topk_from_logits(logits, topk)
+    layer = Layer("moe_w8a8_int8", "int8", "int8", "f32", out, n, k, 0, experts, wq.reshape(experts, n, k),
+                  sw.reshape(experts, n, 1), None)
+    return layer, Acts(xq, sx, ids, router_weights(logits, ids))
 
 
 def absmax_e4m3_blocks(x: np.ndarray, br: int, bc: int):
@@ -428,4 +463,6 @@ WORKLOADS = {
     "dense_w8a8_fp8_block": dense_w8a8_fp8_block,
     "dense_w4a4_mxfp4": dense_w4a4_mxfp4,
     "moe_w4a4_mxfp4": moe_w4a4_mxfp4,
+    "dense_w8a8_int8": dense_w8a8_int8,
+    "moe_w8a8_int8": moe_w8a8_int8,
 }
