@@ -100,6 +100,15 @@ __device__ __forceinline__ uint16_t scaled_out(int sum, float sw, float sx) {
   return f32_to_out<OF>(v);
 }
 
+// Two neighbouring outputs of one row, packed.
+template <int OF>
+__device__ __forceinline__ uint32_t scaled_out2(int s0, int s1, float sw0, float sw1, float sx) {
+  float v0 = (float)s0 * sw0 * sx, v1 = (float)s1 * sw1 * sx;
+  asm("" : "+v"(v0));
+  asm("" : "+v"(v1));
+  return pack2<OF == O_BF16 ? A_BF16 : A_F16>(v0, v1);
+}
+
 // ---- 4-bit unpack ------------------------------------------------------------------
 // Magic-number decode: OR a nibble into the mantissa of 1.0.  bf16: 1 + u/128
 // (0x3F80 | u), f16: 1 + u/1024 (0x3C00 | u); both exact.  Dword q of the result holds
@@ -312,10 +321,51 @@ __device__ __forceinline__ u32x4 bload16(__amdgpu_buffer_rsrc_t r, int off) {
 __device__ __forceinline__ u32x4 bload16_stream(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2);   // nt: streamed once
 }
+// The same with a wave-uniform part of the offset (in range together with the lane's).
+__device__ __forceinline__ u32x4 bload16_s(__amdgpu_buffer_rsrc_t r, int off, int soff) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0);
+}
+// Waits until at most N of this wave's vector-memory loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "vmcnt field is 6 bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+// Workgroup barrier without waits (what is shared has been waited for).
+__device__ __forceinline__ void group_barrier() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tile of a dense grid's workgroup.  The dispatcher hands workgroups to the 8 XCDs round-robin, each
+// with its own L2: the grid is cut into XR x (8 / XR) blocks, one per XCD, with XR chosen so that an
+// XCD's share of rows plus columns (rtile, ctile bytes per tile) is smallest, and row tiles are
+// walked fastest inside a block.
+__device__ __forceinline__ void xcd_tile(int id, int mtiles, int ntiles, int64_t rtile, int64_t ctile, int& mtile,
+                                         int& ntile) {
+  int xr = 0;
+  int64_t best = 0;
+  for (int cand = 1; cand <= 8; cand <<= 1) {
+    if (mtiles % cand != 0 || ntiles % (8 / cand) != 0) continue;
+    const int64_t cost = mtiles * rtile / cand + ntiles * ctile / (8 / cand);
+    if (xr == 0 || cost < best) { xr = cand; best = cost; }
+  }
+  if (xr == 0) {
+    ntile = id / mtiles;
+    mtile = id - ntile * mtiles;
+    return;
+  }
+  const int xc = 8 / xr, mt_x = mtiles / xr, nt_x = ntiles / xc;
+  const int x = id & 7, l = id >> 3;
+  const int lm = l % mt_x, ln = l / mt_x;
+  mtile = (x / xc) * mt_x + lm;
+  ntile = (x % xc) * nt_x + ln;
+}
+
 // An empty asm that takes a 32x32 accumulator in VGPRs: the value must be computed
 // before this point (device-only, so that no host pass sees a 512-bit register operand).
 __device__ __forceinline__ void keep_in_vgprs(const f32x16& v) { asm volatile("" ::"v"(v)); }
-__device__ __forceinline__ void keep_in_vgprs(const i32x16& v) { asm volatile("" ::"v"(v)); }
 
 // 16 bytes per lane from a buffer straight into LDS: lane l writes lds + 16 l (lds is
 // wave-uniform); an out-of-range offset stores zeros.  Kept out of kernel templates: used

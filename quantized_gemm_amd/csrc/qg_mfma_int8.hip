@@ -1,14 +1,329 @@
-// MFMA-bound GEMM instantiations: int8 weights with int8 activations.
-#include "qg_mfma_kernel.h"
+// MFMA-bound int8 x int8 product for more rows than weight streaming serves: dense tiles (with K
+// split over workgroups where the tiles are few) and MoE blocks.
+//
+//   sum[m][n] = sum_k x[m][k] w[n][k] in 32-bit integers (exact, so every tile and split gives the
+//   same), y = out(float(sum) * sw[n] * sx[m]).
+//
+// Nothing is converted on the way, so the tile is chosen for the operands' feed: BM rows x 256
+// columns, 4 waves of all BM rows x 64 columns.  Per 128-wide K step a CU reads BM x 128 bytes of
+// activations and 256 x 128 bytes of weights, each once, and its waves read the activations from
+// LDS four times; eight waves of 32 columns, as the paths that convert weights take, read them
+// eight times.  256-row tiles run one wave per SIMD with the accumulators in the 256 AGPRs;
+// 128- and 64-row tiles run two.
+//
+// Activations go HBM -> LDS (buffer_load ... lds) into a ring of four 128-byte-wide stages, 16-byte
+// chunks XOR-swizzled by row bits 1..3 (conflict-free 16-byte fragment reads); weights go HBM ->
+// VGPR, one 16-byte unit of the prepared image being one lane's operand of one 32x32x32 MFMA.
+//
+// The weights are the MFMAs' first operand, so a lane's products share one activation row (lane (r, g)
+// of a tile: row r, columns 8 (i / 4) + 4 g + i % 4): one row scale per lane and row tile, and four
+// outputs of a row side by side, written into the epilogue's LDS rows 8 bytes at a time.
+//
+// A step is four sub-steps of 32 K.  Sub-step j multiplies, per row tile, NT MFMAs, and right after
+// them reads that tile's fragment of sub-step j + 1 into the same registers: a fragment is read a
+// whole sub-step before it is needed.  So that sub-step 3 can read the next stage, stages are handed
+// over in the middle of a step: after sub-step 1 each wave waits for its own loads of stage
+// step + 1 and passes the barrier; past it that stage is visible to all, and the stage that
+// step - 1 read is free for step + 3, whose loads go out in sub-steps 2 and 3.  The weights of
+// sub-step j are reloaded two steps ahead during the sub-step after it.
+#include <type_traits>
+
+#include "qg_device.h"
+#include "qg_kernels.h"
 
 namespace qg {
 
+namespace {
+
+constexpr int kI8Stages = 4;
+constexpr int kI8Cols = 256;
+
+template <int OF, int BM, bool MOE, bool SPLIT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 1 : 2, BM == 256 ? 1 : 2)))
+void int8_gemm_kernel(MfmaArgs a) {
+  constexpr int MT = BM / 32;                 // 32-row MFMA tiles per wave
+  constexpr int NT = 2;                       // 32-column MFMA tiles per wave
+  constexpr int WCOL = 32 * NT;
+  constexpr int ROWB = 128;                   // bytes of a row per step
+  constexpr int STAGE = BM * ROWB;
+  constexpr int APT = STAGE / 16 / 256;       // 16-byte activation pieces per thread and step
+  // one array per stage, so that the compiler sees which stage a read and a load touch
+  __shared__ __attribute__((aligned(16))) uint8_t sA0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t sA1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t sA2[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t sA3[STAGE];
+  __shared__ int sRowOut[MOE ? BM : 1];       // output row of each tile row (-1: none)
+  __shared__ __attribute__((aligned(16))) float sRowScale[SPLIT ? 4 : BM];
+  __shared__ __attribute__((aligned(16))) float sColScale[SPLIT ? 4 : kI8Cols];
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, g = lane >> 5;
+
+  int expert = 0, ntile;
+  int64_t rowbase;
+  if constexpr (MOE) {
+    ntile = blockIdx.x;
+    rowbase = (int64_t)blockIdx.y * BM;
+    if (rowbase >= (int64_t)(*a.num_post_pad)) return;
+    expert = a.expert_ids[blockIdx.y];
+  } else {
+    int mtile;
+    const int mtiles = (int)((a.m + BM - 1) / BM);
+    xcd_tile(blockIdx.x, mtiles, (int)gridDim.x / mtiles, (int64_t)BM * a.k, (int64_t)kI8Cols * a.k, mtile, ntile);
+    rowbase = (int64_t)mtile * BM;
+  }
+  // input row of a tile row, -1: none
+  auto token_of = [&](int row) __attribute__((always_inline)) -> int {
+    if constexpr (MOE) {
+      const int f = a.sorted_ids[rowbase + row];
+      return f < a.sentinel ? f / a.topk : -1;
+    } else {
+      return rowbase + row < a.m ? (int)rowbase + row : -1;
+    }
+  };
+
+  const int col0 = ntile * kI8Cols + WCOL * wave;                  // first column of this wave
+  const int nsteps = SPLIT ? a.k / ROWB / a.ksplit : a.k / ROWB;
+  const int kstep0 = SPLIT ? (int)blockIdx.z * nsteps : 0;
+  const __amdgpu_buffer_rsrc_t wr =
+      make_rsrc(a.w + (int64_t)expert * a.w_expert_bytes, (uint32_t)a.w_expert_bytes);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)(a.x_rows * a.k));
+
+  // activation piece p of a step: row p / 8, physical 16-byte chunk p % 8; the load of thread tid's
+  // i-th piece lands in slot p = tid + 256 i.  Rows without a token read out of range: zeros.
+  int a_off[APT];
+#pragma unroll
+  for (int i = 0; i < APT; ++i) {
+    const int p = tid + 256 * i, row = p >> 3;
+    const int lc = (p & 7) ^ ((row >> 1) & 7);                     // logical chunk
+    const int tok = token_of(row);
+    a_off[i] = tok < 0 ? -1 : (int)((int64_t)tok * a.k) + kstep0 * ROWB + 16 * lc;
+  }
+  // the scales of the tile's rows and columns, for the epilogue; they land before the first stage
+  if constexpr (!SPLIT) {
+    if (tid < BM) {
+      const int tok = token_of(tid);
+      bload4_lds(make_rsrc(a.x_scale, (uint32_t)(a.x_rows * 4)), sRowScale + (tid & ~63), tok < 0 ? kOOB : 4 * tok);
+    }
+    const int col = ntile * kI8Cols + tid;
+    bload4_lds(make_rsrc((const float*)a.s + (int64_t)expert * a.n, (uint32_t)a.n * 4), sColScale + (tid & ~63),
+               col < a.n ? 4 * col : kOOB);
+  }
+  if constexpr (MOE) {
+    for (int i = tid; i < BM; i += 256) {
+      const int f = a.sorted_ids[rowbase + i];
+      sRowOut[i] = f < a.sentinel ? f : -1;
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  const int wave_slot = wave * 1024;
+  // (steps past the end store zeros, which their MFMAs then add)
+  auto issue_a = [&](int step, uint8_t* stage, int i) __attribute__((always_inline)) {
+    bload16_lds(xr, stage + 4096 * i + wave_slot, a_off[i] < 0 || step >= nsteps ? kOOB : a_off[i] + step * ROWB);
+  };
+  // weight unit j of a step: k = 32 j + 16 g .. of the step, this lane's column of tile t
+  int b_off[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int col = col0 + 32 * t + r;
+    b_off[t] = col < a.n ? (int)(((int64_t)(col >> 4) * (a.k >> 4) + kstep0 * 8 + g) * 256 + (col & 15) * 16) : kOOB;
+  }
+  i32x4 B[2][4][NT];                                               // slot = step % 2
+  auto load_b = [&](int step, int slot, int j) __attribute__((always_inline)) {
+    // (past the end: the last step's weights again, times zeros)
+    const int so = min(step, nsteps - 1) * 2048;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      B[slot][j][t] = __builtin_bit_cast(i32x4, bload16_s(wr, b_off[t], so + 512 * j));
+  };
+
+  i32x16 acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[mt][t][i] = 0;
+
+  auto stg = [&](int i) __attribute__((always_inline)) -> uint8_t* {
+    return i == 0 ? sA0 : i == 1 ? sA1 : i == 2 ? sA2 : sA3;
+  };
+  i32x4 A[MT];
+  auto read_a = [&](const uint8_t* st, int j, int mt) __attribute__((always_inline)) {
+    const int row = 32 * mt + r;
+    A[mt] = *(const i32x4*)(st + row * ROWB + 16 * ((2 * j + g) ^ ((row >> 1) & 7)));
+  };
+
+  // Loads in issue order: A(0) B(0) A(1) B(1).0-2 A(2), then per step s: B(s+1).3 in sub-step 0,
+  // B(s+2).0 in 1, B(s+2).1 and half of A(s+3) in 2, B(s+2).2 and the rest in 3.
+  auto all_a = [&](int step, uint8_t* st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < APT; ++i) issue_a(step, st, i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  all_a(0, sA0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) load_b(0, 0, j);
+  __builtin_amdgcn_sched_barrier(0);
+  all_a(1, sA1);
+#pragma unroll
+  for (int j = 0; j < 3; ++j) load_b(1, 1, j);
+  __builtin_amdgcn_sched_barrier(0);
+  all_a(2, sA2);
+  // loads issued after the last piece of a stage up to the wait for it: for stage 0 B(0), A(1),
+  // B(1).0-2 and A(2); for stage s + 1 in the middle of step s at least one step's loads and B's of
+  // two more sub-steps (stage 1: B(1).0-2, A(2) and B's of two sub-steps)
+  constexpr int VM0 = 7 * NT + 2 * APT;
+  constexpr int VM1 = 5 * NT + APT;
+  wait_loads<VM0>();
+  group_barrier();
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) read_a(sA0, 0, mt);
+  __builtin_amdgcn_sched_barrier(0);
+
+  auto step_body = [&](const int step, auto S_) __attribute__((always_inline)) {
+    constexpr int S = decltype(S_)::value;                         // step % 4
+    uint8_t* const st0 = stg(S);
+    uint8_t* const st1 = stg((S + 1) & 3);
+    uint8_t* const st3 = stg((S + 3) & 3);
+    constexpr int SB = S & 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j == 2) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<VM1>();
+        group_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[mt][t] = mfma32x32x32_i8(B[SB][j][t], A[mt], acc[mt][t]);
+        // (after the sub-step's first tile: the registers of the unit before are free)
+        if (mt == 0) {
+          if (j == 0) load_b(step + 1, SB ^ 1, 3);
+          else load_b(step + 2, SB, j - 1);
+        }
+        if (j >= 2) {
+          constexpr int HALF = APT / 2;
+#pragma unroll
+          for (int i = 0; i < HALF; ++i)
+            if (i * MT / HALF == mt) issue_a(step + 3, st3, (j - 2) * HALF + i);
+        }
+        if (j < 3) read_a(st0, j + 1, mt);
+        else read_a(st1, 0, mt);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  // the step count is padded to whole rounds of the ring
+  for (int step = 0; step < nsteps; step += kI8Stages) {
+    step_body(step, std::integral_constant<int, 0>{});
+    step_body(step + 1, std::integral_constant<int, 1>{});
+    step_body(step + 2, std::integral_constant<int, 2>{});
+    step_body(step + 3, std::integral_constant<int, 3>{});
+  }
+  // the out-of-range loads of the last steps still write zeros into LDS
+  wait_loads<0>();
+  __syncthreads();
+
+  // ---- epilogue: 32 rows of the wave's columns at a time through a stage of its own, then 16-byte
+  // pieces of rows, GR row tiles together so that their LDS round trips overlap
+  if (col0 >= a.n) return;                                         // n % 64 == 0: all or none of a wave's columns
+  uint8_t* const ep = stg(wave);
+  auto out_row = [&](int row) __attribute__((always_inline)) -> int64_t {
+    if constexpr (MOE) return sRowOut[row];
+    else return rowbase + row < a.m ? rowbase + row : -1;
+  };
+  if constexpr (SPLIT) {
+    // rows of 256 bytes, 16-byte pieces XOR-swizzled by the row
+    static_assert(32 * 256 <= STAGE, "a row tile fits a stage");
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(i32x4*)(ep + 256 * r + 16 * ((8 * t + 2 * q + g) ^ (r & 15))) =
+              i32x4{acc[mt][t][4 * q], acc[mt][t][4 * q + 1], acc[mt][t][4 * q + 2], acc[mt][t][4 * q + 3]};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int rl = 4 * q + (lane >> 4), c16 = lane & 15;
+        const int64_t orow = out_row(32 * mt + rl);
+        const u32x4 val = *(const u32x4*)(ep + 256 * rl + 16 * (c16 ^ (rl & 15)));
+        if (orow >= 0) *(u32x4*)(a.part + ((int64_t)blockIdx.z * a.m + orow) * a.n + col0 + 4 * c16) = val;
+      }
+    }
+  } else {
+    constexpr int PITCH = WCOL * 2 + 16;
+    constexpr int GR = BM == 64 ? 1 : 2;
+    static_assert(GR * 32 * PITCH <= STAGE, "the row tiles fit a stage");
+    f32x4 sw[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sw[t][q] = *(const f32x4*)&sColScale[WCOL * wave + 32 * t + 8 * q + 4 * g];
+#pragma unroll
+    for (int m0 = 0; m0 < MT; m0 += GR) {
+#pragma unroll
+      for (int mm = 0; mm < GR; ++mm) {
+        const int mt = m0 + mm;
+        const float sx = sRowScale[32 * mt + r];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            u32x2 o;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              o[h] = scaled_out2<OF>(acc[mt][t][4 * q + 2 * h], acc[mt][t][4 * q + 2 * h + 1], sw[t][q][2 * h],
+                                     sw[t][q][2 * h + 1], sx);
+            *(u32x2*)(ep + (32 * mm + r) * PITCH + (32 * t + 8 * q + 4 * g) * 2) = o;
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < 4 * GR; ++q) {
+        const int rl = 8 * q + (lane >> 3), c16 = lane & 7;
+        const int64_t orow = out_row(32 * m0 + rl);
+        const u32x4 val = *(const u32x4*)(ep + rl * PITCH + 16 * c16);
+        if (orow >= 0) *(u32x4*)((uint16_t*)a.y + orow * a.n + col0 + 8 * c16) = val;
+      }
+    }
+  }
+}
+
+template <int OF, int BM, bool MOE, bool SPLIT>
+void launch_one(const MfmaArgs& a, const MfmaTile& t, hipStream_t st) {
+  hipLaunchKernelGGL((int8_gemm_kernel<OF, BM, MOE, SPLIT>), dim3(t.grid_x, t.grid_y, SPLIT ? t.ksplit : 1), dim3(256), 0, st,
+                     a);
+}
+
+template <int OF>
+bool launch_int8(const MfmaArgs& a, const MfmaTile& t, bool moe, hipStream_t st) {
+  if (moe) {
+    if (t.bm == 128) { launch_one<OF, 128, true, false>(a, t, st); return true; }
+    if (t.bm == 256) { launch_one<OF, 256, true, false>(a, t, st); return true; }
+    return false;
+  }
+  if (t.ksplit > 1) {
+    if (t.bm == 64) { launch_one<OF, 64, false, true>(a, t, st); return true; }
+    if (t.bm == 128) { launch_one<OF, 128, false, true>(a, t, st); return true; }
+    return false;
+  }
+  if (t.bm == 128) { launch_one<OF, 128, false, false>(a, t, st); return true; }
+  if (t.bm == 256) { launch_one<OF, 256, false, false>(a, t, st); return true; }
+  return false;
+}
+
+}  // namespace
+
 bool mfma_int8(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int of, int stype, bool zero, bool moe,
                hipStream_t st) {
-  if (wp == WP_INT8 && af == A_INT8 && of == O_BF16 && stype == S_F32 && zero == false)
-    return launch_mfma_variant<WP_INT8, A_INT8, O_BF16, S_F32, false>(a, t, moe, st);
-  if (wp == WP_INT8 && af == A_INT8 && of == O_F16 && stype == S_F32 && zero == false)
-    return launch_mfma_variant<WP_INT8, A_INT8, O_F16, S_F32, false>(a, t, moe, st);
+  if (wp != WP_INT8 || af != A_INT8 || stype != S_F32 || zero) return false;
+  if (of == O_BF16) return launch_int8<O_BF16>(a, t, moe, st);
+  if (of == O_F16) return launch_int8<O_F16>(a, t, moe, st);
   return false;
 }
 

@@ -12,8 +12,6 @@
 //   * e2m1: hardware e2m1 -> bf16/f16 conversion with the UE8M0 scale folded in;
 //   * e4m3 x e4m3: fp8 MFMA (32x32x64) with the per-token / per-channel scales applied
 //     in the epilogue;
-//   * int8 x int8: i8 MFMA (32x32x32) into 32-bit integers, exact, the same scales in the
-//     epilogue;
 //   * e4m3 x e4m3 with 128 x 128 weight-block and per-(row, 128-K) activation scales: each
 //     128-wide step's product from zero, promoted by (row scale x block scale); the weights
 //     are the MFMAs' first operand, so a lane's products share one activation row and one
@@ -37,8 +35,6 @@
 // through sorted_ids and scattered on store.
 #pragma once
 
-#include <type_traits>
-
 #include "qg_device.h"
 #include "qg_kernels.h"
 
@@ -48,12 +44,10 @@ template <int WP, int AF, int OF, int ST, bool ZERO, int BM, bool MOE, bool SPLI
 __global__ __launch_bounds__(64 * CW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mfma_gemm_kernel(MfmaArgs a) {
   constexpr bool F4A = (AF == A_FP4);                // e2m1 activations: fp4 x fp4 MFMAs
-  constexpr bool I8 = (AF == A_INT8);                // int8 x int8 on the i8 MFMAs, 32-bit integer sums
-  constexpr bool F8 = (AF == A_FP8) || F4A || I8;    // byte operands to scaled / fp8 / i8 MFMAs as stored
+  constexpr bool F8 = (AF == A_FP8) || F4A;          // byte operands to scaled / fp8 MFMAs as stored
   constexpr bool FP4B = (AF == A_FP8) && WP == WP_FP4;   // e4m3 activations with e2m1 weights
   constexpr bool I4F8 = (AF == A_FP8) && WP == WP_INT4Q_FP8;   // int4 weights converted to e4m3 here
   constexpr bool BLK = (AF == A_FP8) && WP == WP_FP8_BLOCK;     // e4m3 x e4m3 with 128 x 128 block scales
-  constexpr bool W8 = WP == WP_FP8 || WP == WP_INT8 || BLK;   // one byte per weight
   constexpr int AB = F8 ? 1 : 2;
   constexpr int BK = F4A ? 256 : F8 ? 128 : 64;   // K per step; one LDS row segment = 128 bytes
   constexpr int NTHR = 64 * CW;              // CW waves, each owning BN / CW columns and all BM rows
@@ -123,7 +117,7 @@ void mfma_gemm_kernel(MfmaArgs a) {
     const int mtiles = (int)((a.m + BM - 1) / BM);
     const int ntiles = (int)gridDim.x / mtiles;
     const int id = blockIdx.x;
-    const int64_t rowb = F4A ? a.k / 2 : (int64_t)a.k * AB, colb = W8 ? a.k : a.k / 2;   // bytes per row / column
+    const int64_t rowb = F4A ? a.k / 2 : (int64_t)a.k * AB, colb = (WP == WP_FP8 || BLK) ? a.k : a.k / 2;   // bytes per row / column
     int xr = 0;
     int64_t best = 0;
     for (int cand = 1; cand <= 8; cand <<= 1) {
@@ -166,7 +160,7 @@ void mfma_gemm_kernel(MfmaArgs a) {
   // sums (the host makes the slices whole scale groups); otherwise all of K.
   const int nsteps = SPLIT ? a.k / BK / a.ksplit : a.k / BK;
   const int kstep0 = SPLIT ? (int)blockIdx.z * nsteps : 0;
-  const int64_t kun = W8 ? (a.k >> 4) : (a.k >> 5);   // 16-byte units along K per column
+  const int64_t kun = (WP == WP_FP8 || BLK) ? (a.k >> 4) : (a.k >> 5);   // 16-byte units along K per column
   const int ngroups = a.group == 0 ? 1 : a.k / a.group;
   const uint8_t* wbase = a.w + (int64_t)expert * a.w_expert_bytes;
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(wbase, (uint32_t)a.w_expert_bytes);
@@ -385,15 +379,14 @@ void mfma_gemm_kernel(MfmaArgs a) {
     }
   };
 
-  using Sum = std::conditional_t<I8, int, float>;
-  using Acc = std::conditional_t<I8, i32x16, f32x16>;
+  using Acc = f32x16;
   Acc acc[MT][NT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[mt][t][i] = 0;
+      for (int i = 0; i < 16; ++i) acc[mt][t][i] = 0.f;
 
   // ---- prologue: A(0), A(1) -> LDS stages 0, 1; weights and scales -------------------
   // Weights and scales live in a ring of NS register sets, slot = step % NS (a
@@ -836,16 +829,10 @@ void mfma_gemm_kernel(MfmaArgs a) {
           }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          if constexpr (FP4B) {
+          if constexpr (FP4B)
             acc[mt][t] = mfma32x32x64_fp8_fp4_byte(j, Af8[q % 3], B[t], (int)__float_as_uint(scl[S][t]), acc[mt][t]);
-          } else if constexpr (I8) {
-            // the lane's 32 bytes of K as two 16-byte operands
-            const i32x8 A = Af8[q % 3];
-            acc[mt][t] = mfma32x32x32_i8(A.lo, B[t].lo, acc[mt][t]);
-            acc[mt][t] = mfma32x32x32_i8(A.hi, B[t].hi, acc[mt][t]);
-          } else {
+          else
             acc[mt][t] = mfma32x32x64_fp8(Af8[q % 3], B[t], acc[mt][t]);
-          }
           // Nothing else depends on an MFMA result, and the code generator otherwise sinks
           // whole steps of MFMAs below later barriers (no overlap, every fragment live at
           // once).  The empty asm takes the result here; with the accumulators in VGPRs
@@ -963,7 +950,7 @@ void mfma_gemm_kernel(MfmaArgs a) {
   const int64_t col0w = col0;                        // first column of this wave
   float sw[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) sw[t] = (WP == WP_FP8 || I8) && !SPLIT ? ((const float*)a.s)[(int64_t)expert * a.n + wcol[t]] : 1.f;
+  for (int t = 0; t < NT; ++t) sw[t] = WP == WP_FP8 && !SPLIT ? ((const float*)a.s)[(int64_t)expert * a.n + wcol[t]] : 1.f;
   constexpr int HALVES = 32 / CR;                    // chunks per 32-row tile
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -986,14 +973,10 @@ void mfma_gemm_kernel(MfmaArgs a) {
           }
           if ((8 * (i >> 2)) / CR != h) continue;              // rows of element i: 8(i/4) + 0..7
           const int rl = 8 * (i >> 2) + 4 * g + (i & 3) - CR * h;
+          float v = acc[mt][t][i];
           if constexpr (SPLIT) {
-            *(Sum*)(ep + rl * PITCH + (32 * t + r) * 4) = acc[mt][t][i];
-          } else if constexpr (I8) {
-            const int tok = sRowTok[rbase + rl];
-            *(uint16_t*)(ep + rl * PITCH + (32 * t + r) * 2) =
-                scaled_out<OF>(acc[mt][t][i], sw[t], tok < 0 ? 0.f : a.x_scale[tok]);
+            *(float*)(ep + rl * PITCH + (32 * t + r) * 4) = v;
           } else {
-            float v = acc[mt][t][i];
             v *= sw[t];
             if constexpr (AF == A_FP8) {   // per-token scale (e4m3 activations)
               const int tok = sRowTok[rbase + rl];
@@ -1031,7 +1014,7 @@ static void launch_mfma_one(const MfmaArgs& a, dim3 grid, hipStream_t st) {
   // (their blocks are many and short, and independent workgroups hide each other's barriers
   // better: measured 15% faster for 16-bit, 13-21% for e2m1 x e4m3, while dense 128-row
   // tiles gain ~10% from 8 waves and 4-wave e4m3-weight tiles spill).
-  constexpr int CW = (BM == 256 || !MOE || WP == WP_FP8 || WP == WP_INT8 || WP == WP_FP8_BLOCK || WP == WP_INT4Q_FP8 || AF == A_FP4) ? 8 : 4;
+  constexpr int CW = (BM == 256 || !MOE || WP == WP_FP8 || WP == WP_FP8_BLOCK || WP == WP_INT4Q_FP8 || AF == A_FP4) ? 8 : 4;
   hipLaunchKernelGGL((mfma_gemm_kernel<WP, AF, OF, ST, ZERO, BM, MOE, SPLIT, CW>), grid, dim3(64 * CW), 0, st, a);
 }
 
