@@ -205,7 +205,7 @@ qg_status launched() {
 
 // ---- M-bucket selector --------------------------------------------------------------
 // Weight-streaming family: a workgroup of 2 column blocks x 4 K parts (4-bit weights)
-// or 1 x 8 (e4m3 or int8 weights) waves; rows in blocks of 4 / 16 / 32 / 64 (mt = 0 / 1 / 2 / 4).
+// or 1 x 8 (byte weights) waves; rows in blocks of 4 / 16 / 32 / 64 (mt = 0 / 1 / 2 / 4).
 StreamTile stream_tile(int64_t rows, int64_t n, bool w8) {
   StreamTile t{};
   t.ncb = w8 ? 1 : 2;
@@ -215,6 +215,26 @@ StreamTile stream_tile(int64_t rows, int64_t n, bool w8) {
   t.grid_x = (unsigned)((n / 16 + t.ncb - 1) / t.ncb);
   t.grid_y = (unsigned)((rows + bm - 1) / bm);
   return t;
+}
+void stream_shape(StreamTile& t, int64_t n, int ncb, int kq) {
+  t.ncb = ncb;
+  t.kq = kq;
+  t.grid_x = (unsigned)((n / 16 + ncb - 1) / ncb);
+}
+
+// int8 dense streaming: 1 x 8 shapes, 2 x 4 where K is short for eight parts (a wave's part is one
+// batch of loads up to 1024) and the columns fill the GPU: one row, K = 4096, N = 14336 13.7 -> 11.2
+// us; at K = 7168 9.8 us with 1 x 8, 10.9 with 2 x 4.  K is never split over workgroups: unsplit
+// shapes or the MFMA kernel's tiles beat it throughout (16 rows, N = K = 4096 8.8 us split, 5.8).
+bool int8_wide(int64_t rows, int64_t n, int64_t k) { return n > 4096 && k <= (rows <= 4 ? 4096 : 2048); }
+// Rows the streaming kernel takes: to 4 always; to 16 and 32 while K is short or, with few columns,
+// of one batch per part (N = K = 4096, 16 / 32 rows: 5.8 / 7.0 us against 7.8 / 8.0 on the MFMA
+// kernel; N = 1024, K = 8192: 6.7 / 9.3 against 8.1 / 8.2; N = 7168, K = 2048: 6.2 / 5.7 against 7.2
+// / 6.9; N = 14336, K = 4096: 12.8 / 16.4 against 11.7).
+bool int8_streams(int64_t rows, int64_t n, int64_t k) {
+  if (rows <= 4) return true;
+  if (rows > 32) return false;
+  return n <= 4096 ? k <= (rows <= 16 ? 8192 : 4096) : k <= 2048;
 }
 
 // MFMA-bound family: rows per tile 256 while that still leaves about 1.5 workgroups per
@@ -251,8 +271,48 @@ bool rows256(int64_t rows, int64_t ntiles) {
   return 2 * 7 * r256 < 8 * r128;
 }
 
+// int8 dense tiles.  A workgroup's K step takes `lat` us while its CU is otherwise idle, and a full
+// GPU gets through 256 of them in `full` us (bound by power and by what a CU loads per clock);
+// beginning and end cost `fixed` us plus `out` us per round of workgroups (writing the outputs).
+// Fitted to 26 shapes (33..4096 rows, 192..28672 columns, K 640..8192), which it orders within 7%:
+// at N = K = 7168 the tiles that measured best are 64 x 128 with K split in two at 64 rows (14.3 us,
+// unsplit 17, 64 x 256 split in four 16.2), 64 x 128 at 256 (20.0; 128 x 128 23.0), 128 x 128 at 512
+// (29.2; 64 x 256 31.2, 128 x 256 38.7), 128 x 256 at 1024 (49.7; 128 x 128 52.4, 256 x 256 69.8),
+// 256 x 256 at 4096 (181; 128 x 256 189, 128 x 128 213).
+struct Int8Tile { int bm, cols; double lat, full, fixed, out; };
+constexpr Int8Tile kInt8Tiles[] = {
+    {256, 256, 1.30, 1.75, 4.5, 6.0}, {128, 256, 0.66, 0.93, 3.8, 3.0}, {128, 128, 0.37, 0.54, 3.2, 1.5},
+    {64, 256, 0.43, 0.55, 3.0, 1.5}, {64, 128, 0.25, 0.33, 2.8, 0.75}};
+MfmaTile int8_tile(int64_t rows, int64_t n, int64_t k) {
+  MfmaTile best{};
+  double best_us = 0;
+  for (const Int8Tile& c : kInt8Tiles) {
+    const int64_t tiles = ((rows + c.bm - 1) / c.bm) * ((n + c.cols - 1) / c.cols);
+    // K split (64-row tiles): slices of whole steps, one workgroup per CU, partials within the
+    // array of the calls that cannot allocate; the reduction's launch, its partials written and read
+    for (int sp = 1; sp <= (c.bm == 64 ? kMaxSplit : 1); sp *= 2) {
+      if (sp > 1 && (tiles * sp > kCUs || (k / 128) % sp != 0 || k / 128 / sp < 4 ||
+                     sp * rows * n * 4 > (int64_t)qg_noalloc_scratch_bytes()))
+        break;
+      const double r = (double)(tiles * sp) / kCUs;
+      double us = fmax(c.lat * ceil(r), c.full * r) * (double)(k / 128 / sp) + c.fixed + c.out * r;
+      if (sp > 1) us += 1.8 + (double)sp * (double)(rows * n) * 8 / 3.0e6;
+      if (best.bm == 0 || us < best_us) {
+        best_us = us;
+        best.bm = c.bm;
+        best.cols = c.cols;
+        best.grid_x = (unsigned)tiles;
+        best.grid_y = 1;
+        best.ksplit = sp;
+      }
+    }
+  }
+  return best;
+}
+
 // Dense tiles (MoE tiles are built by qg_moe_gemm).
 MfmaTile mfma_tile(int64_t rows, int64_t n, int64_t k, int group, const PathInfo& pi) {
+  if (pi.af == A_INT8) return int8_tile(rows, n, k);
   MfmaTile t{};
   const int64_t ntiles = (n + 255) / 256;
   t.bm = rows256(rows, ntiles) ? 256 : 128;
@@ -262,7 +322,7 @@ MfmaTile mfma_tile(int64_t rows, int64_t n, int64_t k, int group, const PathInfo
   // at 33 / 64 rows 25.1 / 27.3 -> 20.1 / 23.7 us, slower at 96 / 128 rows), and up to 128
   // rows for e4m3 and e2m1 x e4m3 weights (W4A8 MXFP4 at 96 / 128 rows 25.6 / 29.8 -> 19.8 /
   // 21.2 us, block-scaled W8A8 27.8 / 29.3 -> 25.3 / 26.4 us).
-  const int64_t rows64 = (pi.af == A_FP8 && pi.wp_mfma != WP_INT4Q_FP8) || pi.af == A_INT8 ? 128 : 64;
+  const int64_t rows64 = pi.af == A_FP8 && pi.wp_mfma != WP_INT4Q_FP8 ? 128 : 64;
   if (t.bm == 128 && rows <= rows64 && pi.af != A_FP4 && !pi.binv) {
     const int64_t tiles64 = ((rows + 63) / 64) * ntiles;
     const int sp64 = split_for(tiles64, k, group, pi);
@@ -312,6 +372,10 @@ bool is_block(const PathInfo& pi) { return pi.wp_small == WP_FP8_BLOCK; }
 // and below the streaming kernel is faster), 64 for block-scaled e4m3 (streamed 15-22 us
 // against 21-24 us at 17..64 rows).
 int64_t dense_stream_max(const PathInfo& pi) { return is_block(pi) ? 64 : 32; }
+bool dense_streams(const PathInfo& pi, int64_t m, int64_t n, int64_t k) {
+  if (pi.binv) return false;   // batch-invariant: one MMA type for every M
+  return pi.af == A_INT8 ? int8_streams(m, n, k) : m <= dense_stream_max(pi);
+}
 MfmaTile block_tile(int64_t rows, int64_t n, int64_t k, const PathInfo& pi) { return mfma_tile(rows, n, k, 128, pi); }
 
 // Workspace of a dense call: the split-K partial sums.
@@ -321,8 +385,8 @@ size_t dense_workspace(const qg_prepared* p, const PathInfo& pi, int64_t m) {
     const MfmaTile t = block_tile(m, p->desc.n, p->desc.k, pi);
     return t.ksplit > 1 ? (size_t)t.ksplit * (size_t)m * (size_t)p->desc.n * sizeof(float) : 0;
   }
-  if (m <= dense_stream_max(pi) && !pi.binv) {
-    const int sp = stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
+  if (dense_streams(pi, m, p->desc.n, p->desc.k)) {
+    const int sp = pi.af == A_INT8 ? 1 : stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
     return sp > 1 ? (size_t)sp * (size_t)m * (size_t)p->desc.n * sizeof(float) : 0;
   }
   const MfmaTile t = mfma_tile(m, p->desc.n, p->desc.k, p->desc.group_k, pi);
@@ -488,8 +552,7 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
     if (t.ksplit > 1 && !launch_split_reduce(a, false, false, pi.of, (hipStream_t)stream)) return QG_ERR_UNSUPPORTED;
     return launched();
   }
-  const bool mfma = m > dense_stream_max(pi) || pi.binv;   // batch-invariant: one MMA type for every M
-  if (mfma) {
+  if (!dense_streams(pi, m, p->desc.n, p->desc.k)) {
     const MfmaTile t = mfma_tile(m, p->desc.n, p->desc.k, p->desc.group_k, pi);
     if (t.ksplit > 1) {
       const size_t need = (size_t)t.ksplit * (size_t)m * (size_t)p->desc.n * sizeof(float);
@@ -508,13 +571,12 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
     return launched();
   }
   StreamTile t = stream_tile(m, p->desc.n, byte_weights(&p->desc));
-  const int sp = stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
+  const int sp = pi.af == A_INT8 ? 1 : stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
+  if (pi.af == A_INT8 && int8_wide(m, p->desc.n, p->desc.k)) stream_shape(t, p->desc.n, 2, 4);
   if (sp > 1) {
     const size_t need = dense_workspace(p, pi, m);
     if (!ws || !aligned16(ws) || ws_bytes < need) return QG_ERR_WORKSPACE;
-    t.ncb = 8;
-    t.kq = 1;
-    t.grid_x = (unsigned)((p->desc.n / 16 + 7) / 8);
+    stream_shape(t, p->desc.n, 8, 1);
     a.part = (float*)ws;
     a.ksplit = sp;
   }
@@ -523,9 +585,8 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
   if (!launch_stream_gemm(a, t, pi.wp_small, pi.af, pi.of, pi.st, p->desc.has_zero != 0, false, (hipStream_t)stream))
     return QG_ERR_UNSUPPORTED;
   // block-scaled partials are scaled already; the others take their scales in the reduction
-  if (sp > 1 && !launch_split_reduce(a, pi.wp_small == WP_FP8 || pi.wp_small == WP_INT8,
-                                     (pi.af == A_FP8 && !is_block(pi)) || pi.af == A_INT8, pi.of, (hipStream_t)stream,
-                                     pi.wp_small == WP_INT8))
+  if (sp > 1 && !launch_split_reduce(a, pi.wp_small == WP_FP8, pi.af == A_FP8 && !is_block(pi), pi.of,
+                                     (hipStream_t)stream))
     return QG_ERR_UNSUPPORTED;
   return launched();
 }
@@ -554,6 +615,18 @@ int32_t qg_moe_block_m(const qg_prepared* p, int64_t tokens, int32_t topk) {
   }
   if (pi.binv) return mean < 512 ? 128 : 256;   // MFMA blocks at every size
   if (busy <= 4) return 4;
+  if (pi.af == A_INT8) {
+    // int8: 16-row streaming blocks to a mean of 9 rows, 32 to 16, then 128-row MFMA blocks (E = 64
+    // top-6, N = 2816, K = 4096, us with 16 / 32 / 128 rows: a mean of 6 114 / 123 / -, 12 129 / 119 / -,
+    // 24 - / 124 / 129, 37 - / 213 / 134; E = 64 top-4, N = 4096, K = 1408: 8 62 / 67 / -, 16 - / 75 / 64).
+    // 128-row blocks, two workgroups per CU, beat 256-row blocks (a mean of 375 / 768 325 / 600 against
+    // 366 / 620 us, K = 1408, a mean of 512 262 against 310) but where one 256-row block holds what takes two
+    // of 128, the second nearly empty, K is long and there are tiles enough (a mean of 150: 222 -> 192 us).
+    if (mean <= 9) return 16;
+    if (mean <= 16) return 32;
+    const int64_t tiles = (int64_t)p->desc.num_experts * ((p->desc.n + 255) / 256);
+    return mean > 128 && mean <= 224 && p->desc.k >= 4096 && tiles >= 2 * kCUs ? 256 : 128;
+  }
   if (is_block(pi) && busy <= 64) return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
   if (mean <= 16) return 16;
   if (mean <= 24 && pi.af != A_FP8 && pi.af != A_INT8) return 32;
@@ -663,19 +736,19 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
   if (block_m > kStreamMaxRows) {
     MfmaTile t{};
     t.bm = block_m;
-    t.grid_x = (unsigned)((p->desc.n + 255) / 256);
+    t.cols = 256;
+    t.once = 4 * tokens * topk <= 3 * (int64_t)p->desc.num_experts * block_m;
+    t.grid_x = (unsigned)((p->desc.n + t.cols - 1) / t.cols);
     t.grid_y = (unsigned)cb;
+    if (pi.af == A_INT8 && (int64_t)t.grid_x * cb >= ((int64_t)1 << 24) - 8) return QG_ERR_UNSUPPORTED;   // one grid axis
     QG_LOG("moe_gemm T=%lld topk=%d bm=%d -> mfma grid=%ux%u", (long long)tokens, topk, block_m, t.grid_x, t.grid_y);
     if (!launch_mfma_gemm(a, t, pi.wp_mfma, pi.af, pi.of, pi.st, p->desc.has_zero != 0, true, (hipStream_t)stream))
       return QG_ERR_UNSUPPORTED;
     return launched();
   }
   StreamTile t = stream_tile(block_m, p->desc.n, byte_weights(&p->desc));
-  if (!byte_weights(&p->desc)) {   // 128 columns per workgroup (see launch_mt)
-    t.ncb = 8;
-    t.kq = 1;
-    t.grid_x = (unsigned)((p->desc.n / 16 + 7) / 8);
-  }
+  if (!byte_weights(&p->desc)) stream_shape(t, p->desc.n, 8, 1);   // 128 columns per workgroup (see launch_mt)
+  if (pi.af == A_INT8) stream_shape(t, p->desc.n, 4, 2);           // 64
   t.grid_y = (unsigned)cb;
   QG_LOG("moe_gemm T=%lld topk=%d bm=%d -> stream mt=%d grid=%ux%u", (long long)tokens, topk, block_m, t.mt,
          t.grid_x, t.grid_y);

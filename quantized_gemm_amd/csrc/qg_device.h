@@ -322,8 +322,9 @@ __device__ __forceinline__ u32x4 bload16_stream(__amdgpu_buffer_rsrc_t r, int of
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2);   // nt: streamed once
 }
 // The same with a wave-uniform part of the offset (in range together with the lane's).
+template <bool NTL>   // non-temporal: streamed once
 __device__ __forceinline__ u32x4 bload16_s(__amdgpu_buffer_rsrc_t r, int off, int soff) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0);
+  return __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, NTL ? 2 : 0);
 }
 // Waits until at most N of this wave's vector-memory loads are in flight.
 template <int N>

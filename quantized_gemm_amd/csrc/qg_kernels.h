@@ -38,7 +38,9 @@ typedef StreamArgs MfmaArgs;
 struct MfmaTile {
   int bm;                    // rows per workgroup tile (128 or 256); 256 columns per tile
   unsigned grid_x, grid_y;   // dense: grid_x = all tiles; MoE: grid_x = column tiles, grid_y = blocks
-  int ksplit;                // dense, 128-row tiles: K slices (grid z), 1 = none
+  int ksplit;                // dense: K slices (grid z), 1 = none
+  int cols;                  // int8 products: columns per workgroup (128 or 256; the others 256)
+  bool once;                 // int8 MoE: most weights are read by one row block
 };
 bool launch_mfma_gemm(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int of, int stype, bool zero, bool moe,
                       hipStream_t st);

@@ -26,6 +26,14 @@
 // step + 1 and passes the barrier; past it that stage is visible to all, and the stage that
 // step - 1 read is free for step + 3, whose loads go out in sub-steps 2 and 3.  The weights of
 // sub-step j are reloaded two steps ahead during the sub-step after it.
+//
+// MoE: workgroups go to the 8 XCDs round-robin, each with its own L2, so each XCD takes an eighth of
+// the tiles in order, groups of 8 row blocks with the block walked fastest: the tiles that run
+// together share activation rows and, where an expert has several blocks, its weights (E = 64
+// top-6, N = 2816, K = 4096: 4000 tokens 468 -> 325 us, 400 tokens 158 -> 140 us; E = 32 top-4,
+// N = 7168, K = 2048, 8192 tokens in groups of 1 / 2 / 8: 620 / 545 / 540 us).  Where most experts have one
+// block, whose weights are then read once, they are loaded past the caches (NTW: 400 tokens 140 ->
+// 134 us; with two blocks per expert 108 -> 119 us).
 #include <type_traits>
 
 #include "qg_device.h"
@@ -36,14 +44,17 @@ namespace qg {
 namespace {
 
 constexpr int kI8Stages = 4;
-constexpr int kI8Cols = 256;
 
-template <int OF, int BM, bool MOE, bool SPLIT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 1 : 2, BM == 256 ? 1 : 2)))
+// waves per SIMD: what the accumulators and LDS stages of a tile leave room for
+constexpr int waves_of(int bm, int nt) { return bm == 256 ? 1 : bm == 64 && nt == 1 ? 4 : 2; }
+
+// NT: 32-column MFMA tiles per wave; NTW: non-temporal weight loads
+template <int OF, int BM, int NT, bool MOE, bool SPLIT, bool NTW>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(waves_of(BM, NT), waves_of(BM, NT))))
 void int8_gemm_kernel(MfmaArgs a) {
   constexpr int MT = BM / 32;                 // 32-row MFMA tiles per wave
-  constexpr int NT = 2;                       // 32-column MFMA tiles per wave
   constexpr int WCOL = 32 * NT;
+  constexpr int COLS = 4 * WCOL;              // columns per workgroup
   constexpr int ROWB = 128;                   // bytes of a row per step
   constexpr int STAGE = BM * ROWB;
   constexpr int APT = STAGE / 16 / 256;       // 16-byte activation pieces per thread and step
@@ -54,7 +65,7 @@ void int8_gemm_kernel(MfmaArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t sA3[STAGE];
   __shared__ int sRowOut[MOE ? BM : 1];       // output row of each tile row (-1: none)
   __shared__ __attribute__((aligned(16))) float sRowScale[SPLIT ? 4 : BM];
-  __shared__ __attribute__((aligned(16))) float sColScale[SPLIT ? 4 : kI8Cols];
+  __shared__ __attribute__((aligned(16))) float sColScale[SPLIT ? 4 : COLS];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -64,14 +75,21 @@ void int8_gemm_kernel(MfmaArgs a) {
   int expert = 0, ntile;
   int64_t rowbase;
   if constexpr (MOE) {
-    ntile = blockIdx.x;
-    rowbase = (int64_t)blockIdx.y * BM;
-    if (rowbase >= (int64_t)(*a.num_post_pad)) return;
-    expert = a.expert_ids[blockIdx.y];
+    const int ntiles = (a.n + COLS - 1) / COLS;
+    const int total = *a.num_post_pad / BM * ntiles;
+    const int chunk = (total + 7) >> 3, l = (int)blockIdx.x >> 3;
+    const int tile = ((int)blockIdx.x & 7) * chunk + l;
+    if (l >= chunk || tile >= total) return;
+    const int group = tile / (8 * ntiles), gl = tile - group * (8 * ntiles);
+    const int gb = min(8, total / ntiles - 8 * group);             // row blocks of the group
+    ntile = gl / gb;
+    const int block = 8 * group + gl - ntile * gb;
+    rowbase = (int64_t)block * BM;
+    expert = a.expert_ids[block];
   } else {
     int mtile;
     const int mtiles = (int)((a.m + BM - 1) / BM);
-    xcd_tile(blockIdx.x, mtiles, (int)gridDim.x / mtiles, (int64_t)BM * a.k, (int64_t)kI8Cols * a.k, mtile, ntile);
+    xcd_tile(blockIdx.x, mtiles, (int)gridDim.x / mtiles, (int64_t)BM * a.k, (int64_t)COLS * a.k, mtile, ntile);
     rowbase = (int64_t)mtile * BM;
   }
   // input row of a tile row, -1: none
@@ -84,7 +102,7 @@ void int8_gemm_kernel(MfmaArgs a) {
     }
   };
 
-  const int col0 = ntile * kI8Cols + WCOL * wave;                  // first column of this wave
+  const int col0 = ntile * COLS + WCOL * wave;                  // first column of this wave
   const int nsteps = SPLIT ? a.k / ROWB / a.ksplit : a.k / ROWB;
   const int kstep0 = SPLIT ? (int)blockIdx.z * nsteps : 0;
   const __amdgpu_buffer_rsrc_t wr =
@@ -107,9 +125,10 @@ void int8_gemm_kernel(MfmaArgs a) {
       const int tok = token_of(tid);
       bload4_lds(make_rsrc(a.x_scale, (uint32_t)(a.x_rows * 4)), sRowScale + (tid & ~63), tok < 0 ? kOOB : 4 * tok);
     }
-    const int col = ntile * kI8Cols + tid;
-    bload4_lds(make_rsrc((const float*)a.s + (int64_t)expert * a.n, (uint32_t)a.n * 4), sColScale + (tid & ~63),
-               col < a.n ? 4 * col : kOOB);
+    const int col = ntile * COLS + tid;
+    if (tid < COLS)
+      bload4_lds(make_rsrc((const float*)a.s + (int64_t)expert * a.n, (uint32_t)a.n * 4), sColScale + (tid & ~63),
+                 col < a.n ? 4 * col : kOOB);
   }
   if constexpr (MOE) {
     for (int i = tid; i < BM; i += 256) {
@@ -119,7 +138,7 @@ void int8_gemm_kernel(MfmaArgs a) {
   }
   __builtin_amdgcn_sched_barrier(0);
   const int wave_slot = wave * 1024;
-  // (steps past the end store zeros, which their MFMAs then add)
+  // (loads of steps past the end store zeros that nothing reads)
   auto issue_a = [&](int step, uint8_t* stage, int i) __attribute__((always_inline)) {
     bload16_lds(xr, stage + 4096 * i + wave_slot, a_off[i] < 0 || step >= nsteps ? kOOB : a_off[i] + step * ROWB);
   };
@@ -132,11 +151,11 @@ void int8_gemm_kernel(MfmaArgs a) {
   }
   i32x4 B[2][4][NT];                                               // slot = step % 2
   auto load_b = [&](int step, int slot, int j) __attribute__((always_inline)) {
-    // (past the end: the last step's weights again, times zeros)
+    // (past the end: the last step's again, which nothing reads)
     const int so = min(step, nsteps - 1) * 2048;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-      B[slot][j][t] = __builtin_bit_cast(i32x4, bload16_s(wr, b_off[t], so + 512 * j));
+      B[slot][j][t] = __builtin_bit_cast(i32x4, bload16_s<NTW>(wr, b_off[t], so + 512 * j));
   };
 
   i32x16 acc[MT][NT];
@@ -218,13 +237,16 @@ void int8_gemm_kernel(MfmaArgs a) {
       }
     }
   };
-  // the step count is padded to whole rounds of the ring
-  for (int step = 0; step < nsteps; step += kI8Stages) {
+  int step = 0;
+  for (; step + kI8Stages <= nsteps; step += kI8Stages) {
     step_body(step, std::integral_constant<int, 0>{});
     step_body(step + 1, std::integral_constant<int, 1>{});
     step_body(step + 2, std::integral_constant<int, 2>{});
     step_body(step + 3, std::integral_constant<int, 3>{});
   }
+  if (step < nsteps) step_body(step, std::integral_constant<int, 0>{});
+  if (step + 1 < nsteps) step_body(step + 1, std::integral_constant<int, 1>{});
+  if (step + 2 < nsteps) step_body(step + 2, std::integral_constant<int, 2>{});
   // the out-of-range loads of the last steps still write zeros into LDS
   wait_loads<0>();
   __syncthreads();
@@ -238,26 +260,28 @@ void int8_gemm_kernel(MfmaArgs a) {
     else return rowbase + row < a.m ? rowbase + row : -1;
   };
   if constexpr (SPLIT) {
-    // rows of 256 bytes, 16-byte pieces XOR-swizzled by the row
-    static_assert(32 * 256 <= STAGE, "a row tile fits a stage");
+    // 16-byte pieces XOR-swizzled by the row
+    constexpr int PPR = WCOL / 4;                                  // pieces per row
+    static_assert(32 * PPR * 16 <= STAGE, "a row tile fits a stage");
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          *(i32x4*)(ep + 256 * r + 16 * ((8 * t + 2 * q + g) ^ (r & 15))) =
+          *(i32x4*)(ep + 16 * PPR * r + 16 * ((8 * t + 2 * q + g) ^ (r & (PPR - 1)))) =
               i32x4{acc[mt][t][4 * q], acc[mt][t][4 * q + 1], acc[mt][t][4 * q + 2], acc[mt][t][4 * q + 3]};
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int rl = 4 * q + (lane >> 4), c16 = lane & 15;
+      for (int q = 0; q < PPR / 2; ++q) {
+        const int rl = (64 / PPR) * q + lane / PPR, c16 = lane % PPR;
         const int64_t orow = out_row(32 * mt + rl);
-        const u32x4 val = *(const u32x4*)(ep + 256 * rl + 16 * (c16 ^ (rl & 15)));
+        const u32x4 val = *(const u32x4*)(ep + 16 * PPR * rl + 16 * (c16 ^ (rl & (PPR - 1))));
         if (orow >= 0) *(u32x4*)(a.part + ((int64_t)blockIdx.z * a.m + orow) * a.n + col0 + 4 * c16) = val;
       }
     }
   } else {
     constexpr int PITCH = WCOL * 2 + 16;
+    constexpr int PPR = WCOL / 8;                                  // 16-byte pieces per row
     constexpr int GR = BM == 64 ? 1 : 2;
     static_assert(GR * 32 * PITCH <= STAGE, "the row tiles fit a stage");
     f32x4 sw[NT][4];
@@ -284,8 +308,8 @@ void int8_gemm_kernel(MfmaArgs a) {
           }
       }
 #pragma unroll
-      for (int q = 0; q < 4 * GR; ++q) {
-        const int rl = 8 * q + (lane >> 3), c16 = lane & 7;
+      for (int q = 0; q < GR * PPR / 2; ++q) {
+        const int rl = (64 / PPR) * q + lane / PPR, c16 = lane % PPR;
         const int64_t orow = out_row(32 * m0 + rl);
         const u32x4 val = *(const u32x4*)(ep + rl * PITCH + 16 * c16);
         if (orow >= 0) *(u32x4*)((uint16_t*)a.y + orow * a.n + col0 + 8 * c16) = val;
@@ -294,26 +318,35 @@ void int8_gemm_kernel(MfmaArgs a) {
   }
 }
 
-template <int OF, int BM, bool MOE, bool SPLIT>
+template <int OF, int BM, int NT, bool MOE, bool SPLIT, bool NTW>
 void launch_one(const MfmaArgs& a, const MfmaTile& t, hipStream_t st) {
-  hipLaunchKernelGGL((int8_gemm_kernel<OF, BM, MOE, SPLIT>), dim3(t.grid_x, t.grid_y, SPLIT ? t.ksplit : 1), dim3(256), 0, st,
-                     a);
+  const dim3 grid = MOE ? dim3((t.grid_x * t.grid_y + 7) / 8 * 8) : dim3(t.grid_x, 1, SPLIT ? t.ksplit : 1);
+  hipLaunchKernelGGL((int8_gemm_kernel<OF, BM, NT, MOE, SPLIT, NTW>), grid, dim3(256), 0, st, a);
+}
+
+template <int OF, int BM, int NT>
+bool launch_dense(const MfmaArgs& a, const MfmaTile& t, hipStream_t st) {
+  if (t.ksplit <= 1) launch_one<OF, BM, NT, false, false, false>(a, t, st);
+  else if constexpr (BM == 64) launch_one<OF, BM, NT, false, true, false>(a, t, st);
+  else return false;
+  return true;
 }
 
 template <int OF>
 bool launch_int8(const MfmaArgs& a, const MfmaTile& t, bool moe, hipStream_t st) {
   if (moe) {
-    if (t.bm == 128) { launch_one<OF, 128, true, false>(a, t, st); return true; }
-    if (t.bm == 256) { launch_one<OF, 256, true, false>(a, t, st); return true; }
-    return false;
+    if (t.cols != 256 || (t.bm != 128 && t.bm != 256)) return false;
+    if (t.bm == 128 && t.once) launch_one<OF, 128, 2, true, false, true>(a, t, st);
+    else if (t.bm == 128) launch_one<OF, 128, 2, true, false, false>(a, t, st);
+    else if (t.once) launch_one<OF, 256, 2, true, false, true>(a, t, st);
+    else launch_one<OF, 256, 2, true, false, false>(a, t, st);
+    return true;
   }
-  if (t.ksplit > 1) {
-    if (t.bm == 64) { launch_one<OF, 64, false, true>(a, t, st); return true; }
-    if (t.bm == 128) { launch_one<OF, 128, false, true>(a, t, st); return true; }
-    return false;
-  }
-  if (t.bm == 128) { launch_one<OF, 128, false, false>(a, t, st); return true; }
-  if (t.bm == 256) { launch_one<OF, 256, false, false>(a, t, st); return true; }
+  if (t.cols == 256 && t.bm == 256) return launch_dense<OF, 256, 2>(a, t, st);
+  if (t.cols == 256 && t.bm == 128) return launch_dense<OF, 128, 2>(a, t, st);
+  if (t.cols == 256 && t.bm == 64) return launch_dense<OF, 64, 2>(a, t, st);
+  if (t.cols == 128 && t.bm == 128) return launch_dense<OF, 128, 1>(a, t, st);
+  if (t.cols == 128 && t.bm == 64) return launch_dense<OF, 64, 1>(a, t, st);
   return false;
 }
 
