@@ -128,14 +128,23 @@ def version() -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_torch_c = None
 
 
 def _stream(stream):
-    if stream is None:
+    """The hipStream_t of a torch stream or of an address; None: torch's current stream of the current device."""
+    global _torch_c
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if _torch_c is None:
         import torch
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        torch.cuda.current_stream()      # initialises torch's side once; the raw lookups below need it
+        _torch_c = torch._C
+    # the address alone: a torch.cuda.Stream object costs more than the launch of a small kernel
+    return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
 
 
 def _check(status: int, where: str):
