@@ -50,9 +50,12 @@ def _logits(values, dtype, pad=0):
 
 
 def _check(values, dtype, scoring, topk, bias=None, groups=1, topk_groups=1, group_top=1, renorm=False, scale=1.0, pad=0,
-           stream=None):
-    t, e = np.asarray(values).shape
-    dev, held = _logits(values, dtype, pad)
+           stream=None, total=None):
+    # total: so many tokens, whose rows repeat the given ones
+    n, e = np.asarray(values).shape
+    t = n if total is None else total
+    dev, held = _logits(np.resize(np.asarray(values, np.float32), (t, e)), dtype, pad)
+    held = held[:n]
     desc = qg.make_route_desc(qg.R_SOFTMAX if scoring == "softmax" else qg.R_SIGMOID, e, topk, groups, topk_groups,
                               group_top, renorm, scale)
     ids = torch.full((t + 1, topk), 77, dtype=torch.int32, device="cuda")
@@ -64,6 +67,7 @@ def _check(values, dtype, scoring, topk, bias=None, groups=1, topk_groups=1, gro
     assert (ids[t] == 77).all() and (w[t] == 77).all()           # nothing behind the last token
     rid, rw = RT.route(held, scoring, topk, bias=None if bias is None else np.asarray(bias, np.float32), groups=groups,
                        topk_groups=topk_groups, group_top=group_top, renorm=renorm, scale=scale)
+    rid, rw = np.resize(rid, (t, topk)), np.resize(rw, (t, topk))
     got_id, got_w = ids[:t].cpu().numpy(), w[:t].cpu().numpy()
     assert np.array_equal(got_id, rid), f"{np.count_nonzero((got_id != rid).any(1))} tokens differ: {got_id[(got_id != rid).any(1)][:2]} {rid[(got_id != rid).any(1)][:2]}"
     assert np.all(np.abs(got_w - rw) <= 2.0 ** -24 * (1 + 2.0 ** -16) * np.abs(rw) + 2.0 ** -149)
@@ -155,6 +159,53 @@ def test_large_batches(t):
     _check(v, "f32", "sigmoid", 8, bias=rng.standard_normal(256) * 0.05, groups=8, topk_groups=4, group_top=2, renorm=True,
            scale=2.5)
     _check(v[:, :128], "bf16", "softmax", 8, renorm=True)
+
+
+def _odd_rows(e, dtype, seed):
+    """Rows that masks, ties and extremes make awkward, among ordinary ones."""
+    rng = np.random.default_rng(seed)
+    v = (rng.standard_normal((550, e)) * 1.5).astype(np.float32)
+    v[3::50] = rng.integers(0, 3, size=v[3::50].shape)                 # ties, among groups too
+    v[4::50] = np.where(rng.random(v[4::50].shape) < 0.5, 0.0, -0.0)   # zeros of both signs are equal
+    v[5::50] = -np.inf
+    v[6::50] = np.nan
+    v[7::50, : e - 2] = -np.inf                                        # two experts left
+    v[8::50, ::2] = np.finfo(np.float32).min if dtype != "f16" else -65504
+    v[9::50, ::3] = np.nan
+    v[10::50, 1::4] = np.inf
+    v[11::50] = np.linspace(-8, 8, e)[rng.permutation(e)]
+    v[12::50] = 1 + rng.permutation(e) * np.float32(2.0 ** -23)        # scores closer than float32 resolves
+    return v
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,topk", [(8, 2), (60, 4), (64, 6), (65, 16), (128, 8), (200, 8), (256, 8), (320, 8), (33, 17)])
+def test_odd_rows_of_large_batches(e, topk, scoring, dtype):
+    v = _odd_rows(e, dtype, e)
+    bias = np.random.default_rng(e).standard_normal(e) * 0.05
+    for t in (550, 4101):                       # a wave per token, and four tokens per wave
+        _check(v, dtype, scoring, topk, renorm=True, pad=3, total=t)
+        _check(v, dtype, scoring, topk, total=t)
+        _check(v, dtype, scoring, topk, bias=bias, scale=2.5, total=t)
+        odd = bias.copy()
+        odd[[0, e - 1]] = [-np.inf, np.inf]
+        odd[1] = np.nan
+        _check(v, dtype, scoring, topk, bias=odd, renorm=True, total=t)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,groups,kept,topk", [(256, 8, 4, 8), (160, 8, 3, 6), (128, 16, 5, 7), (128, 2, 1, 16),
+                                                (30, 3, 2, 7), (36, 6, 6, 4), (8, 4, 1, 2), (512, 32, 4, 8), (480, 5, 2, 8)])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_odd_rows_of_large_batches_with_groups(e, groups, kept, topk, group_top, scoring, dtype):
+    v = _odd_rows(e, dtype, e + groups)
+    kw = dict(groups=groups, topk_groups=kept, group_top=group_top)
+    bias = np.random.default_rng(e).standard_normal(e) * 0.05
+    for t in (550, 4102):
+        _check(v, dtype, scoring, topk, renorm=scoring == "sigmoid", total=t, **kw)
+        _check(v, dtype, scoring, topk, bias=bias, renorm=True, scale=2.5, total=t, **kw)
 
 
 def test_another_stream_and_no_tokens():
