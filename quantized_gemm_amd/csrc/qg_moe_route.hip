@@ -22,7 +22,7 @@
 // bytes (8192 tokens of 256 float32 logits are 8.4 MB), so larger batches take four tokens per wave, one
 // per row of 16 lanes, whose reductions are four lane moves: see moe_route_rows_kernel.
 // Measured, launches in a graph: 1 token of 128 experts 3.3 us (a launch by itself), 4096 of 128 float32
-// 4.9 us, 8192 of 256 float32 with bias and groups 13.7 us (0.61 TB/s).
+// 4.9 us, 8192 of 256 float32 with bias and groups 10.0 us (0.84 TB/s).
 #include "qg_device.h"
 #include "qg_kernels.h"
 
@@ -120,24 +120,37 @@ __device__ __forceinline__ void group_best(const RouteLane& p, double& b1, doubl
   for (int off = 1; off < p.lanes; off <<= 1) merge2(b1, b2, __shfl_xor(b1, off, 64), __shfl_xor(b2, off, 64));
 }
 
-// A score to 2^-35, for fixed-point choice values: exp(l - mx) (softmax, still to be divided by the
-// row's sum) or 1 / (1 + exp(-l)).  The exponential is 2^n e^r with |r| <= ln 2 / 2 and e^r by its Taylor
-// series to r^10 / 10!.
-__device__ __forceinline__ double quick_score(bool softmax, float l, float mx) {
-  double x = softmax ? (double)l - (double)mx : -(double)l;
-  x = fmin(fmax(x, -700.0), 700.0);
+// Scores of V logits to 2^-34, for fixed-point choice values: exp(l - mx) (softmax, still to be divided by
+// the row's sum) or 1 / (1 + exp(-l)), 0 for experts that are out.  The exponential is 2^n e^r with
+// |r| <= ln 2 / 2 and e^r by its Taylor series to r^9 / 9!, which leaves 2^-37.  Without branches, so that
+// the V chains of dependent operations run through one another.
+__device__ __forceinline__ double quick_exp(double x) {            // |x| <= 700
   const double n = rint(x * 1.4426950408889634);
   const double r = fma(n, -0.69314718055994531, x);
-  double e = 1.0 / 3628800;
-  constexpr double kFact[] = {362880, 40320, 5040, 720, 120, 24, 6, 2, 1, 1};
+  double e = 1.0 / 362880;
+  constexpr double kFact[] = {40320, 5040, 720, 120, 24, 6, 2, 1, 1};
 #pragma unroll
-  for (int i = 0; i < 10; ++i) e = fma(e, r, 1.0 / kFact[i]);
-  e = __builtin_ldexp(e, (int)n);
-  if (softmax) return e;
-  const double d = 1.0 + e;
-  double y = __builtin_amdgcn_rcp(d);
-  y = fma(fma(-d, y, 1.0), y, y);
-  return fma(fma(-d, y, 1.0), y, y);
+  for (int i = 0; i < 9; ++i) e = fma(e, r, 1.0 / kFact[i]);
+  return __builtin_ldexp(e, (int)n);
+}
+template <int V>
+__device__ __forceinline__ void quick_scores(bool softmax, const float (&l)[V], float mx, double (&s)[V]) {
+  if (softmax) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const double e = quick_exp(fmax((double)l[i] - (double)mx, -700.0));   // (-inf - -inf: -700)
+      s[i] = l[i] > -__builtin_inff() ? e : 0.0;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const double d = 1.0 + quick_exp((double)fminf(fmaxf(-l[i], -700.f), 700.f));
+      double y = __builtin_amdgcn_rcp(d);
+      y = fma(fma(-d, y, 1.0), y, y);
+      y = fma(fma(-d, y, 1.0), y, y);
+      s[i] = l[i] > -__builtin_inff() ? y : 0.0;
+    }
+  }
 }
 
 // Fixed-point choice values of a row: key = 1 + (c - lo) * inv, of kBits bits.
@@ -220,10 +233,12 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const RouteLane& p, K
 
 // The float32 logit a row holds for an expert: +inf as the largest finite value, NaN as -inf (not eligible),
 // -0 as 0 (keys order bits, and the two are equal).
+__device__ __forceinline__ float eligible(float x) {
+  return x > -__builtin_inff() ? fminf(x, 3.402823466e38f) + 0.f : -__builtin_inff();
+}
 template <int T>
 __device__ __forceinline__ float eligible_logit(const RouteArgs& a, int64_t t, int e) {
-  const float x = logit_of<T>(a.logits, t * a.stride + e);
-  return x > -__builtin_inff() ? fminf(x, 3.402823466e38f) + 0.f : -__builtin_inff();
+  return eligible(logit_of<T>(a.logits, t * a.stride + e));
 }
 
 // One token by a whole wave, up to V experts per lane.
@@ -259,9 +274,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   } else {
     double s[V], sum = 0;
     float blo = finf, bhi = -finf;
+    quick_scores<V>(a.softmax, l, mx, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      s[i] = l[i] > -finf ? quick_score(a.softmax, l[i], mx) : 0.0;
       sum += s[i];
       const bool ok = l[i] > -finf && b[i] > -finf;
       blo = ok ? fminf(blo, b[i]) : blo;
@@ -273,8 +288,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
     bool sure = f.ok;
     if (sure) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        k[i] = gk[i] = l[i] > -finf && b[i] > -finf ? (int)f.key(s[i] * scale + (double)b[i]) : kNone;
+      for (int i = 0; i < V; ++i) {
+        const int fixed = (int)f.key(s[i] * scale + (double)b[i]);
+        k[i] = gk[i] = l[i] > -finf && b[i] > -finf ? fixed : kNone;
+      }
       sure = choose<int, V>(a, p, k, gk, (int)f.key(0.0), 1, id, key);
     }
     if (!sure) {
@@ -335,6 +352,44 @@ __device__ __forceinline__ F row_sum(F x, int lanes) {
   return x;
 }
 
+// V values of a row from element e on, at an address that is a multiple of 16 bytes (16-bit ones: 8).
+template <int T, int V>
+__device__ __forceinline__ void load_run(const void* p, int64_t e, float (&v)[V]) {
+  if constexpr (T == S_F32) {
+    const f32x4* q = (const f32x4*)((const float*)p + e);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const f32x4 x = q[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j];
+    }
+  } else {
+    const u32x2* q = (const u32x2*)((const uint16_t*)p + e);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const u32x2 x = q[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint16_t bits = (uint16_t)(x[j >> 1] >> (16 * (j & 1)));
+        v[4 * i + j] = logit_of<T>(&bits, 0);
+      }
+    }
+  }
+}
+
+// Counts the groups before this lane's, gv being each group's value in all of its lanes: those of greater value, or of an equal one and lower index.
+template <int R>
+__device__ __forceinline__ void count_before(uint32_t gv, int group, int lanes, int& before) {
+  if constexpr (R < 16) {
+    if ((R & (lanes - 1)) == 0) {                                  // (turns by whole groups: one lane of each)
+      const uint32_t o = lane_move<0x120 + R>(gv, 0u);
+      const int og = (int)lane_move<0x120 + R>((uint32_t)group, 0u);
+      before += (o > gv) || (o == gv && og < group) ? 1 : 0;
+    }
+    count_before<R + 1>(gv, group, lanes, before);
+  }
+}
+
 // Four tokens per wave, token r on lanes 16 r .. 16 r + 15, up to V experts per lane: for choices by
 // scores (fixed-point ones, checked; a token too close to call goes to route_token) and for choices by
 // 16-bit logits, whose float32 images leave bits for the expert's index.
@@ -345,7 +400,8 @@ __device__ __forceinline__ F row_sum(F x, int lanes) {
 // without taking that one out: of all u - before, modulo 2^32, those of smaller keys are the larger
 // ones, in order.
 template <int T, int V>
-__global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a, int lanes_log2, int wave_lanes_log2) {
+__global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a, int lanes_log2, bool runs,
+                                                             int wave_lanes_log2) {
   const int lane = threadIdx.x & 63, l16 = lane & 15;
   const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 4;
   if (t0 >= a.tokens) return;
@@ -357,11 +413,30 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a, int la
   const bool by_score = T == S_F32 || a.bias || (a.groups > 1 && a.group_top == 2);
   auto key_of = [](float x) __attribute__((always_inline)) { return (uint32_t)KeyOf<int>::of(x) ^ 0x80000000u; };
   auto value_of = [](uint32_t u) __attribute__((always_inline)) { return KeyOf<int>::value((int)(u ^ 0x80000000u)); };
-  float l[V], mx = -finf;
+  // The lane's i-th expert is its group's at(i): runs of V, read 16 bytes at a time, where they fill the
+  // group and are aligned, else every lanes-th (places past a group's experts read its last one and are out).
+  // With 8 groups a scalar load touches 32 lines: 8192 tokens of 256 logits 14.3 us so, 10.0 us by runs.
+  const int at_step = runs ? 1 : lanes, l_step = runs ? V : 1;
+  auto at = [&](int i) __attribute__((always_inline)) { return i * at_step + gl * l_step; };
+  float l[V], b[V], mx = -finf;
+  const int first = (group < a.groups ? group : 0) * size;
+  if (runs) {
+    const int64_t e = first + gl * V;                               // (groups past the last one read the first)
+    load_run<T, V>(a.logits, t * a.stride + e, l);
+    if (a.bias) load_run<S_F32, V>(a.bias, e, b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = first + min(at(i), size - 1);
+      l[i] = logit_of<T>(a.logits, t * a.stride + e);
+      if (a.bias) b[i] = a.bias[e];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int j = (i << lanes_log2) + gl;
-    l[i] = group < a.groups && j < size ? eligible_logit<T>(a, t, group * size + j) : -finf;
+    const float x = eligible(l[i]);
+    l[i] = (group < a.groups) & (at(i) < size) ? x : -finf;
+    b[i] = a.bias ? b[i] : 0.f;
     mx = fmaxf(mx, l[i]);
   }
   if (a.softmax) mx = value_of(row_max(key_of(mx)));
@@ -369,12 +444,10 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a, int la
   bool sure = true;
   if (by_score) {
     double s[V], sum = 0;
-    float b[V], blo = finf, bhi = -finf;
+    float blo = finf, bhi = -finf;
+    quick_scores<V>(a.softmax, l, mx, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int j = (i << lanes_log2) + gl;
-      b[i] = a.bias && group < a.groups && j < size ? a.bias[group * size + j] : 0.f;
-      s[i] = l[i] > -finf ? quick_score(a.softmax, l[i], mx) : 0.0;
       sum += s[i];
       const bool ok = l[i] > -finf && b[i] > -finf;
       blo = ok ? fminf(blo, b[i]) : blo;
@@ -386,15 +459,15 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a, int la
     zero = f.key(0.0);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool ok = l[i] > -finf && b[i] > -finf;
-      u[i] = ok && f.ok ? f.key(s[i] * scale + (double)b[i]) << 4 | (15u - i) : 0u;
+      const uint32_t fixed = f.key(s[i] * scale + (double)b[i]) << 4 | (15u - i);
+      u[i] = (int)f.ok & (l[i] > -finf) & (b[i] > -finf) ? fixed : 0u;
       b2 = max(b2, min(b1, u[i]));
       b1 = max(b1, u[i]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = group * size + (i << lanes_log2) + gl;
+      const int e = group * size + at(i);
       u[i] = l[i] > -finf ? (key_of(l[i]) & ~511u) | (511u - e) : 0u;
       b1 = max(b1, u[i]);
     }
@@ -409,14 +482,8 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a, int la
     if (lanes > 4) join(lane_move<kHalfMirror>(b1, 0u), lane_move<kHalfMirror>(b2, 0u));
     const uint32_t gv = group >= a.groups || b1 == 0 ? 0u
                         : a.group_top == 1 || !by_score ? b1 : (b1 >> 4) + (b2 == 0 ? zero : b2 >> 4);
-    int before = 0;                                                // lanes of groups before this lane's
-#pragma unroll
-    for (int r = 1; r < 16; ++r) {
-      const uint32_t o = (uint32_t)__shfl((int)gv, (lane & 48) | ((l16 + r) & 15), 64);
-      const int og = ((l16 + r) & 15) >> lanes_log2;
-      before += (o > gv) || (o == gv && og < group) ? 1 : 0;
-    }
-    const int rank = before >> lanes_log2;
+    int rank = 0;
+    count_before<1>(gv, group, lanes, rank);
     const bool kept = rank < a.topk_groups && group < a.groups;
     if (by_score) {
       const uint32_t low = row_max(rank == a.topk_groups - 1 && group < a.groups ? gv : 0u);
@@ -443,7 +510,7 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a, int la
       const uint64_t holders = __ballot(here), rows = __ballot(found);
       sure = sure && 16 * __popcll(holders) == __popcll(rows);     // the same key on two lanes of a row: too close
       const int i = 15 - (int)(best & 15u);
-      e = (int)row_min(here ? (uint32_t)(group * size + (i << lanes_log2) + gl) : ~0u);
+      e = (int)row_min(here ? (uint32_t)(group * size + at(i)) : ~0u);
     } else {
       e = 511 - (int)(best & 511u);
     }
@@ -481,10 +548,19 @@ int lanes_per_group(int lanes, int groups) {   // log2
 }
 
 // Rows of 16 lanes from kRowTokens tokens, four per SIMD: below, a token per wave takes less time by
-// itself.  Wave per token against rows: 2048 tokens of 256 sigmoid scores with bias and groups 6.8 / 9.8 us,
-// 4096 9.4 / 10.0, 8192 14.6 / 13.7; 64 softmax scores with bias 4.8 / 5.5, 6.6 / 5.6, 9.0 / 6.6; 128 bf16
-// logits 4.1 / 5.0, 4.9 / 5.0, 7.0 / 5.2.
+// itself.  Wave per token against rows: 2048 tokens of 256 sigmoid scores with bias and groups 6.8 / 7.3 us,
+// 4096 9.1 / 7.5, 8192 14.4 / 10.0; 64 softmax scores with bias 4.8 / 5.1, 6.1 / 5.1, 8.8 / 6.1; 128 bf16
+// logits 4.1 / 4.4, 4.9 / 4.5, 7.0 / 4.7.
 constexpr int64_t kRowTokens = 4096;
+
+template <int T, int V>
+void launch_rows(const RouteArgs& a, int lanes_log2, int wave_lanes_log2, hipStream_t st) {
+  constexpr int kAlign = T == S_F32 ? 16 : 8, kBytes = T == S_F32 ? 4 : 2;
+  const bool runs = (V << lanes_log2) * a.groups == a.experts && (uintptr_t)a.logits % kAlign == 0 &&
+                    a.stride * kBytes % kAlign == 0 && (uintptr_t)a.bias % 16 == 0;
+  hipLaunchKernelGGL((moe_route_rows_kernel<T, V>), dim3((unsigned)((a.tokens + 15) / 16)), dim3(256), 0, st, a, lanes_log2,
+                     runs, wave_lanes_log2);
+}
 
 template <int T>
 bool launch_route(const RouteArgs& a, hipStream_t st) {
@@ -494,10 +570,9 @@ bool launch_route(const RouteArgs& a, hipStream_t st) {
       (T != S_F32 || a.bias || (a.groups > 1 && a.group_top == 2))) {
     const int row_log2 = lanes_per_group(16, a.groups);
     const int v = (size + (1 << row_log2) - 1) >> row_log2;
-    const dim3 grid((unsigned)((a.tokens + 15) / 16));
-    if (v <= 4) hipLaunchKernelGGL((moe_route_rows_kernel<T, 4>), grid, dim3(256), 0, st, a, row_log2, log2);
-    else if (v <= 8) hipLaunchKernelGGL((moe_route_rows_kernel<T, 8>), grid, dim3(256), 0, st, a, row_log2, log2);
-    else if (v <= 16) hipLaunchKernelGGL((moe_route_rows_kernel<T, 16>), grid, dim3(256), 0, st, a, row_log2, log2);
+    if (v <= 4) launch_rows<T, 4>(a, row_log2, log2, st);
+    else if (v <= 8) launch_rows<T, 8>(a, row_log2, log2, st);
+    else if (v <= 16) launch_rows<T, 16>(a, row_log2, log2, st);
     if (v <= 16) return true;
   }
   const dim3 grid((unsigned)((a.tokens + 3) / 4));

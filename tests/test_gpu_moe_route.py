@@ -206,6 +206,7 @@ def test_odd_rows_of_large_batches_with_groups(e, groups, kept, topk, group_top,
     for t in (550, 4102):
         _check(v, dtype, scoring, topk, renorm=scoring == "sigmoid", total=t, **kw)
         _check(v, dtype, scoring, topk, bias=bias, renorm=True, scale=2.5, total=t, **kw)
+        _check(v, dtype, scoring, topk, bias=bias, pad=3, total=t, **kw)          # rows at odd addresses
 
 
 def test_another_stream_and_no_tokens():
