@@ -3,8 +3,8 @@
  *
  * What it computes: Y = X . dequant(Wq, scales, zeros)^T with low-bit weights
  * (int4 / uint4 + zero points, FP4 e2m1 with UE8M0 block scales, FP8 e4m3 with
- * channel scales, int8 with channel scales) and f16 / bf16 / FP8 e4m3 / int8 activations, as a dense layer and as
- * an MoE grouped GEMM over routed tokens.  Sources: the web pages on the Humming
+ * channel scales, int8 with channel scales) and f16 / bf16 / FP8 e4m3 / int8 activations,
+ * as a dense layer and as an MoE grouped GEMM over routed tokens.  Sources: the web pages on the Humming
  * quantized-GEMM library -- "Humming" (README), "Key Features" and "Support Matrix"
  * (weight, activation and scale types; dense and MoE GEMM); "Humming: Fast,
  * Flexible Kernels for Quantized Inference" (the standard format of weights,
@@ -321,10 +321,10 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
  *             rows; out = packed e2m1 codes uint8 [rows][inter/2] (16-byte aligned)
  *             QG_A_INT8: each row quantized for the next product's int8 activations, act in
  *             float32 under the rule of qg_quantize_int8_rows; out = int8 [rows][inter]
- *   out_scale device float32 [rows] for QG_A_FP8_E4M3 and QG_A_INT8, uint8 [rows][inter/32] UE8M0 exponents
- *             for QG_A_FP4_E2M1, else ignored (may be NULL)
- * inter % 8 == 0 (and inter <= 8192 for QG_A_FP8_E4M3, <= 32768 for QG_A_INT8, inter % 32 == 0 for QG_A_FP4_E2M1),
- * else QG_ERR_UNSUPPORTED.  Rows of
+ *   out_scale device float32 [rows] for QG_A_FP8_E4M3 and QG_A_INT8, uint8 [rows][inter/32]
+ *             UE8M0 exponents for QG_A_FP4_E2M1, else ignored (may be NULL)
+ * inter % 8 == 0 (and inter <= 8192 for QG_A_FP8_E4M3, <= 32768 for QG_A_INT8, inter % 32 == 0
+ * for QG_A_FP4_E2M1), else QG_ERR_UNSUPPORTED.  Rows of
  * slots the gate/up product did not write give unspecified values, which nothing reads.
  */
 qg_status qg_moe_swiglu(const void* gate_up, int64_t rows, int64_t inter, int32_t in_type, int32_t out_type,

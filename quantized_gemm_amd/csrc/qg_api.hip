@@ -250,7 +250,7 @@ constexpr int64_t kStreamMaxRows = 64;
 constexpr int kMaxSplit = 8;
 int split_for(int64_t tiles, int64_t k, int group, const PathInfo& pi) {
   if (pi.binv || tiles * 2 > kCUs) return 1;
-  const int64_t bk = pi.af == A_FP8 || pi.af == A_INT8 ? 128 : 64;   // K per step: 128 bytes
+  const int64_t bk = pi.af == A_FP8 ? 128 : 64;   // K per step: fp8 MFMAs take 128
   const int64_t steps = k / bk;
   int sp = 1;
   while (sp < kMaxSplit && tiles * sp * 2 <= kCUs && steps % (sp * 2) == 0 && steps / (sp * 2) >= 8 &&
@@ -629,7 +629,7 @@ int32_t qg_moe_block_m(const qg_prepared* p, int64_t tokens, int32_t topk) {
   }
   if (is_block(pi) && busy <= 64) return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
   if (mean <= 16) return 16;
-  if (mean <= 24 && pi.af != A_FP8 && pi.af != A_INT8) return 32;
+  if (mean <= 24 && pi.af != A_FP8) return 32;
   // 256-row blocks halve the weight conversion per FLOP and add padding rows: int4 weights
   // converted to e4m3 take them from a mean of 128 rows (E = 64 top-6 skewed, K = 4096: a mean
   // of 144 / 192 / 256 / 512 / 768 rows 240 / 319 / 386 / 663 / 943 -> 221 / 293 / 343 / 568 /
@@ -771,7 +771,8 @@ qg_status qg_moe_swiglu(const void* gate_up, int64_t rows, int64_t inter, int32_
   if (rows > ((int64_t)1 << 31) - 1 || rows * inter > ((int64_t)1 << 40)) return QG_ERR_UNSUPPORTED;
   if (rows == 0) return QG_OK;
   if (!gate_up || !out || !aligned16(gate_up) || !aligned16(out)) return QG_ERR_INVALID_ARG;
-  if ((out_type == QG_A_FP8_E4M3 || out_type == QG_A_INT8) && (!out_scale || ((uintptr_t)out_scale & 3u) != 0)) return QG_ERR_INVALID_ARG;
+  if ((out_type == QG_A_FP8_E4M3 || out_type == QG_A_INT8) && (!out_scale || ((uintptr_t)out_scale & 3u) != 0))
+    return QG_ERR_INVALID_ARG;
   if (out_type == QG_A_FP4_E2M1 && !out_scale) return QG_ERR_INVALID_ARG;
   qg_status s = check_arch();
   if (s != QG_OK) return s;

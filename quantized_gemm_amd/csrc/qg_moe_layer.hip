@@ -317,11 +317,17 @@ static bool launch_rows_e4m3(const uint16_t* g, int64_t rows, int64_t inter, int
   return true;
 }
 
+// (a launch takes fewer than 2^32 threads)
+constexpr int64_t kInt8RowsPerLaunch = 1 << 21;
+
 template <int IN, bool SILU, int NT, int P>
 static void launch_rows_int8_one(const uint16_t* x, int64_t rows, int64_t k, int8_t* codes, float* scale, hipStream_t st) {
   constexpr int RPB = NT < 256 ? 256 / NT : 1;
-  hipLaunchKernelGGL((rows_int8_kernel<IN, SILU, NT, P>), dim3((unsigned)((rows + RPB - 1) / RPB)), dim3(NT * RPB), 0, st, x,
-                     rows, k, codes, scale);
+  for (int64_t r = 0; r < rows; r += kInt8RowsPerLaunch) {
+    const int64_t n = rows - r < kInt8RowsPerLaunch ? rows - r : kInt8RowsPerLaunch;
+    hipLaunchKernelGGL((rows_int8_kernel<IN, SILU, NT, P>), dim3((unsigned)((n + RPB - 1) / RPB)), dim3(NT * RPB), 0, st,
+                       x + r * (SILU ? 2 : 1) * k, n, k, codes + r * k, scale + r);
+  }
 }
 
 // A wave per row up to 2048 values, 256 threads up to 8192, 1024 up to kInt8RowMax.

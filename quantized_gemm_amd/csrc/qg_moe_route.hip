@@ -588,12 +588,23 @@ bool launch_route(const RouteArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// A launch takes fewer than 2^32 threads, 64 per token.
+constexpr int64_t kTokensPerLaunch = 1 << 24;
+
 bool launch_moe_route(const RouteArgs& a, int in_t, hipStream_t st) {
   if (a.experts > kRouteMaxExperts) return false;
-  if (in_t == S_F32) return launch_route<S_F32>(a, st);
-  if (in_t == S_BF16) return launch_route<S_BF16>(a, st);
-  if (in_t == S_F16) return launch_route<S_F16>(a, st);
-  return false;
+  for (int64_t t = 0; t < a.tokens; t += kTokensPerLaunch) {
+    RouteArgs b = a;
+    b.logits = (const char*)a.logits + t * a.stride * (in_t == S_F32 ? 4 : 2);
+    b.ids += t * a.topk;
+    b.weights += t * a.topk;
+    b.tokens = a.tokens - t < kTokensPerLaunch ? a.tokens - t : kTokensPerLaunch;
+    if (in_t == S_F32 ? !launch_route<S_F32>(b, st)
+        : in_t == S_BF16 ? !launch_route<S_BF16>(b, st)
+        : in_t == S_F16 ? !launch_route<S_F16>(b, st) : true)
+      return false;
+  }
+  return true;
 }
 
 }  // namespace qg

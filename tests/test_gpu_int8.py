@@ -11,8 +11,8 @@ Bars, from the arithmetic:
 * SwiGLU -> int8: bit-exact where silu(gate) is exact; else scales to 2^-20 relative (float32
   sigmoid with the hardware exponential, as for e4m3) and each value within half a code of the
   float64 activation plus that noise;
-* the layer: the float64 layer (unrounded, unquantized intermediates) within 5e-2 of its largest
-  output, see test_int8_layer_from_logits.
+* the layer: the float64 layer with its two quantizations within 2e-2 of its largest output, see
+  test_int8_layer_from_logits.
 """
 import numpy as np
 import pytest
@@ -114,6 +114,36 @@ def test_dense_full_size_is_exact(m):
     assert np.array_equal(_got(y)[rows], want)
 
 
+# every tile height and width, K split and not, with 1, 2, 3 and no steps after the last whole turn of the stage ring
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(40, 8256, 640), (260, 8320, 1408), (257, 7168, 640), (200, 8256, 896), (513, 4160, 768),
+                                   (1224, 1600, 512), (1000, 7168, 896), (2500, 1856, 1408), (1500, 10304, 896),
+                                   (4000, 7168, 640), (668, 704, 23040), (300, 576, 4096), (65, 4160, 4096),
+                                   (33, 1856, 8192)])
+def test_every_tile_is_exact(m, n, k, out):
+    layer, acts = synth.dense_w8a8_int8(m=m, n=n, k=k, out=out, seed=m + n + k)
+    p, buf = layers.prepare_layer(layer)
+    x, xs = layers.acts_to_dev(acts)
+    y = torch.full((m + 1, n), float("nan"), dtype=T_DTYPE[out], device="cuda")
+    need = qg.workspace_bytes(p, m)
+    ws = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    qg.gemm(p, x, xs, y, m, ws[:need] if need else None)
+    torch.cuda.synchronize()
+    assert torch.isnan(y[m]).all() and (ws[need:] == 0xA5).all()        # nothing behind the last row or the partials
+    rows = np.unique(np.concatenate([[0, m - 1], np.random.default_rng(0).integers(0, m, 60)]))
+    want = _want(acts.x[rows], acts.x_scale[rows], layer.w[0], layer.s[0, :, 0], out)
+    assert np.array_equal(_got(y[:m])[rows], want)
+    # the rows not sampled: the same bits as by the kernel or tile of 32 rows
+    again = torch.full((m, n), float("nan"), dtype=T_DTYPE[out], device="cuda")
+    for r in range(0, m, 32):                                         
+        e = min(m, r + 32)
+        z = qg.workspace_bytes(p, e - r)
+        qg.gemm(p, x[r:e], xs[r:e].contiguous(), again[r:e], e - r,
+                torch.empty(z, dtype=torch.uint8, device="cuda") if z else None)
+    torch.cuda.synchronize()
+    assert torch.equal(again.view(torch.int16), y[:m].view(torch.int16))
+
+
 @pytest.mark.parametrize("m", [1, 20, 40, 200])
 def test_sums_up_to_the_31st_bit(m):
     # K = 130944 of -128 x -128: 2145386496 < 2^31; then of -128 x 127, and rows of zeros
@@ -171,6 +201,42 @@ def test_missing_or_small_workspace_is_refused():
         assert e.value.status == 5
     torch.cuda.synchronize()
     assert torch.isnan(y).all()
+
+
+def test_no_rows():
+    layer, acts = synth.dense_w8a8_int8(m=1, n=64, k=128, seed=1)
+    p, buf = layers.prepare_layer(layer)
+    x, xs = layers.acts_to_dev(acts)
+    y = torch.full((1, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    qg.gemm(p, x, xs, y, 0)
+    i = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    qg.moe_gemm(p, x, xs, i, i, i, 0, 1, 16, y)
+    codes, scale = torch.full((1, 64), 7, dtype=torch.int8, device="cuda"), torch.full((1,), 7.0, device="cuda")
+    qg.quantize_int8_rows(y, 0, 64, qg.A_BF16, codes, scale)
+    qg.moe_swiglu(y, 0, 32, qg.O_BF16, qg.A_INT8, codes, scale)
+    torch.cuda.synchronize()
+    assert torch.isnan(y).all() and (codes == 7).all() and (scale == 7).all()
+
+
+def test_two_streams_at_once():
+    # two products in flight together, each with its own workspace and outputs
+    layer, acts = synth.dense_w8a8_int8(m=200, n=1024, k=4096, seed=12)
+    p, buf = layers.prepare_layer(layer)
+    x, xs = layers.acts_to_dev(acts)
+    want = _want(acts.x, acts.x_scale, layer.w[0], layer.s[0, :, 0], "bf16")
+    need = max(qg.workspace_bytes(p, 64), qg.workspace_bytes(p, 200), 16)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ys = [[torch.full((m, 1024), float("nan"), dtype=torch.bfloat16, device="cuda") for m in (64, 200)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s_, w_, y_ in zip(streams, ws, ys):
+            for m, y in zip((64, 200), y_):
+                qg.gemm(p, x, xs, y, m, w_, stream=s_)
+    torch.cuda.synchronize()
+    for y_ in ys:
+        for m, y in zip((64, 200), y_):
+            assert np.array_equal(_got(y), want[:m])
 
 
 # ---- grouped ---------------------------------------------------------------------------------
@@ -303,6 +369,27 @@ def test_swiglu_int8(rows, inter, dtype):
     # half a code, the quotient's own rounding (127 * 2^-24 of a code) and the float32 activation
     bound = (0.5 + 2.0 ** -17) * step + 2.0 ** -16 * np.abs(act)
     assert np.all(np.abs(codes * step - act) <= bound)
+
+
+def test_more_rows_than_one_launch_takes():
+    # 2^21 rows a launch: the last rows of the first and the rows of the second against the first ones' results
+    rows, k = (1 << 21) + 70, 16
+    bits, _ = synth.act_rows(1000, k, "bf16", sigma=3.0, seed=1)
+    x = _dev16(bits).repeat((rows + 999) // 1000, 1)[:rows].contiguous()
+    rc, rs = Q.absmax_int8_rows(F.decode_act(bits, "bf16").astype(np.float32))
+    codes = torch.full((rows + 1, k), 77, dtype=torch.int8, device="cuda")
+    scale = torch.full((rows + 1,), 77.0, device="cuda")
+    qg.quantize_int8_rows(x, rows, k, qg.A_BF16, codes, scale)
+    torch.cuda.synchronize()
+    reps = (rows + 999) // 1000
+    assert torch.equal(codes[:rows], torch.from_numpy(rc).cuda().repeat(reps, 1)[:rows]) and (codes[rows] == 77).all()
+    assert torch.equal(scale[:rows], torch.from_numpy(rs).cuda().repeat(reps)[:rows]) and scale[rows] == 77
+    act = torch.full((rows + 1, 8), 77, dtype=torch.int8, device="cuda")
+    first = torch.empty((1000, 8), dtype=torch.int8, device="cuda")
+    qg.moe_swiglu(x, 1000, 8, qg.O_BF16, qg.A_INT8, first, torch.empty(1000, device="cuda"))
+    qg.moe_swiglu(x, rows, 8, qg.O_BF16, qg.A_INT8, act, scale)
+    torch.cuda.synchronize()
+    assert torch.equal(act[:rows], first.repeat(reps, 1)[:rows]) and (act[rows] == 77).all()
 
 
 # ---- a whole layer -----------------------------------------------------------------------------

@@ -209,6 +209,14 @@ def test_odd_rows_of_large_batches_with_groups(e, groups, kept, topk, group_top,
         _check(v, dtype, scoring, topk, bias=bias, pad=3, total=t, **kw)          # rows at odd addresses
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_more_tokens_than_one_launch_takes(scoring):
+    t = (1 << 24) + 37
+    v = np.random.default_rng(0).standard_normal((1009, 4))
+    _check(v, "bf16", scoring, 1, total=t)
+    _check(v, "f32", scoring, 2, bias=np.array([0.1, 0, -0.1, 0.3]), renorm=True, total=t)
+
+
 def test_another_stream_and_no_tokens():
     v = np.random.default_rng(0).standard_normal((77, 64))
     s = torch.cuda.Stream()
