@@ -222,19 +222,17 @@ void stream_shape(StreamTile& t, int64_t n, int ncb, int kq) {
   t.grid_x = (unsigned)((n / 16 + ncb - 1) / ncb);
 }
 
-// int8 dense streaming: 1 x 8 shapes, 2 x 4 where K is short for eight parts (a wave's part is one
-// batch of loads up to 1024) and the columns fill the GPU: one row, K = 4096, N = 14336 13.7 -> 11.2
-// us; at K = 7168 9.8 us with 1 x 8, 10.9 with 2 x 4.  K is never split over workgroups: unsplit
-// shapes or the MFMA kernel's tiles beat it throughout (16 rows, N = K = 4096 8.8 us split, 5.8).
-bool int8_wide(int64_t rows, int64_t n, int64_t k) { return n > 4096 && k <= (rows <= 4 ? 4096 : 2048); }
-// Rows the streaming kernel takes: to 4 always; to 16 and 32 while K is short or, with few columns,
-// of one batch per part (N = K = 4096, 16 / 32 rows: 5.8 / 7.0 us against 7.8 / 8.0 on the MFMA
-// kernel; N = 1024, K = 8192: 6.7 / 9.3 against 8.1 / 8.2; N = 7168, K = 2048: 6.2 / 5.7 against 7.2
-// / 6.9; N = 14336, K = 4096: 12.8 / 16.4 against 11.7).
-bool int8_streams(int64_t rows, int64_t n, int64_t k) {
-  if (rows <= 4) return true;
-  if (rows > 32) return false;
-  return n <= 4096 ? k <= (rows <= 16 ? 8192 : 4096) : k <= 2048;
+// Rows the few-rows int8 kernel takes.  To 32 rows it reads the weights faster than the tiles with K split
+// (us with 3 / 16 sets of weights in turn, of which the first stay in the last-level cache: N = K = 7168, 8
+// rows 9.2 / 9.6 against 12.1 / 14.4, 32 rows 10.3 / 12.8 against 13.0 / 15.3; N = 1024, K = 8192, 16 rows 4.8 /
+// 4.9 against 6.3 / 6.8); few columns leave CUs idle then, which K split over workgroups uses, so with long
+// K those win (N = 2048, K = 14336, 32 rows 9.5 / 14.7 against 10.1 / 13.1).  To 64 rows while
+// activations are no more of what a CU loads than the weights it can wait for (64 rows: N = K = 4096 7.4 /
+// 8.4 against 9.1 / 10.2, N = K = 7168 12.1 / 17.2 against 14.5 / 17.3, N = 2048, K = 14336 14.3 / 21 against
+// 11.1 / 14.7) and the columns are one round of workgroups (N = 14336, K = 4096 16.5 / 20.6 against 12.2 / 20.7).
+bool int8_rows(int64_t rows, int64_t n, int64_t k) {
+  if (rows <= 32) return n > 4096 || (16 + (rows <= 8 ? 8 : rows <= 16 ? 16 : 32)) * k <= 3 << 18;
+  return rows <= 64 && n <= 8192 && k <= (n > 4096 ? 8192 : 6528);
 }
 
 // MFMA-bound family: rows per tile 256 while that still leaves about 1.5 workgroups per
@@ -276,7 +274,7 @@ bool rows256(int64_t rows, int64_t ntiles) {
 // beginning and end cost `fixed` us plus `out` us per round of workgroups (writing the outputs).
 // Fitted to 26 shapes (33..4096 rows, 192..28672 columns, K 640..8192), which it orders within 7%:
 // at N = K = 7168 the tiles that measured best are 64 x 128 with K split in two at 64 rows (14.3 us,
-// unsplit 17, 64 x 256 split in four 16.2), 64 x 128 at 256 (20.0; 128 x 128 23.0), 128 x 128 at 512
+// unsplit 17, 64 x 256 split in four 16.2; the few-rows kernel 12.1), 64 x 128 at 256 (20.0; 128 x 128 23.0), 128 x 128 at 512
 // (29.2; 64 x 256 31.2, 128 x 256 38.7), 128 x 256 at 1024 (49.7; 128 x 128 52.4, 256 x 256 69.8),
 // 256 x 256 at 4096 (181; 128 x 256 189, 128 x 128 213).
 struct Int8Tile { int bm, cols; double lat, full, fixed, out; };
@@ -372,21 +370,21 @@ bool is_block(const PathInfo& pi) { return pi.wp_small == WP_FP8_BLOCK; }
 // and below the streaming kernel is faster), 64 for block-scaled e4m3 (streamed 15-22 us
 // against 21-24 us at 17..64 rows).
 int64_t dense_stream_max(const PathInfo& pi) { return is_block(pi) ? 64 : 32; }
-bool dense_streams(const PathInfo& pi, int64_t m, int64_t n, int64_t k) {
-  if (pi.binv) return false;   // batch-invariant: one MMA type for every M
-  return pi.af == A_INT8 ? int8_streams(m, n, k) : m <= dense_stream_max(pi);
+bool dense_streams(const PathInfo& pi, int64_t m) {
+  return !pi.binv && pi.af != A_INT8 && m <= dense_stream_max(pi);   // batch-invariant: one MMA type for every M
 }
 MfmaTile block_tile(int64_t rows, int64_t n, int64_t k, const PathInfo& pi) { return mfma_tile(rows, n, k, 128, pi); }
 
 // Workspace of a dense call: the split-K partial sums.
 size_t dense_workspace(const qg_prepared* p, const PathInfo& pi, int64_t m) {
+  if (pi.af == A_INT8 && int8_rows(m, p->desc.n, p->desc.k)) return 0;
   if (pi.af == A_FP4) return 0;   // W4A4 splits K only inside a workgroup
   if (is_block(pi) && (m > dense_stream_max(pi) || pi.binv)) {
     const MfmaTile t = block_tile(m, p->desc.n, p->desc.k, pi);
     return t.ksplit > 1 ? (size_t)t.ksplit * (size_t)m * (size_t)p->desc.n * sizeof(float) : 0;
   }
-  if (dense_streams(pi, m, p->desc.n, p->desc.k)) {
-    const int sp = pi.af == A_INT8 ? 1 : stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
+  if (dense_streams(pi, m)) {
+    const int sp = stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
     return sp > 1 ? (size_t)sp * (size_t)m * (size_t)p->desc.n * sizeof(float) : 0;
   }
   const MfmaTile t = mfma_tile(m, p->desc.n, p->desc.k, p->desc.group_k, pi);
@@ -552,7 +550,12 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
     if (t.ksplit > 1 && !launch_split_reduce(a, false, false, pi.of, (hipStream_t)stream)) return QG_ERR_UNSUPPORTED;
     return launched();
   }
-  if (!dense_streams(pi, m, p->desc.n, p->desc.k)) {
+  if (pi.af == A_INT8 && int8_rows(m, p->desc.n, p->desc.k)) {
+    QG_LOG("gemm m=%lld n=%lld k=%lld -> int8 rows", (long long)m, (long long)p->desc.n, (long long)p->desc.k);
+    if (!launch_rows_gemm_int8(a, pi.of, (hipStream_t)stream)) return QG_ERR_UNSUPPORTED;
+    return launched();
+  }
+  if (!dense_streams(pi, m)) {
     const MfmaTile t = mfma_tile(m, p->desc.n, p->desc.k, p->desc.group_k, pi);
     if (t.ksplit > 1) {
       const size_t need = (size_t)t.ksplit * (size_t)m * (size_t)p->desc.n * sizeof(float);
@@ -571,8 +574,7 @@ qg_status qg_gemm(const qg_prepared* p, const void* x, const void* x_scale, void
     return launched();
   }
   StreamTile t = stream_tile(m, p->desc.n, byte_weights(&p->desc));
-  const int sp = pi.af == A_INT8 ? 1 : stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
-  if (pi.af == A_INT8 && int8_wide(m, p->desc.n, p->desc.k)) stream_shape(t, p->desc.n, 2, 4);
+  const int sp = stream_split(m, p->desc.n, p->desc.k, p->desc.group_k);
   if (sp > 1) {
     const size_t need = dense_workspace(p, pi, m);
     if (!ws || !aligned16(ws) || ws_bytes < need) return QG_ERR_WORKSPACE;

@@ -45,6 +45,9 @@ struct MfmaTile {
 bool launch_mfma_gemm(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int of, int stype, bool zero, bool moe,
                       hipStream_t st);
 
+// int8 products of up to 64 dense rows.
+bool launch_rows_gemm_int8(const MfmaArgs& a, int of, hipStream_t st);
+
 // Sum of the split-K partials a.part[ksplit][m][n] into a.y, with the e4m3 per-channel
 // (w_scale, fp8 weights) and per-token (a.x_scale, e4m3 activations) scales.  whole: the partials
 // are 32-bit integers (int8 products; both scales).

@@ -1,4 +1,4 @@
-// Weight-streaming GEMM instantiations: int8 weights with int8 activations.
+// Weight-streaming GEMM instantiations: int8 weights with int8 activations (MoE blocks).
 #include "qg_stream_kernel.h"
 
 namespace qg {

@@ -498,10 +498,7 @@ static bool launch_shape(const StreamArgs& a, const StreamTile& t, hipStream_t s
     case 0: launch_one<WP, AF, OF, ST, ZERO, 0, NCB, KQ, MOE>(a, t, st); return true;
     case 1: launch_one<WP, AF, OF, ST, ZERO, 1, NCB, KQ, MOE>(a, t, st); return true;
     case 2: launch_one<WP, AF, OF, ST, ZERO, 2, NCB, KQ, MOE>(a, t, st); return true;
-    case 4:
-      if constexpr (WP == WP_INT8 && !MOE) return false;   // dense int8: at most 32 rows
-      else launch_one<WP, AF, OF, ST, ZERO, 4, NCB, KQ, MOE>(a, t, st);
-      return true;
+    case 4: launch_one<WP, AF, OF, ST, ZERO, 4, NCB, KQ, MOE>(a, t, st); return true;
     default: return false;
   }
 }
@@ -510,13 +507,9 @@ template <int WP, int AF, int OF, int ST, bool ZERO, bool MOE>
 static bool launch_mt(const StreamArgs& a, const StreamTile& t, hipStream_t st) {
   if constexpr (WP == WP_INT8) {
     // MoE blocks: 4 column blocks x 2 K parts (E = 64 top-6, N = 2816, K = 4096, 64 / 200 tokens: 113 /
-    // 122 us; 1 x 8 172 / 236, 2 x 4 114 / 159, 8 x 1 125 / -)
-    if constexpr (MOE) {
+    // 122 us; 1 x 8 172 / 236, 2 x 4 114 / 159, 8 x 1 125 / -); dense rows have a kernel of their own
+    if constexpr (MOE)
       if (t.ncb == 4 && t.kq == 2) return launch_shape<WP, AF, OF, ST, ZERO, MOE, 4, 2>(a, t, st);
-    } else if (t.mt <= 2) {
-      if (t.ncb == 1 && t.kq == 8) return launch_shape<WP, AF, OF, ST, ZERO, MOE, 1, 8>(a, t, st);
-      if (t.ncb == 2 && t.kq == 4) return launch_shape<WP, AF, OF, ST, ZERO, MOE, 2, 4>(a, t, st);
-    }
   } else if constexpr (StreamTraits<WP, AF>::kBytes) {
     if (t.ncb == 1 && t.kq == 8) return launch_shape<WP, AF, OF, ST, ZERO, MOE, 1, 8>(a, t, st);
     if constexpr (!MOE)

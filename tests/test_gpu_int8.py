@@ -85,7 +85,7 @@ def test_prepare_and_read_back_are_exact():
 # rows around every tile height and the largest drawn, columns that end inside a tile, reductions of
 # one step, of an odd number of steps and of many
 @pytest.mark.parametrize("n,k,out", [(64, 128, "bf16"), (192, 768, "f16"), (320, 1408, "bf16"), (1856, 1408, "f16"),
-                                     (256, 4096, "bf16"), (576, 8192, "bf16")])
+                                     (256, 4096, "bf16"), (576, 8192, "bf16"), (6208, 896, "f16")])
 def test_dense_is_exact_for_every_row_count(n, k, out):
     ms = [1, 2, 3, 4, 5, 8, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 100, 127, 128, 129, 200, 255, 257, 300, 513]
     layer, acts = synth.dense_w8a8_int8(m=max(ms), n=n, k=k, out=out, seed=n + k)
@@ -189,15 +189,15 @@ def test_noalloc_and_another_stream(m):
 
 
 def test_missing_or_small_workspace_is_refused():
-    layer, acts = synth.dense_w8a8_int8(m=64, n=512, k=4096, seed=1)
+    layer, acts = synth.dense_w8a8_int8(m=200, n=512, k=4096, seed=1)
     p, buf = layers.prepare_layer(layer)
     x, xs = layers.acts_to_dev(acts)
-    need = qg.workspace_bytes(p, 64)
+    need = qg.workspace_bytes(p, 200)
     assert need > 0
-    y = torch.full((64, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    y = torch.full((200, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
     for ws in (None, torch.empty(need - 16, dtype=torch.uint8, device="cuda")):
         with pytest.raises(qg.QGError) as e:
-            qg.gemm(p, x, xs, y, 64, ws)
+            qg.gemm(p, x, xs, y, 200, ws)
         assert e.value.status == 5
     torch.cuda.synchronize()
     assert torch.isnan(y).all()
@@ -501,23 +501,24 @@ def test_int8_layer_captured_and_replayed():
             assert torch.equal(b[name], eager[name]), (k, name)
 
 
-def test_two_captured_products_replayed_with_their_own_workspaces():
-    layer, acts = synth.dense_w8a8_int8(m=64, n=1024, k=4096, seed=9)
+@pytest.mark.parametrize("m", [64, 200])
+def test_two_captured_products_replayed_with_their_own_workspaces(m):
+    layer, acts = synth.dense_w8a8_int8(m=m, n=1024, k=4096, seed=9)
     p, buf = layers.prepare_layer(layer)
     x, xs = layers.acts_to_dev(acts)
-    need = qg.workspace_bytes(p, 64)
+    need = qg.workspace_bytes(p, m)
     graphs, s = [], torch.cuda.Stream()
     for i in range(2):
         xi = torch.roll(x, i, 0).contiguous()
         xsi = torch.roll(xs, i, 0).contiguous()
-        y = torch.empty((64, 1024), dtype=torch.bfloat16, device="cuda")
+        y = torch.empty((m, 1024), dtype=torch.bfloat16, device="cuda")
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
-        qg.gemm(p, xi, xsi, y, 64, ws, stream=s)
+        qg.gemm(p, xi, xsi, y, m, ws, stream=s)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
-            qg.gemm(p, xi, xsi, y, 64, ws, stream=s)
+            qg.gemm(p, xi, xsi, y, m, ws, stream=s)
         graphs.append((g, y, xi, xsi, ws))
     want = _want(acts.x, acts.x_scale, layer.w[0], layer.s[0, :, 0], "bf16")
     for _ in range(3):
