@@ -345,6 +345,26 @@ def test_quantize_int8_rows_is_bit_exact(rows, k, dtype):
     assert np.array_equal(codes, rc), f"{np.count_nonzero(codes != rc)} codes differ"
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quantize_int8_rows_over_the_whole_range(dtype):
+    # every finite value up to a row's largest, for largest values over the whole range: subnormal, ordinary,
+    # near the type's largest, with scales that float32 rounds either way
+    rng = np.random.default_rng(7)
+    top = 0x7F80 if dtype == "bf16" else 0x7C00                             # first bits that are not finite
+    tops = np.concatenate([rng.integers(1, top, 90), [1, 2, 126, 127, 128, top - 1, top - 2, top // 2]])
+    k = 32768
+    rows = len(tops)
+    bits = np.empty((rows, k), np.uint16)
+    for r, t in enumerate(tops):
+        near = rng.integers(max(0, int(t) - 9 * 128), int(t) + 1, k)         # the last few octaves: codes that are not 0
+        bits[r] = np.where(rng.random(k) < 0.7, near, rng.integers(0, int(t) + 1, k)) | (rng.integers(0, 2, k) << 15)
+        bits[r, int(t) % k] = t
+    codes, scale = _quant_gpu(_dev16(bits), rows, k, lambda x, c, s: qg.quantize_int8_rows(x, rows, k, Q_ACT[dtype], c, s))
+    rc, rs = Q.absmax_int8_rows(F.decode_act(bits, dtype).astype(np.float32))
+    assert np.array_equal(scale.view(np.uint32), rs.view(np.uint32))
+    assert np.array_equal(codes, rc), f"{np.count_nonzero(codes != rc)} codes differ, rows {np.unique(np.nonzero(codes != rc)[0])}"
+
+
 @pytest.mark.parametrize("rows,inter,dtype", [(6, 64, "bf16"), (11, 1408, "bf16"), (3, 8192, "f16"), (2, 16384, "bf16")])
 def test_swiglu_int8_is_bit_exact_on_exact_activations(rows, inter, dtype):
     # gate = 32: silu(32) rounds to 32 in float32 and from float64, so act = 32 * up on both sides
