@@ -276,7 +276,7 @@ def test_grouped_is_exact_for_every_block(bm, t, n, k, out):
 @pytest.mark.parametrize("flag", [0, qg.C_BATCH_INVARIANT])
 @pytest.mark.parametrize("t", [1, 9, 64, 500, 2000])
 def test_grouped_with_the_chosen_block(t, flag):
-    experts, topk, n, k = 16, 4, 256, 512
+    experts, topk, n, k = 16, 4, 256, 512          # blocks of 4, 16, 16, 64 and 128 rows
     layer, acts = synth.moe_w8a8_int8(t=t, experts=experts, topk=topk, n=n, k=k, seed=t)
     p, buf = layers.prepare_layer(layer, compute_flags=flag)
     bm = qg.moe_block_m(p, t, topk)
