@@ -6,7 +6,8 @@ library's HIP kernels.  The entry points mirror include/qg.h one to one:
 ``prepared_bytes``, ``prepare``, ``workspace_bytes``, ``gemm``, ``moe_block_m``,
 ``moe_capacity``, ``moe_align``, ``moe_grouped_map``, ``moe_gemm``, ``moe_swiglu``,
 ``moe_combine``, ``moe_route``, ``quantize_e4m3_rows``, ``quantize_int8_rows``,
-``quantize_e2m1_rows``, ``dequant``, ``status_str``, ``version`` and the measurement helpers ``ceiling_read`` and ``ceiling_mfma``.
+``quantize_e2m1_rows``, ``dequant``, ``status_str``, ``version`` and the measurement helpers
+``ceiling_read`` and ``ceiling_mfma``.
 
 There is no fallback: if libqg.so is missing or cannot be loaded, every call raises.
 """

@@ -312,7 +312,7 @@ MfmaTile int8_tile(int64_t rows, int64_t n, int64_t k) {
 // int8 MoE blocks: 16-, 32- or 64-row streaming blocks or 128-row MFMA blocks, whichever is estimated to
 // take least.  A streaming workgroup (64 columns) by itself takes lat0 + lat us per K step, and wg0 + wg ns
 // per K step of a full GPU's time; the weights arrive at 6.5 TB/s; 128-row tiles as above, their weights at
-// 5.7 TB/s.  Routed rows are taken as spread evenly, an expert's last block half full.  Over 52
+// 5.7 TB/s.  Routed rows are taken as spread evenly, an expert's last block half full.  Over 54
 // measured products (2 to 64 experts, means of 6 to 750 rows) its choice is within 1% of the best on
 // average, 14% at most; blocks by the mean alone lose where tiles are few: E = 4, N = 1024, K = 2048, a mean
 // of 32 rows 5.5 us with 16-row blocks, 14.5 with 128; E = 16, N = 512, K = 1024, 100 rows 8.6 with 64, 11.3
