@@ -227,13 +227,18 @@ void stream_shape(StreamTile& t, int64_t n, int ncb, int kq) {
 // (us with 3 / 16 sets of weights in turn, of which the first stay in the last-level cache: N = K = 7168, 8
 // rows 9.2 / 9.6 against 12.1 / 14.4, 32 rows 10.3 / 12.8 against 13.0 / 15.3; N = 1024, K = 8192, 16 rows 4.8 /
 // 4.9 against 6.3 / 6.8); few columns leave CUs idle then, which K split over workgroups uses, so with long
-// K those win (N = 2048, K = 14336, 32 rows 9.5 / 14.7 against 10.1 / 13.1).  To 64 rows while
-// activations are no more of what a CU loads than the weights it can wait for (64 rows: N = K = 4096 7.4 /
-// 8.4 against 9.1 / 10.2, N = K = 7168 12.1 / 17.2 against 14.5 / 17.3, N = 2048, K = 14336 14.3 / 21 against
-// 11.1 / 14.7) and the columns are one round of workgroups (N = 14336, K = 4096 16.5 / 20.6 against 12.2 / 20.7).
+// K those win (N = 2048, K = 14336, 32 rows 9.5 / 14.7 against 10.1 / 13.1).  Above, while one round of
+// workgroups of 64 rows holds them, K is short enough for a CU that loads the activations of all of it (64
+// rows: N = K = 4096 7.4 / 8.4 against 9.1 / 10.2, N = K = 7168 12.1 / 17.2 against 14.5 / 17.3, N = 2048, K = 14336
+// 14.3 / 21 against 11.1 / 14.7) and long enough for its waves' steps in turn to pay (128 rows: N = K = 4096 8.7 /
+// 10.1 against 11.1 / 15.8, N = K = 7168 15.0 / 21.4 against 17.7 / 27.7, N = 7168, K = 2048 8.7 / 9.6 against 7.7 /
+// 9.9; 300 rows, N = 192: K = 640 4.2 against 4.1, K = 2048 4.9 against 7.3).
 bool int8_rows(int64_t rows, int64_t n, int64_t k) {
   if (rows <= 32) return n > 4096 || (16 + (rows <= 8 ? 8 : rows <= 16 ? 16 : 32)) * k <= 3 << 18;
-  return rows <= 64 && n <= 8192 && k <= (n > 4096 ? 8192 : 6528);
+  if (rows <= 64) return n <= 8192 && k <= (n > 4096 ? 8192 : 6528);
+  const int64_t cols = (rows + 63) / 64 * n;   // of all row tiles: 16, 32 or 64 per workgroup
+  if (cols <= 4096) return k >= 1024 && k <= 6528;
+  return cols <= 16384 && k >= (cols <= 8192 ? 2048 : 4096) && k <= 8192;
 }
 
 // MFMA-bound family: rows per tile 256 while that still leaves about 1.5 workgroups per

@@ -45,7 +45,7 @@ struct MfmaTile {
 bool launch_mfma_gemm(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int of, int stype, bool zero, bool moe,
                       hipStream_t st);
 
-// int8 products of up to 64 dense rows.
+// int8 products of few dense rows, 64 per workgroup.
 bool launch_rows_gemm_int8(const MfmaArgs& a, int of, hipStream_t st);
 
 // Sum of the split-K partials a.part[ksplit][m][n] into a.y, with the e4m3 per-channel

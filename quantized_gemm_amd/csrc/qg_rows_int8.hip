@@ -1,9 +1,9 @@
-// int8 x int8 product of up to 64 rows: the weights are read once, past few rows of activations.
+// int8 x int8 product of few rows: the weights are read once, or once per 64 rows, past the activations.
 //
 //   sum[m][n] = sum_k x[m][k] w[n][k] in 32-bit integers, y = out(float(sum) * sw[n] * sx[m]).
 //
 // Bound by reading the weights, and by what a CU loads (about 65 bytes per ns), of which every workgroup's
-// copy of the activations is a part.  A workgroup takes all rows x CW columns, and its waves take the
+// copy of the activations is a part.  A workgroup takes up to 64 rows x CW columns, and its waves take the
 // 128-wide K steps in turn: a wave shares nothing with the others until the end, so the loop has no
 // barrier, only waits for its own loads.  Activations go HBM -> LDS (buffer_load ... lds) into the
 // wave's own ring of four stages, 16-byte chunks XOR-swizzled by row bits 1..3; weights go HBM -> VGPR,
@@ -12,7 +12,7 @@
 //
 // Measured with 3 / 16 sets of weights in turn, of which the first stay in the 256 MB last-level cache:
 // N = K = 7168, 1 row 9.0 / 9.6 us (5.7 / 5.4 TB/s of weights), 16 rows 10.0 / 10.3, 32 rows 10.3 / 12.8,
-// 64 rows 12.1 / 17.2; N = K = 4096, 1 row 4.0 / 4.7, 64 rows 7.4 / 8.4.
+// 64 rows 12.1 / 17.2, 128 rows 15.0 / 21.4; N = K = 4096, 1 row 4.0 / 4.7, 64 rows 7.4 / 8.4, 128 rows 8.7 / 10.1.
 #include <type_traits>
 
 #include "qg_device.h"
@@ -25,17 +25,18 @@ namespace {
 constexpr int kParts = 4;             // waves (8: N = K = 4096, 16 rows 4.6 -> 4.7 us, N = K = 7168 10.3 -> 10.9)
 
 // RB: rows staged (8, 16, 32 or 64; those that fill no MFMA tile repeat others and are left out at the
-// end), CW: columns (32 or 16, the MFMA tile), NTW: non-temporal weight loads
+// end), CW: columns (16, 32 or 64, by MFMA tiles of 16 or 32), NTW: non-temporal weight loads
 template <int OF, int RB, int CW, bool NTW>
 __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   constexpr int KP = kParts;
-  constexpr int MT = RB > CW ? RB / CW : 1;                        // row tiles
-  constexpr int TR = RB < CW ? RB : CW;                            // rows of a tile that are staged
-  constexpr int G = 64 / CW, KJ = 8 / G;                           // 16-byte chunks of K per MFMA, MFMAs per step
+  constexpr int TW = CW < 32 ? CW : 32, NT = CW / TW;              // MFMA tile, column tiles
+  constexpr int MT = RB > TW ? RB / TW : 1;                        // row tiles
+  constexpr int TR = RB < TW ? RB : TW;                            // rows of a tile that are staged
+  constexpr int G = 64 / TW, KJ = 8 / G;                           // 16-byte chunks of K per MFMA, MFMAs per step
   constexpr int AP = RB / 8;                                       // 16-byte activation pieces per lane and step
   constexpr int ROWB = 128;                                        // bytes of a row per step
   constexpr int STAGE = RB * ROWB;                                 // per wave
-  constexpr int LOADS = AP + KJ;                                   // per step
+  constexpr int LOADS = AP + KJ * NT;                              // per step
   __shared__ __attribute__((aligned(16))) uint8_t sA0[KP * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t sA1[KP * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t sA2[KP * STAGE];
@@ -44,8 +45,14 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   __shared__ __attribute__((aligned(16))) float sColScale[64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & (CW - 1), g = lane / CW;
-  const int col0 = (int)blockIdx.x * CW;
+  const int r = lane & (TW - 1), g = lane / TW;
+  // (rows past RB: further row tiles, those of the same columns on the same XCD)
+  int mtile = 0, ntile = (int)blockIdx.x;
+  if (RB == 64 && a.m > RB) {
+    const int mtiles = (int)((a.m + RB - 1) / RB);
+    xcd_tile(blockIdx.x, mtiles, (int)gridDim.x / mtiles, (int64_t)RB * a.k, (int64_t)CW * a.k, mtile, ntile);
+  }
+  const int row0 = mtile * RB, col0 = ntile * CW;
   const int nsteps = a.k / ROWB;
   const int cnt = (nsteps - wave + KP - 1) / KP;                   // this wave's steps: wave, wave + KP, ...
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w, (uint32_t)a.w_expert_bytes);
@@ -55,18 +62,22 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
 #pragma unroll
   for (int i = 0; i < AP; ++i) {
     const int p = lane + 64 * i, row = p >> 3;
-    a_off[i] = row < a.m ? row * a.k + 16 * ((p & 7) ^ ((row >> 1) & 7)) : -1;
+    a_off[i] = row0 + row < a.m ? (row0 + row) * a.k + 16 * ((p & 7) ^ ((row >> 1) & 7)) : -1;
   }
-  const int b_off = (int)(((int64_t)((col0 + r) >> 4) * (a.k >> 4) + g) * 256 + (r & 15) * 16);
+  int b_off[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    b_off[t] = (int)(((int64_t)((col0 + TW * t + r) >> 4) * (a.k >> 4) + g) * 256 + (r & 15) * 16);
   // the scales, for the end
-  if (wave == 0) bload4_lds(make_rsrc(a.x_scale, (uint32_t)(a.m * 4)), sRowScale, lane < a.m ? 4 * lane : kOOB);
+  if (wave == 0) bload4_lds(make_rsrc(a.x_scale, (uint32_t)(a.m * 4)), sRowScale,
+                            lane < RB && row0 + lane < a.m ? 4 * (row0 + lane) : kOOB);
   if (wave == 1) bload4_lds(make_rsrc((const float*)a.s + col0, 4 * CW), sColScale, lane < CW ? 4 * lane : kOOB);
   __builtin_amdgcn_sched_barrier(0);
 
   auto stg = [&](int i) __attribute__((always_inline)) -> uint8_t* {
     return (i == 0 ? sA0 : i == 1 ? sA1 : i == 2 ? sA2 : sA3) + wave * STAGE;
   };
-  i32x4 B[4][KJ];
+  i32x4 B[4][KJ][NT];
   // (past the end: zeros)
   auto load = [&](int i, auto S_) __attribute__((always_inline)) {
     constexpr int S = decltype(S_)::value;
@@ -76,15 +87,19 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
       bload16_lds(xr, stg(S) + 1024 * c, a_off[c] < 0 || i >= cnt ? kOOB : a_off[c] + step * ROWB);
 #pragma unroll
     for (int j = 0; j < KJ; ++j)
-      B[S][j] = __builtin_bit_cast(i32x4, bload16_s<NTW>(wr, i >= cnt ? kOOB : b_off, step * 2048 + 256 * G * j));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        B[S][j][t] = __builtin_bit_cast(i32x4, bload16_s<NTW>(wr, i >= cnt ? kOOB : b_off[t], step * 2048 + 256 * G * j));
     __builtin_amdgcn_sched_barrier(0);
   };
-  using Acc = std::conditional_t<CW == 32, i32x16, i32x4>;
-  Acc acc[MT];
+  using Acc = std::conditional_t<TW == 32, i32x16, i32x4>;
+  Acc acc[MT][NT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int i = 0; i < CW * CW / 64; ++i) acc[mt][i] = 0;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < TW * TW / 64; ++i) acc[mt][t][i] = 0;
   load(0, std::integral_constant<int, 0>{});
   load(1, std::integral_constant<int, 1>{});
   load(2, std::integral_constant<int, 2>{});
@@ -97,10 +112,13 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
     for (int j = 0; j < KJ; ++j)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int row = CW * mt + (r & (TR - 1));
+        const int row = TW * mt + (r & (TR - 1));
         const i32x4 A = *(const i32x4*)(st + row * ROWB + 16 * ((G * j + g) ^ ((row >> 1) & 7)));
-        if constexpr (CW == 32) acc[mt] = mfma32x32x32_i8(B[S][j], A, acc[mt]);
-        else acc[mt] = mfma16x16x64_i8(__builtin_bit_cast(u32x4, B[S][j]), __builtin_bit_cast(u32x4, A), acc[mt]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if constexpr (TW == 32) acc[mt][t] = mfma32x32x32_i8(B[S][j][t], A, acc[mt][t]);
+          else acc[mt][t] = mfma16x16x64_i8(__builtin_bit_cast(u32x4, B[S][j][t]), __builtin_bit_cast(u32x4, A), acc[mt][t]);
+        }
       }
     __builtin_amdgcn_sched_barrier(0);
     load(i + 4, S_);
@@ -117,21 +135,23 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   if (i + 2 < cnt) step(i + 2, std::integral_constant<int, 2>{});
   wait_loads<0>();
 
-  // Each wave's sums into its first stage, 16-byte pieces XOR-swizzled by the row: with the weights as
-  // the MFMAs' first operand lane (r, g) holds columns 4 (G q + g) .. of row r.
-  constexpr int PPR = CW / 4;                                      // pieces per row
+  // Each wave's sums into its first stages, one per column tile, 16-byte pieces XOR-swizzled by the row: with
+  // the weights as the MFMAs' first operand lane (r, g) holds columns 4 (G q + g) .. of row r.
+  constexpr int PPR = TW / 4;                                      // pieces per row of a tile
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int q = 0; q < PPR / G; ++q)
-      if (r < TR)
-        *(i32x4*)(stg(0) + 16 * (PPR * (CW * mt + r) + ((G * q + g) ^ (r & (PPR - 1))))) =
-            i32x4{acc[mt][4 * q], acc[mt][4 * q + 1], acc[mt][4 * q + 2], acc[mt][4 * q + 3]};
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < PPR / G; ++q)
+        if (r < TR)
+          *(i32x4*)(stg(t) + 16 * (PPR * (TW * mt + r) + ((G * q + g) ^ (r & (PPR - 1))))) =
+              i32x4{acc[mt][t][4 * q], acc[mt][t][4 * q + 1], acc[mt][t][4 * q + 2], acc[mt][t][4 * q + 3]};
   __syncthreads();
-  for (int p = tid; p < RB * PPR; p += 64 * KP) {
-    const int row = p / PPR, c = p % PPR;                          // piece c of the row: columns 4 c ..
-    if (row >= a.m) break;
-    const uint8_t* src = sA0 + 16 * (PPR * row + (c ^ (row & (PPR - 1))));
+  for (int p = tid; p < RB * PPR * NT; p += 64 * KP) {
+    const int row = p / (PPR * NT), c = p % (PPR * NT);            // piece c of the row: columns 4 c ..
+    if (row0 + row >= a.m) break;
+    const uint8_t* src = (NT == 1 || c < PPR ? sA0 : sA1) + 16 * (PPR * row + ((c & (PPR - 1)) ^ (row & (PPR - 1))));
     i32x4 v = *(const i32x4*)src;
 #pragma unroll
     for (int w = 1; w < KP; ++w) v += *(const i32x4*)(src + w * STAGE);
@@ -140,34 +160,39 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
     u32x2 o;
     o[0] = scaled_out2<OF>(v[0], v[1], sw[0], sw[1], sx);
     o[1] = scaled_out2<OF>(v[2], v[3], sw[2], sw[3], sx);
-    *(u32x2*)((uint16_t*)a.y + (int64_t)row * a.n + col0 + 4 * c) = o;
+    *(u32x2*)((uint16_t*)a.y + (int64_t)(row0 + row) * a.n + col0 + 4 * c) = o;
   }
 }
 
 template <int OF, int RB, int CW>
 void launch_one(const MfmaArgs& a, bool ntw, hipStream_t st) {
-  const dim3 grid(a.n / CW), block(64 * kParts);
+  const dim3 grid((unsigned)(a.n / CW * ((a.m + RB - 1) / RB))), block(64 * kParts);
   if (ntw) hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, false>), grid, block, 0, st, a);
 }
 
 // 16 columns while they are at most one workgroup per CU, else 32, which load the activations half as
 // often (16 rows, 16 / 32 columns: N = K = 4096 4.6 / 4.9 us, N = 2048, K = 14336 7.2 / 9.6; N = K = 5120 7.1 /
-// 6.2, N = K = 7168 11.5 / 10.0).
+// 6.2, N = K = 7168 11.5 / 10.0), and 64 for several row tiles when 32 are more than one round.
 template <int OF, int RB>
 void launch_width(const MfmaArgs& a, bool ntw, hipStream_t st) {
-  if (a.n <= 4096) launch_one<OF, RB, 16>(a, ntw, st);
-  else launch_one<OF, RB, 32>(a, ntw, st);
+  const int64_t tiles = (a.m + RB - 1) / RB * a.n;
+  if (tiles <= 4096) return launch_one<OF, RB, 16>(a, ntw, st);
+  if constexpr (RB == 64) {
+    if (tiles > 8192) return launch_one<OF, RB, 64>(a, ntw, st);
+  }
+  launch_one<OF, RB, 32>(a, ntw, st);
 }
 
 // Weights past the caches where they are too many to stay there from one call to the next and activations
 // are few (N = K = 7168, 3 / 16 sets of weights in turn, past / through: 5 rows 8.9 / 9.5 against 9.1 / 10.5 us,
 // 16 rows 9.9 / 10.3 against 9.6 / 11.0; 64 rows 15.2 / 15.7 against 12.2 / 17.1; N = 8192, K = 14336, 32 rows
-// 22.2 / 22.5 against 23.3 / 23.7; N = K = 4096, 5 rows 5.4 / 5.6 against 4.4 / 5.4).
+// 22.2 / 22.5 against 23.3 / 23.7; N = K = 4096, 5 rows 5.4 / 5.6 against 4.4 / 5.4); through them where several
+// row tiles read them (N = K = 8192, 128 rows 23.7 / 23.7 against 18.3 / 24.9).
 template <int OF>
 void launch_rows(const MfmaArgs& a, hipStream_t st) {
   const int64_t bytes = a.w_expert_bytes;
-  const bool ntw = bytes >= (a.m <= 16 ? (int64_t)1 << 25 : (int64_t)1 << 26);
+  const bool ntw = a.m <= 64 && bytes >= (a.m <= 16 ? (int64_t)1 << 25 : (int64_t)1 << 26);
   if (a.m <= 8) launch_width<OF, 8>(a, ntw, st);
   else if (a.m <= 16) launch_width<OF, 16>(a, ntw, st);
   else if (a.m <= 32) launch_width<OF, 32>(a, ntw, st);
@@ -177,7 +202,6 @@ void launch_rows(const MfmaArgs& a, hipStream_t st) {
 }  // namespace
 
 bool launch_rows_gemm_int8(const MfmaArgs& a, int of, hipStream_t st) {
-  if (a.m > 64) return false;
   if (of == O_BF16) launch_rows<O_BF16>(a, st);
   else if (of == O_F16) launch_rows<O_F16>(a, st);
   else return false;

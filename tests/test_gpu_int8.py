@@ -119,7 +119,8 @@ def test_dense_full_size_is_exact(m):
 @pytest.mark.parametrize("m,n,k", [(40, 8256, 640), (260, 8320, 1408), (257, 7168, 640), (200, 8256, 896), (513, 4160, 768),
                                    (1224, 1600, 512), (1000, 7168, 896), (2500, 1856, 1408), (1500, 10304, 896),
                                    (4000, 7168, 640), (668, 704, 23040), (300, 576, 4096), (65, 4160, 4096),
-                                   (33, 1856, 8192)])
+                                   (33, 1856, 8192), (300, 192, 2048), (777, 64, 1152), (200, 1856, 2176), (777, 1024, 4096),
+                                   (130, 4160, 4224), (128, 8192, 8192), (500, 512, 8320)])
 def test_every_tile_is_exact(m, n, k, out):
     layer, acts = synth.dense_w8a8_int8(m=m, n=n, k=k, out=out, seed=m + n + k)
     p, buf = layers.prepare_layer(layer)
@@ -173,9 +174,9 @@ def test_rows_do_not_depend_on_the_call():
         assert np.array_equal(_got(_run(pi, x, xs, m, 1024, "bf16")), whole[:m])
 
 
-@pytest.mark.parametrize("m", [16, 64, 200])
-def test_noalloc_and_another_stream(m):
-    layer, acts = synth.dense_w8a8_int8(m=m, n=1024, k=4096, seed=m)
+@pytest.mark.parametrize("m,k", [(16, 4096), (64, 4096), (200, 4096), (200, 8192)])
+def test_noalloc_and_another_stream(m, k):
+    layer, acts = synth.dense_w8a8_int8(m=m, n=1024, k=k, seed=m)
     p, buf = layers.prepare_layer(layer)
     x, xs = layers.acts_to_dev(acts)
     want = _want(acts.x, acts.x_scale, layer.w[0], layer.s[0, :, 0], "bf16")
@@ -189,7 +190,7 @@ def test_noalloc_and_another_stream(m):
 
 
 def test_missing_or_small_workspace_is_refused():
-    layer, acts = synth.dense_w8a8_int8(m=200, n=512, k=4096, seed=1)
+    layer, acts = synth.dense_w8a8_int8(m=200, n=512, k=8192, seed=1)
     p, buf = layers.prepare_layer(layer)
     x, xs = layers.acts_to_dev(acts)
     need = qg.workspace_bytes(p, 200)
@@ -220,11 +221,12 @@ def test_no_rows():
 
 def test_two_streams_at_once():
     # two products in flight together, each with its own workspace and outputs
-    layer, acts = synth.dense_w8a8_int8(m=200, n=1024, k=4096, seed=12)
+    layer, acts = synth.dense_w8a8_int8(m=200, n=1024, k=8192, seed=12)
     p, buf = layers.prepare_layer(layer)
     x, xs = layers.acts_to_dev(acts)
     want = _want(acts.x, acts.x_scale, layer.w[0], layer.s[0, :, 0], "bf16")
-    need = max(qg.workspace_bytes(p, 64), qg.workspace_bytes(p, 200), 16)
+    need = max(qg.workspace_bytes(p, 64), qg.workspace_bytes(p, 200))
+    assert need > 0
     streams = [torch.cuda.Stream() for _ in range(2)]
     ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
     ys = [[torch.full((m, 1024), float("nan"), dtype=torch.bfloat16, device="cuda") for m in (64, 200)] for _ in range(2)]
@@ -521,9 +523,9 @@ def test_int8_layer_captured_and_replayed():
             assert torch.equal(b[name], eager[name]), (k, name)
 
 
-@pytest.mark.parametrize("m", [64, 200])
-def test_two_captured_products_replayed_with_their_own_workspaces(m):
-    layer, acts = synth.dense_w8a8_int8(m=m, n=1024, k=4096, seed=9)
+@pytest.mark.parametrize("m,k", [(64, 4096), (200, 4096), (200, 8192)])
+def test_two_captured_products_replayed_with_their_own_workspaces(m, k):
+    layer, acts = synth.dense_w8a8_int8(m=m, n=1024, k=k, seed=9)
     p, buf = layers.prepare_layer(layer)
     x, xs = layers.acts_to_dev(acts)
     need = qg.workspace_bytes(p, m)
