@@ -414,6 +414,57 @@ def test_more_rows_than_one_launch_takes():
     assert torch.equal(act[:rows], first.repeat(reps, 1)[:rows]) and (act[rows] == 77).all()
 
 
+# ---- sizes past 32 bits ------------------------------------------------------------------------
+
+def test_outputs_past_2_31_elements():
+    m, n, k = 1_060_000, 2048, 256                                       # 2.17e9 outputs
+    layer, _ = synth.dense_w8a8_int8(m=1, n=n, k=k, seed=4)
+    p, buf = layers.prepare_layer(layer)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(-127, 128, (m, k), generator=gen, device="cuda", dtype=torch.int8)
+    xs = torch.rand(m, generator=gen, device="cuda") + 0.5
+    y = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    qg.gemm(p, x, xs, y, m)
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 1, 524_287, 1_048_575, 1_048_576, 1_048_577, m - 257, m - 1])
+    want = _want(x[rows.cuda()].cpu().numpy(), xs[rows.cuda()].cpu().numpy(), layer.w[0], layer.s[0, :, 0], "bf16")
+    assert np.array_equal(_got(y[rows.cuda()]), want)
+
+
+@pytest.mark.parametrize("bm", [16, 128])
+def test_expert_weights_past_2_32_bytes(bm):
+    experts, n, k, t = 40, 7168, 16384, 40                                # 4.7e9 bytes
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.randint(-127, 128, (experts, n, k), generator=gen, device="cuda", dtype=torch.int8)
+    sw = torch.rand((experts, n, 1), generator=gen, device="cuda") * 1e-4
+    desc = qg.make_desc(qg.W_INT8, qg.S_F32, 0, 0, qg.A_INT8, qg.C_NATIVE, qg.O_BF16, experts, n, k)
+    img = torch.empty(qg.prepared_bytes(desc), dtype=torch.uint8, device="cuda")
+    p = qg.prepare(desc, w, sw, None, img)
+    x = torch.randint(-127, 128, (t, k), generator=gen, device="cuda", dtype=torch.int8)
+    xs = torch.rand(t, generator=gen, device="cuda") + 0.5
+    ids = np.arange(t, dtype=np.int32).reshape(t, 1) % experts
+    y = torch.empty((t, n), dtype=torch.bfloat16, device="cuda")
+    qg.moe_gemm(p, x, xs, *_align(ids, experts, bm), t, 1, bm, y)
+    torch.cuda.synchronize()
+    for e in (0, 18, 36, 37, 39):                                         # 36 * n * k < 2^32 < 37 * n * k
+        want = _want(x[e:e + 1].cpu().numpy(), xs[e:e + 1].cpu().numpy(), w[e].cpu().numpy(), sw[e, :, 0].cpu().numpy(), "bf16")
+        assert np.array_equal(_got(y[e:e + 1]), want), e
+
+
+def test_quantized_rows_past_2_31_elements():
+    rows, k = 66_000, 32768                                               # 2.16e9 values
+    bits, _ = synth.act_rows(500, k, "bf16", sigma=3.0, seed=9)
+    x = _dev16(bits).repeat(rows // 500, 1)
+    codes = torch.empty((rows, k), dtype=torch.int8, device="cuda")
+    scale = torch.empty(rows, device="cuda")
+    qg.quantize_int8_rows(x, rows, k, qg.A_BF16, codes, scale)
+    torch.cuda.synchronize()
+    rc, rs = Q.absmax_int8_rows(F.decode_bf16(bits).astype(np.float32))
+    for first in (0, 65_000, 65_500):                                     # 65536 * k = 2^31
+        assert np.array_equal(codes[first:first + 500].cpu().numpy(), rc)
+        assert np.array_equal(scale[first:first + 500].cpu().numpy(), rs)
+
+
 # ---- a whole layer -----------------------------------------------------------------------------
 
 def _layer_buffers(t, topk, experts, up, down, pu, pd):

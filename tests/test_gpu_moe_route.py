@@ -217,6 +217,45 @@ def test_more_tokens_than_one_launch_takes(scoring):
     _check(v, "f32", scoring, 2, bias=np.array([0.1, 0, -0.1, 0.3]), renorm=True, total=t)
 
 
+def test_logits_past_2_31_elements():
+    t, e = 8_400_000, 256                                                 # 2.15e9 logits
+    v = np.random.default_rng(5).standard_normal((1000, e)).astype(np.float32)
+    bits = synth.f32_to_bf16_bits(v)
+    dev = torch.from_numpy(bits.view(np.int16)).cuda().repeat(t // 1000, 1)
+    d = qg.make_route_desc(qg.R_SOFTMAX, e, 8, renormalize=True)
+    ids = torch.empty((t, 8), dtype=torch.int32, device="cuda")
+    w = torch.empty((t, 8), device="cuda")
+    qg.moe_route(d, dev, qg.L_BF16, t, ids, w)
+    torch.cuda.synchronize()
+    rid, rw = RT.route(F.decode_bf16(bits), "softmax", 8, renorm=True)
+    for first in (0, 8_388_000, t - 1000):                                # 8388608 * e = 2^31
+        assert np.array_equal(ids[first:first + 1000].cpu().numpy(), rid)
+        assert np.all(np.abs(w[first:first + 1000].cpu().numpy() - rw) <= 2.0 ** -24 * (1 + 2.0 ** -16) * rw + 2.0 ** -149)
+
+
+@pytest.mark.parametrize("t", [70, 4100])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_addresses_of_single_elements(dtype, t):
+    # logits and bias that start one element past a 16-byte boundary, rows of 64 without a gap
+    rng = np.random.default_rng(t)
+    v = rng.standard_normal((t, 64)).astype(np.float32)
+    dev, held = _logits(v, dtype)
+    shifted = torch.empty(t * 64 + 1, dtype=dev.dtype, device="cuda")
+    shifted[1:] = dev.view(-1)
+    b = torch.empty(65, device="cuda")
+    bias = (rng.standard_normal(64) * 0.05).astype(np.float32)
+    b[1:] = torch.from_numpy(bias).cuda()
+    d = qg.make_route_desc(qg.R_SIGMOID, 64, 6, 8, 3, 2, True)
+    ids = torch.empty((t, 6), dtype=torch.int32, device="cuda")
+    w = torch.empty((t, 6), device="cuda")
+    for lg, bs in ((shifted[1:], b[1:]), (dev, b[1:]), (shifted[1:], b[1:].clone())):
+        qg.moe_route(d, lg, TYPE[dtype], t, ids, w, bs)
+        torch.cuda.synchronize()
+        rid, rw = RT.route(held, "sigmoid", 6, bias=bias, groups=8, topk_groups=3, group_top=2, renorm=True)
+        assert np.array_equal(ids.cpu().numpy(), rid)
+        assert np.all(np.abs(w.cpu().numpy() - rw) <= 2.0 ** -24 * (1 + 2.0 ** -16) * rw + 2.0 ** -149)
+
+
 def test_another_stream_and_no_tokens():
     v = np.random.default_rng(0).standard_normal((77, 64))
     s = torch.cuda.Stream()
