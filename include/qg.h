@@ -280,7 +280,7 @@ qg_status qg_moe_grouped_map(int32_t layout, const int32_t* offsets_or_counts, i
  *   x        device [T][K] of a_type (FP4: uint8 [T][K/2]);  x_scale device float32 [T] for
  *            e4m3 and int8 ([T][K/128] for block-scaled layers), uint8 [T][K/32] for FP4, else NULL
  *   sorted_ids / expert_ids / num_post_pad  from qg_moe_align with the same block_m
- *   block_m  4, 16, 32 or 64 (weight-streaming kernel) or 128, 256 (MFMA kernel; 256 not
+ *   block_m  4, 16, 32 or 64 (weights streamed past few rows) or 128, 256 (MFMA kernel; 256 not
  *            for e4m3 or int4->e4m3 weights); FP4 activations: 16, 32, 64 or 128;
  *            qg_moe_block_m picks one, any other is QG_ERR_UNSUPPORTED
  *   y        device [T*topk][N] of out_type; rows of dropped slots are not written

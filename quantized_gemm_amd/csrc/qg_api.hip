@@ -314,28 +314,29 @@ MfmaTile int8_tile(int64_t rows, int64_t n, int64_t k) {
   return best;
 }
 
-// int8 MoE blocks: 16-, 32- or 64-row streaming blocks or 128-row MFMA blocks, whichever is estimated to
-// take least.  A streaming workgroup (64 columns) by itself takes lat0 + lat us per K step, and wg0 + wg ns
-// per K step of a full GPU's time; the weights arrive at 6.5 TB/s; 128-row tiles as above, their weights at
-// 5.7 TB/s.  Routed rows are taken as spread evenly, an expert's last block half full.  Over 54
-// measured products (2 to 64 experts, means of 6 to 750 rows) its choice is within 1% of the best on
-// average, 14% at most; blocks by the mean alone lose where tiles are few: E = 4, N = 1024, K = 2048, a mean
-// of 32 rows 5.5 us with 16-row blocks, 14.5 with 128; E = 16, N = 512, K = 1024, 100 rows 8.6 with 64, 11.3
-// with 128; E = 64, N = 2816, K = 4096, 37 rows 213 with 32, 136 with 128.
+// int8 MoE blocks: 16, 32 or 64 rows on the few-rows kernel or 128-row tiles, whichever is estimated to take
+// least.  A few-rows workgroup (per 64 columns) by itself takes lat0 + lat us per K step, and wg0 + wg ns
+// per K step of a full GPU's time; weights arrive at 8.3 TB/s, counted once per block, 13 TB/s where all
+// of them stay in the last-level cache; 128-row tiles as above, their weights at 5.7 TB/s.  Routed rows are
+// taken as spread evenly, an expert's last block half full.  Over 58 measured products (2 to 64 experts,
+// means of 6 to 512 rows) its choice is within 2% of the best on average, 19% at most; blocks by the mean
+// alone lose where tiles are few: E = 4, N = 1024, K = 2048, a mean of 32 rows 5.8 us with 16-row blocks, 14.8
+// with 128; E = 16, N = 512, K = 1024, 32 rows 5.4 with 32, 10.1 with 128; E = 64, N = 2816, K = 4096, 37 rows 160
+// with 64, 136 with 128.
 struct Int8Block { int bm; double lat0, lat, wg0, wg; };
 constexpr Int8Block kInt8Blocks[] = {
-    {16, 3.0, 0.225, 5.2, 0.93}, {32, 3.4, 0.25, 6.4, 1.3}, {64, 3.7, 0.31, 9.4, 2.13}};
+    {16, 3.5, 0.10, 5.7, 0.68}, {32, 4.0, 0.08, 5.9, 1.04}, {64, 5.9, 0.15, 12.8, 1.46}};
 int32_t int8_block(int64_t experts, int64_t n, int64_t k, int64_t rows) {
-  const double touched = (double)std::min(experts, rows), steps = (double)(k / 128);
-  const double bytes = touched * (double)n * (double)k;
+  const double touched = (double)std::min(experts, rows), steps = (double)(k / 128), expert = (double)n * (double)k;
+  const double rate = touched * expert > (double)(1 << 28) ? 8.3e6 : 13e6;   // bytes per us
   auto blocks = [&](int bm) { return fmax(touched, (double)rows / bm + 0.5 * touched); };
   const Int8Tile& t = kInt8Tiles[1];
   const double r = blocks(128) * (double)((n + 255) / 256) / kCUs;
-  double best = fmax(fmax(t.lat * ceil(r), t.full * r) * steps + t.fixed + t.out * r, bytes / 5.7e6 + 2.5);
+  double best = fmax(fmax(t.lat * ceil(r), t.full * r) * steps + t.fixed + t.out * r, touched * expert / 5.7e6 + 2.5);
   int32_t bm = 128;
   for (const Int8Block& c : kInt8Blocks) {
     const double us = fmax(fmax(c.lat0 + c.lat * steps, blocks(c.bm) * (double)(n / 64) * (c.wg0 + c.wg * steps) / 1e3 + 2.0),
-                           bytes / 6.5e6 + 2.5);
+                           blocks(c.bm) * expert / rate + 2.5);
     if (us < best) {
       best = us;
       bm = c.bm;
@@ -780,9 +781,23 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
       return QG_ERR_UNSUPPORTED;
     return launched();
   }
+  if (pi.af == A_INT8) {
+    if (cb > 65535) return QG_ERR_UNSUPPORTED;   // a grid axis
+    QG_LOG("moe_gemm T=%lld topk=%d bm=%d -> int8 rows", (long long)tokens, topk, block_m);
+    const int64_t experts = p->desc.num_experts, rows = tokens * topk, touched = std::min(experts, rows);
+    MoeRows r{};
+    r.block = block_m;
+    r.blocks = (unsigned)cb;
+    // past the caches where most weights are read once, and too many to stay there; 64 columns where
+    // that leaves two workgroups per CU (32-row blocks, us with 32 / 64 columns: E = 64, N = 2816, K = 4096,
+    // 128 tokens top-6 124 / 117; E = 8, 64 tokens top-2 20.2 / 21.9)
+    r.once = 4 * rows <= 3 * experts * block_m && touched * (int64_t)p->w_expert_bytes >= (int64_t)1 << 25;
+    r.wide = std::max(touched, rows / block_m + touched / 2) * (p->desc.n / 64) > 2 * kCUs;
+    if (!launch_moe_rows_int8(a, r, pi.of, (hipStream_t)stream)) return QG_ERR_UNSUPPORTED;
+    return launched();
+  }
   StreamTile t = stream_tile(block_m, p->desc.n, byte_weights(&p->desc));
   if (!byte_weights(&p->desc)) stream_shape(t, p->desc.n, 8, 1);   // 128 columns per workgroup (see launch_mt)
-  if (pi.af == A_INT8) stream_shape(t, p->desc.n, 4, 2);           // 64
   t.grid_y = (unsigned)cb;
   QG_LOG("moe_gemm T=%lld topk=%d bm=%d -> stream mt=%d grid=%ux%u", (long long)tokens, topk, block_m, t.mt,
          t.grid_x, t.grid_y);

@@ -47,6 +47,13 @@ bool launch_mfma_gemm(const MfmaArgs& a, const MfmaTile& t, int wp, int af, int 
 
 // int8 products of few dense rows, 64 per workgroup.
 bool launch_rows_gemm_int8(const MfmaArgs& a, int of, hipStream_t st);
+struct MoeRows {
+  int block;                 // rows of a block (4, 16, 32 or 64)
+  unsigned blocks;           // grid's blocks (capacity)
+  bool once;                 // most weights are read by one block, from memory
+  bool wide;                 // 32-row blocks: 64 columns per workgroup instead of 32
+};
+bool launch_moe_rows_int8(const MfmaArgs& a, const MoeRows& m, int of, hipStream_t st);
 
 // Sum of the split-K partials a.part[ksplit][m][n] into a.y, with the e4m3 per-channel
 // (w_scale, fp8 weights) and per-token (a.x_scale, e4m3 activations) scales.  whole: the partials

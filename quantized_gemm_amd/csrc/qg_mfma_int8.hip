@@ -1,4 +1,4 @@
-// MFMA-bound int8 x int8 product for more rows than the few-rows and streaming kernels serve: dense
+// MFMA-bound int8 x int8 product for more rows than the few-rows kernel serves: dense
 // tiles (with K split over workgroups where the tiles are few) and MoE blocks.
 //
 //   sum[m][n] = sum_k x[m][k] w[n][k] in 32-bit integers (exact, so every tile and split gives the

@@ -1,4 +1,5 @@
-// int8 x int8 product of few rows: the weights are read once, or once per 64 rows, past the activations.
+// int8 x int8 product of few rows, dense or an MoE block's: the weights are read once, or once per 64 rows,
+// past the activations.
 //
 //   sum[m][n] = sum_k x[m][k] w[n][k] in 32-bit integers, y = out(float(sum) * sw[n] * sx[m]).
 //
@@ -13,6 +14,8 @@
 // Measured with 3 / 16 sets of weights in turn, of which the first stay in the 256 MB last-level cache:
 // N = K = 7168, 1 row 9.0 / 9.6 us (5.7 / 5.4 TB/s of weights), 16 rows 10.0 / 10.3, 32 rows 10.3 / 12.8,
 // 64 rows 12.1 / 17.2, 128 rows 15.0 / 21.4; N = K = 4096, 1 row 4.0 / 4.7, 64 rows 7.4 / 8.4, 128 rows 8.7 / 10.1.
+// MoE, E = 64 top-6, N = 2816, K = 4096: 1 token 15.0 us (6 experts, 4.6 TB/s), 64 tokens 106.6 (6.9 TB/s); the kernel
+// that streams weights through workgroups sharing staged activations took 17.8 and 112.2.
 #include <type_traits>
 
 #include "qg_device.h"
@@ -26,7 +29,7 @@ constexpr int kParts = 4;             // waves (8: N = K = 4096, 16 rows 4.6 -> 
 
 // RB: rows staged (8, 16, 32 or 64; those that fill no MFMA tile repeat others and are left out at the
 // end), CW: columns (16, 32 or 64, by MFMA tiles of 16 or 32), NTW: non-temporal weight loads
-template <int OF, int RB, int CW, bool NTW>
+template <int OF, int RB, int CW, bool MOE, bool NTW>
 __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   constexpr int KP = kParts;
   constexpr int TW = CW < 32 ? CW : 32, NT = CW / TW;              // MFMA tile, column tiles
@@ -37,41 +40,61 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   constexpr int ROWB = 128;                                        // bytes of a row per step
   constexpr int STAGE = RB * ROWB;                                 // per wave
   constexpr int LOADS = AP + KJ * NT;                              // per step
+  constexpr int BLOCK = RB == 8 ? 4 : RB;                          // MoE: rows of a block
   __shared__ __attribute__((aligned(16))) uint8_t sA0[KP * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t sA1[KP * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t sA2[KP * STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t sA3[KP * STAGE];
   __shared__ __attribute__((aligned(16))) float sRowScale[64];
   __shared__ __attribute__((aligned(16))) float sColScale[64];
+  __shared__ int sRowOut[MOE ? 64 : 1];                            // output row of each row (-1: none)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & (TW - 1), g = lane / TW;
   // (rows past RB: further row tiles, those of the same columns on the same XCD)
-  int mtile = 0, ntile = (int)blockIdx.x;
-  if (RB == 64 && a.m > RB) {
+  int mtile = 0, ntile = (int)blockIdx.x, expert = 0;
+  if constexpr (MOE) {
+    if ((int64_t)blockIdx.y * BLOCK >= *a.num_post_pad) return;
+    expert = a.expert_ids[blockIdx.y];
+  } else if (RB == 64 && a.m > RB) {
     const int mtiles = (int)((a.m + RB - 1) / RB);
     xcd_tile(blockIdx.x, mtiles, (int)gridDim.x / mtiles, (int64_t)RB * a.k, (int64_t)CW * a.k, mtile, ntile);
   }
   const int row0 = mtile * RB, col0 = ntile * CW;
   const int nsteps = a.k / ROWB;
   const int cnt = (nsteps - wave + KP - 1) / KP;                   // this wave's steps: wave, wave + KP, ...
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w, (uint32_t)a.w_expert_bytes);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)(a.m * a.k));
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (int64_t)expert * a.w_expert_bytes, (uint32_t)a.w_expert_bytes);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)(a.x_rows * a.k));
+  // output row (MoE: of the token's slot) of a row, -1: none
+  auto out_of = [&](int row) __attribute__((always_inline)) -> int {
+    if constexpr (MOE) {
+      const int f = row < BLOCK ? a.sorted_ids[(int64_t)blockIdx.y * BLOCK + row] : a.sentinel;
+      return f < a.sentinel ? f : -1;
+    } else {
+      return row < RB && row0 + row < a.m ? row0 + row : -1;
+    }
+  };
+  auto in_of = [&](int out) __attribute__((always_inline)) { return MOE && out >= 0 ? out / a.topk : out; };
 
   int a_off[AP];
 #pragma unroll
   for (int i = 0; i < AP; ++i) {
     const int p = lane + 64 * i, row = p >> 3;
-    a_off[i] = row0 + row < a.m ? (row0 + row) * a.k + 16 * ((p & 7) ^ ((row >> 1) & 7)) : -1;
+    const int in = in_of(out_of(row));
+    a_off[i] = in >= 0 ? in * a.k + 16 * ((p & 7) ^ ((row >> 1) & 7)) : -1;
   }
   int b_off[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     b_off[t] = (int)(((int64_t)((col0 + TW * t + r) >> 4) * (a.k >> 4) + g) * 256 + (r & 15) * 16);
   // the scales, for the end
-  if (wave == 0) bload4_lds(make_rsrc(a.x_scale, (uint32_t)(a.m * 4)), sRowScale,
-                            lane < RB && row0 + lane < a.m ? 4 * (row0 + lane) : kOOB);
-  if (wave == 1) bload4_lds(make_rsrc((const float*)a.s + col0, 4 * CW), sColScale, lane < CW ? 4 * lane : kOOB);
+  if (wave == 0) {
+    const int out = out_of(lane), in = in_of(out);
+    bload4_lds(make_rsrc(a.x_scale, (uint32_t)(a.x_rows * 4)), sRowScale, in >= 0 ? 4 * in : kOOB);
+    if constexpr (MOE) sRowOut[lane] = out;
+  }
+  if (wave == 1)
+    bload4_lds(make_rsrc((const float*)a.s + (int64_t)expert * a.n + col0, 4 * CW), sColScale, lane < CW ? 4 * lane : kOOB);
   __builtin_amdgcn_sched_barrier(0);
 
   auto stg = [&](int i) __attribute__((always_inline)) -> uint8_t* {
@@ -150,7 +173,13 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   __syncthreads();
   for (int p = tid; p < RB * PPR * NT; p += 64 * KP) {
     const int row = p / (PPR * NT), c = p % (PPR * NT);            // piece c of the row: columns 4 c ..
-    if (row0 + row >= a.m) break;
+    int64_t out = row0 + row;
+    if constexpr (MOE) {
+      out = row < BLOCK ? sRowOut[row] : -1;
+      if (out < 0) continue;
+    } else if (out >= a.m) {
+      break;
+    }
     const uint8_t* src = (NT == 1 || c < PPR ? sA0 : sA1) + 16 * (PPR * row + ((c & (PPR - 1)) ^ (row & (PPR - 1))));
     i32x4 v = *(const i32x4*)src;
 #pragma unroll
@@ -160,15 +189,15 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
     u32x2 o;
     o[0] = scaled_out2<OF>(v[0], v[1], sw[0], sw[1], sx);
     o[1] = scaled_out2<OF>(v[2], v[3], sw[2], sw[3], sx);
-    *(u32x2*)((uint16_t*)a.y + (int64_t)(row0 + row) * a.n + col0 + 4 * c) = o;
+    *(u32x2*)((uint16_t*)a.y + out * a.n + col0 + 4 * c) = o;
   }
 }
 
 template <int OF, int RB, int CW>
 void launch_one(const MfmaArgs& a, bool ntw, hipStream_t st) {
   const dim3 grid((unsigned)(a.n / CW * ((a.m + RB - 1) / RB))), block(64 * kParts);
-  if (ntw) hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, false>), grid, block, 0, st, a);
+  if (ntw) hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, false, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, false, false>), grid, block, 0, st, a);
 }
 
 // 16 columns while they are at most one workgroup per CU, else 32, which load the activations half as
@@ -199,6 +228,26 @@ void launch_rows(const MfmaArgs& a, hipStream_t st) {
   else launch_width<OF, 64>(a, ntw, st);
 }
 
+// 32 columns for blocks of 4 and 16 rows (64 tokens of the above with 16 / 32 / 64 columns: 123 / 107 / 113 us), 64 for
+// blocks of 64 (400 tokens 328 / 208 / 160).
+template <int OF, int RB, int CW>
+void launch_moe(const MfmaArgs& a, unsigned blocks, bool ntw, hipStream_t st) {
+  const dim3 grid(a.n / CW, blocks), block(64 * kParts);
+  if (ntw) hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, true, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((int8_rows_kernel<OF, RB, CW, true, false>), grid, block, 0, st, a);
+}
+
+template <int OF>
+bool launch_moe_rows(const MfmaArgs& a, const MoeRows& m, hipStream_t st) {
+  if (m.block == 4) launch_moe<OF, 8, 32>(a, m.blocks, m.once, st);
+  else if (m.block == 16) launch_moe<OF, 16, 32>(a, m.blocks, m.once, st);
+  else if (m.block == 32 && !m.wide) launch_moe<OF, 32, 32>(a, m.blocks, m.once, st);
+  else if (m.block == 32) launch_moe<OF, 32, 64>(a, m.blocks, m.once, st);
+  else if (m.block == 64) launch_moe<OF, 64, 64>(a, m.blocks, m.once, st);
+  else return false;
+  return true;
+}
+
 }  // namespace
 
 bool launch_rows_gemm_int8(const MfmaArgs& a, int of, hipStream_t st) {
@@ -206,6 +255,12 @@ bool launch_rows_gemm_int8(const MfmaArgs& a, int of, hipStream_t st) {
   else if (of == O_F16) launch_rows<O_F16>(a, st);
   else return false;
   return true;
+}
+
+bool launch_moe_rows_int8(const MfmaArgs& a, const MoeRows& m, int of, hipStream_t st) {
+  if (of == O_BF16) return launch_moe_rows<O_BF16>(a, m, st);
+  if (of == O_F16) return launch_moe_rows<O_F16>(a, m, st);
+  return false;
 }
 
 }  // namespace qg

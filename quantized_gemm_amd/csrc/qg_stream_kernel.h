@@ -17,8 +17,6 @@
 //  * e2m1 x 16-bit: the UE8M0 block scale is folded into the hardware e2m1 -> bf16/f16
 //    conversion (exact).
 //  * e4m3 x e4m3: fp8 MFMA, per-token x per-channel scale in the epilogue.
-//  * int8 x int8: i8 MFMA into 32-bit integers (exact), the same scales in the epilogue; K parts
-//    and slices are added as integers.
 //  * e4m3 x e2m1 (W4A8 MXFP4): the e2m1 codes and their UE8M0 block scales go to the
 //    scaled fp8/fp4 MFMA as they are; per-token scale in the epilogue.
 //  * block-scaled e4m3: one fp8 MFMA per chunk (= one 128-wide scale group) from zero,
@@ -33,8 +31,6 @@
 // blocks (rows gathered through sorted_ids).
 #pragma once
 
-#include <type_traits>
-
 #include "qg_device.h"
 #include "qg_kernels.h"
 
@@ -42,16 +38,16 @@ namespace qg {
 
 template <int WP, int AF>
 struct StreamTraits {
-  static constexpr bool kBytes = (WP == WP_FP8 || WP == WP_FP8_BLOCK || WP == WP_INT8);   // one byte per weight
-  static constexpr int ABYTES = (AF == A_FP8 || AF == A_INT8) ? 1 : 2;
-  static constexpr int B_U4 = kBytes ? 2 : 1;       // 16-byte weight units per lane per chunk
+  static constexpr bool kFp8Mfma = (WP == WP_FP8 || WP == WP_FP8_BLOCK);
+  static constexpr int ABYTES = (AF == A_FP8) ? 1 : 2;
+  static constexpr int B_U4 = kFp8Mfma ? 2 : 1;       // 16-byte weight units per lane per chunk
   // staged scale bytes per (column block, chunk): int4 paths 16 scales, fp4 4 groups x 16 bytes
-  static constexpr int SBYTES = kBytes ? 0 : (WP == WP_FP4 ? 64 : 32);
+  static constexpr int SBYTES = kFp8Mfma ? 0 : (WP == WP_FP4 ? 64 : 32);
 };
 
 // Chunks per wave whose weights are in flight at once (<= 16 KB per wave).
 template <int WP>
-constexpr int stream_max_chunks() { return StreamTraits<WP, A_FP8>::kBytes ? 8 : 16; }
+constexpr int stream_max_chunks() { return (WP == WP_FP8 || WP == WP_FP8_BLOCK) ? 8 : 16; }
 
 // Chunks per K part staged per round: <= 64 KB of activations in LDS.
 template <int WP, int AF, int MT, int KQ>
@@ -139,7 +135,7 @@ __global__ __launch_bounds__(64 * NCB * KQ) void stream_gemm_kernel(StreamArgs a
   const int myn = max(0, min(nchunks, my0 + per) - my0);
 
   const uint8_t* wbase = a.w + (int64_t)expert * a.w_expert_bytes;
-  const int64_t kun = T::kBytes ? (a.k >> 4) : (a.k >> 5);   // 16-byte units along K per column block
+  const int64_t kun = T::kFp8Mfma ? (a.k >> 4) : (a.k >> 5);   // 16-byte units along K per column block
   const int ngroups = a.group == 0 ? 1 : (a.k / a.group);
   const int64_t xrow_bytes = (int64_t)a.k * T::ABYTES;
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)(a.x_rows * xrow_bytes));
@@ -237,12 +233,9 @@ __global__ __launch_bounds__(64 * NCB * KQ) void stream_gemm_kernel(StreamArgs a
     }
   };
 
-  // int8 products are summed as 32-bit integers up to the output conversion
-  using Sum = std::conditional_t<WP == WP_INT8, int, float>;
-  using Acc = std::conditional_t<WP == WP_INT8, i32x4, f32x4>;
-  Acc acc[NMT];
+  f32x4 acc[NMT];
 #pragma unroll
-  for (int mt = 0; mt < NMT; ++mt) acc[mt] = Acc{0, 0, 0, 0};
+  for (int mt = 0; mt < NMT; ++mt) acc[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
   // the lane's activation row within a 16-row tile: staged rows only.  4-row tiles: rows
   // 4..15 of the MFMA operand read row r & 3 again; the products of those rows are finite
   // copies that land in accumulator rows 4..15, which nothing stores, so they need no zeroing
@@ -264,7 +257,7 @@ __global__ __launch_bounds__(64 * NCB * KQ) void stream_gemm_kernel(StreamArgs a
       const int ch = cbase + my0 + b0 + c;
 #pragma unroll
       for (int u = 0; u < T::B_U4; ++u) {
-        const int64_t ku = T::kBytes ? ((int64_t)ch * 8 + 2 * g + u) : ((int64_t)ch * 4 + g);
+        const int64_t ku = T::kFp8Mfma ? ((int64_t)ch * 8 + 2 * g + u) : ((int64_t)ch * 4 + g);
         const bool ok = (b0 + c) < myn && wact;
         bw[c][u] = bload16_stream(wr, ok ? (int)((((int64_t)nbw * kun + ku) * 16 + r) << 4) : kOOB);
       }
@@ -317,14 +310,7 @@ __global__ __launch_bounds__(64 * NCB * KQ) void stream_gemm_kernel(StreamArgs a
           if (!NOBR && ((b0 + c) >= myn || !wact)) continue;
             const uint8_t* arow0 = sA + q * PART + lc * 128 * T::ABYTES;
             const int slot = (cb * KQ + q) * RCR + lc;
-            if constexpr (WP == WP_INT8) {
-    #pragma unroll
-              for (int mt = 0; mt < NMT; ++mt) {
-                const uint8_t* ap = arow0 + (16 * mt + ar) * AROW + 32 * g;
-                acc[mt] = mfma16x16x64_i8(*(const u32x4*)ap, bw[c][0], acc[mt]);
-                acc[mt] = mfma16x16x64_i8(*(const u32x4*)(ap + 16), bw[c][1], acc[mt]);
-              }
-            } else if constexpr (WP == WP_FP8 || WP == WP_FP8_BLOCK) {
+            if constexpr (WP == WP_FP8 || WP == WP_FP8_BLOCK) {
     #pragma unroll
               for (int mt = 0; mt < NMT; ++mt) {
                 const uint8_t* ap = arow0 + (16 * mt + ar) * AROW + 32 * g;
@@ -442,10 +428,10 @@ __global__ __launch_bounds__(64 * NCB * KQ) void stream_gemm_kernel(StreamArgs a
 
   // ---- add the K parts through LDS (fixed order) and store ------------------------------
   // (the activation buffer is free after the last round's barrier)
-  typedef Sum RedRow[NCB * 16 + 1];
+  typedef float RedRow[NCB * 16 + 1];
   static_assert(sizeof(float) * KQ * BM * (NCB * 16 + 1) <= sizeof(sA), "reduction buffer");
   RedRow* sRed0 = reinterpret_cast<RedRow*>(sA);
-  auto sRed = [&](int p, int row) -> Sum* { return sRed0[p * BM + row]; };
+  auto sRed = [&](int p, int row) -> float* { return sRed0[p * BM + row]; };
 #pragma unroll
   for (int mt = 0; mt < NMT; ++mt)
 #pragma unroll
@@ -459,24 +445,19 @@ __global__ __launch_bounds__(64 * NCB * KQ) void stream_gemm_kernel(StreamArgs a
     const int tok = sRowTok[row];
     const int64_t n = (int64_t)blockIdx.x * BN + col;
     if (tok < 0 || n >= a.n) continue;
-    Sum sum = 0;
+    float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < KQ; ++p) sum += sRed(p, row)[col];
+    for (int p = 0; p < KQ; ++p) v += sRed(p, row)[col];
     if (ksl > 1) {                                    // partial sum of this K slice, unscaled
-      ((Sum*)a.part)[((int64_t)blockIdx.z * a.m + rowbase + row) * a.n + n] = sum;
+      a.part[((int64_t)blockIdx.z * a.m + rowbase + row) * a.n + n] = v;
       continue;
     }
-    float v = 0.f;
-    if constexpr (WP != WP_INT8) v = sum;
     if constexpr (WP == WP_FP8) v *= ((const float*)a.s)[(int64_t)expert * a.n + n];
     if constexpr (AF == A_FP8 && !BLOCK) v *= a.x_scale[tok];
     int64_t orow;
     if constexpr (MOE) orow = a.sorted_ids[rowbase + row];
     else orow = rowbase + row;
-    if constexpr (WP == WP_INT8)
-      yb[orow * a.n + n] = scaled_out<OF>(sum, ((const float*)a.s)[(int64_t)expert * a.n + n], a.x_scale[tok]);
-    else
-      yb[orow * a.n + n] = f32_to_out<OF>(v);
+    yb[orow * a.n + n] = f32_to_out<OF>(v);
   }
 }
 
@@ -505,12 +486,7 @@ static bool launch_shape(const StreamArgs& a, const StreamTile& t, hipStream_t s
 
 template <int WP, int AF, int OF, int ST, bool ZERO, bool MOE>
 static bool launch_mt(const StreamArgs& a, const StreamTile& t, hipStream_t st) {
-  if constexpr (WP == WP_INT8) {
-    // MoE blocks: 4 column blocks x 2 K parts (E = 64 top-6, N = 2816, K = 4096, 64 / 200 tokens: 113 /
-    // 122 us; 1 x 8 172 / 236, 2 x 4 114 / 159, 8 x 1 125 / -); dense rows have a kernel of their own
-    if constexpr (MOE)
-      if (t.ncb == 4 && t.kq == 2) return launch_shape<WP, AF, OF, ST, ZERO, MOE, 4, 2>(a, t, st);
-  } else if constexpr (StreamTraits<WP, AF>::kBytes) {
+  if constexpr (WP == WP_FP8 || WP == WP_FP8_BLOCK) {
     if (t.ncb == 1 && t.kq == 8) return launch_shape<WP, AF, OF, ST, ZERO, MOE, 1, 8>(a, t, st);
     if constexpr (!MOE)
       if (t.ncb == 8 && t.kq == 1) return launch_shape<WP, AF, OF, ST, ZERO, MOE, 8, 1>(a, t, st);

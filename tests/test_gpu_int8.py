@@ -278,7 +278,7 @@ def test_grouped_is_exact_for_every_block(bm, t, n, k, out):
 @pytest.mark.parametrize("flag", [0, qg.C_BATCH_INVARIANT])
 @pytest.mark.parametrize("t", [1, 9, 64, 500, 2000])
 def test_grouped_with_the_chosen_block(t, flag):
-    experts, topk, n, k = 16, 4, 256, 512          # blocks of 4, 16, 16, 64 and 128 rows
+    experts, topk, n, k = 16, 4, 256, 512
     layer, acts = synth.moe_w8a8_int8(t=t, experts=experts, topk=topk, n=n, k=k, seed=t)
     p, buf = layers.prepare_layer(layer, compute_flags=flag)
     bm = qg.moe_block_m(p, t, topk)
@@ -290,6 +290,30 @@ def test_grouped_with_the_chosen_block(t, flag):
     for e in range(experts):
         tt, jj = np.nonzero(acts.topk_ids == e)
         assert np.array_equal(got[tt, jj], _want(acts.x[tt], acts.x_scale[tt], layer.w[e], layer.s[e, :, 0], "bf16"))
+
+
+@pytest.mark.parametrize("t,bm", [(1, 4), (9, 4), (100, 16), (100, 32), (1000, 32), (250, 64), (1000, 64), (1000, 128)])
+def test_grouped_weights_beyond_the_caches(t, bm):
+    # 115 MB of weights: loads past the caches and through them, 32 and 64 columns per workgroup
+    experts, topk, n, k = 40, 4, 2816, 1024
+    gen = torch.Generator(device="cuda").manual_seed(t + bm)
+    w = torch.randint(-127, 128, (experts, n, k), generator=gen, device="cuda", dtype=torch.int8)
+    sw = torch.rand((experts, n, 1), generator=gen, device="cuda") * 1e-3
+    desc = qg.make_desc(qg.W_INT8, qg.S_F32, 0, 0, qg.A_INT8, qg.C_NATIVE, qg.O_BF16, experts, n, k)
+    img = torch.empty(qg.prepared_bytes(desc), dtype=torch.uint8, device="cuda")
+    p = qg.prepare(desc, w, sw, None, img)
+    x = torch.randint(-127, 128, (t, k), generator=gen, device="cuda", dtype=torch.int8)
+    xs = torch.rand(t, generator=gen, device="cuda") + 0.5
+    ids = np.stack([np.random.default_rng(i).permutation(experts)[:topk] for i in range(t)]).astype(np.int32)
+    y = torch.full((t * topk, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    qg.moe_gemm(p, x, xs, *_align(ids, experts, bm), t, topk, bm, y)
+    torch.cuda.synchronize()
+    got = _got(y).reshape(t, topk, n)
+    for e in (0, 7, 23, 39) if t > 1 else ids[0]:
+        tt, jj = np.nonzero(ids == e)
+        want = _want(x.cpu().numpy()[tt], xs.cpu().numpy()[tt], w[e].cpu().numpy(), sw[e, :, 0].cpu().numpy(), "bf16")
+        assert np.array_equal(got[tt, jj], want), e
+    assert not torch.isnan(y).any()
 
 
 def test_grouped_contiguous_rows():
