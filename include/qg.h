@@ -282,7 +282,8 @@ qg_status qg_moe_grouped_map(int32_t layout, const int32_t* offsets_or_counts, i
  *   sorted_ids / expert_ids / num_post_pad  from qg_moe_align with the same block_m
  *   block_m  4, 16, 32 or 64 (weights streamed past few rows) or 128, 256 (MFMA kernel; 256 not
  *            for e4m3 or int4->e4m3 weights); FP4 activations: 16, 32, 64 or 128;
- *            qg_moe_block_m picks one, any other is QG_ERR_UNSUPPORTED
+ *            qg_moe_block_m picks one, any other is QG_ERR_UNSUPPORTED, as are int8 blocks of 4
+ *            to 64 rows of which qg_moe_capacity gives more than 65535
  *   y        device [T*topk][N] of out_type; rows of dropped slots are not written
  * The grid is sized from capacity; blocks past num_post_pad exit at once.
  */

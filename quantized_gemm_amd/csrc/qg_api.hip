@@ -323,6 +323,7 @@ MfmaTile int8_tile(int64_t rows, int64_t n, int64_t k) {
 // alone lose where tiles are few: E = 4, N = 1024, K = 2048, a mean of 32 rows 5.8 us with 16-row blocks, 14.8
 // with 128; E = 16, N = 512, K = 1024, 32 rows 5.4 with 32, 10.1 with 128; E = 64, N = 2816, K = 4096, 37 rows 160
 // with 64, 136 with 128.
+constexpr int64_t kMaxBlocks = 65535;   // of a few-rows launch: a grid axis
 struct Int8Block { int bm; double lat0, lat, wg0, wg; };
 constexpr Int8Block kInt8Blocks[] = {
     {16, 3.5, 0.10, 5.7, 0.68}, {32, 4.0, 0.08, 5.9, 1.04}, {64, 5.9, 0.15, 12.8, 1.46}};
@@ -335,6 +336,7 @@ int32_t int8_block(int64_t experts, int64_t n, int64_t k, int64_t rows) {
   double best = fmax(fmax(t.lat * ceil(r), t.full * r) * steps + t.fixed + t.out * r, touched * expert / 5.7e6 + 2.5);
   int32_t bm = 128;
   for (const Int8Block& c : kInt8Blocks) {
+    if (rows / c.bm + std::min(experts, rows) >= kMaxBlocks) continue;
     const double us = fmax(fmax(c.lat0 + c.lat * steps, blocks(c.bm) * (double)(n / 64) * (c.wg0 + c.wg * steps) / 1e3 + 2.0),
                            blocks(c.bm) * expert / rate + 2.5);
     if (us < best) {
@@ -782,7 +784,7 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
     return launched();
   }
   if (pi.af == A_INT8) {
-    if (cb > 65535) return QG_ERR_UNSUPPORTED;   // a grid axis
+    if (cb > kMaxBlocks) return QG_ERR_UNSUPPORTED;
     QG_LOG("moe_gemm T=%lld topk=%d bm=%d -> int8 rows", (long long)tokens, topk, block_m);
     const int64_t experts = p->desc.num_experts, rows = tokens * topk, touched = std::min(experts, rows);
     MoeRows r{};

@@ -316,6 +316,30 @@ def test_grouped_weights_beyond_the_caches(t, bm):
     assert not torch.isnan(y).any()
 
 
+def test_grouped_with_more_blocks_than_a_grid_axis():
+    # 4.2 million rows of narrow experts: the chosen block is one that fits, a smaller one is refused
+    experts, topk, n, k, t = 8, 8, 64, 4096, 524_200
+    layer, _ = synth.moe_w8a8_int8(t=1, experts=experts, topk=topk, n=n, k=k, seed=3)
+    p, buf = layers.prepare_layer(layer)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randint(-127, 128, (t, k), generator=gen, device="cuda", dtype=torch.int8)
+    xs = torch.rand(t, generator=gen, device="cuda") + 0.5
+    ids = np.tile(np.arange(experts, dtype=np.int32), (t, 1))
+    y = torch.full((t * topk, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    bm = qg.moe_block_m(p, t, topk)
+    qg.moe_gemm(p, x, xs, *_align(ids, experts, bm), t, topk, bm, y)
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 1, t // 2, t - 1], device="cuda")
+    got = _got(y.view(t, topk, n)[rows])
+    for e in range(experts):
+        want = _want(x[rows].cpu().numpy(), xs[rows].cpu().numpy(), layer.w[e], layer.s[e, :, 0], "bf16")
+        assert np.array_equal(got[:, e], want)
+    few = torch.empty(16, dtype=torch.int32, device="cuda")
+    with pytest.raises(qg.QGError) as err:
+        qg.moe_gemm(p, x, xs, few, few, few, t, topk, 16, y)
+    assert err.value.status == 2
+
+
 def test_grouped_contiguous_rows():
     experts, n, k, rows = 4, 128, 256, 150
     layer, acts = synth.moe_w8a8_int8(t=rows, experts=experts, topk=1, n=n, k=k, seed=8)
