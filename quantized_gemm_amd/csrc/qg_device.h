@@ -321,7 +321,7 @@ __device__ __forceinline__ u32x4 bload16(__amdgpu_buffer_rsrc_t r, int off) {
 __device__ __forceinline__ u32x4 bload16_stream(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2);   // nt: streamed once
 }
-// The same with a wave-uniform part of the offset (in range together with the lane's).
+// The same with a wave-uniform part of the offset, inside the buffer also where the lane's is out of range.
 template <bool NTL>   // non-temporal: streamed once
 __device__ __forceinline__ u32x4 bload16_s(__amdgpu_buffer_rsrc_t r, int off, int soff) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, NTL ? 2 : 0);

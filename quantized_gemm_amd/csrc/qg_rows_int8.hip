@@ -19,13 +19,12 @@
 #include <type_traits>
 
 #include "qg_device.h"
+#include "qg_int8_steps.h"
 #include "qg_kernels.h"
 
 namespace qg {
 
 namespace {
-
-constexpr int kParts = 4;             // waves (8: N = K = 4096, 16 rows 4.6 -> 4.7 us, N = K = 7168 10.3 -> 10.9)
 
 // RB: rows staged (8, 16, 32 or 64; those that fill no MFMA tile repeat others and are left out at the
 // end), CW: columns (16, 32 or 64, by MFMA tiles of 16 or 32), NTW: non-temporal weight loads
@@ -62,7 +61,7 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   }
   const int row0 = mtile * RB, col0 = ntile * CW;
   const int nsteps = a.k / ROWB;
-  const int cnt = (nsteps - wave + KP - 1) / KP;                   // this wave's steps: wave, wave + KP, ...
+  const int cnt = wave_steps(nsteps, wave);                        // this wave's steps
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (int64_t)expert * a.w_expert_bytes, (uint32_t)a.w_expert_bytes);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)(a.x_rows * a.k));
   // output row (MoE: of the token's slot) of a row, -1: none
@@ -104,7 +103,7 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
   // (past the end: zeros)
   auto load = [&](int i, auto S_) __attribute__((always_inline)) {
     constexpr int S = decltype(S_)::value;
-    const int step = wave + KP * i;
+    const int step = wave_step(wave, i);
 #pragma unroll
     for (int c = 0; c < AP; ++c)
       bload16_lds(xr, stg(S) + 1024 * c, a_off[c] < 0 || i >= cnt ? kOOB : a_off[c] + step * ROWB);
@@ -112,7 +111,8 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
     for (int j = 0; j < KJ; ++j)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        B[S][j][t] = __builtin_bit_cast(i32x4, bload16_s<NTW>(wr, i >= cnt ? kOOB : b_off[t], step * 2048 + 256 * G * j));
+        B[S][j][t] = __builtin_bit_cast(i32x4, bload16_s<NTW>(wr, i >= cnt ? kOOB : b_off[t],
+                                                            weight_step_offset(wave, i, cnt, G * j)));
     __builtin_amdgcn_sched_barrier(0);
   };
   using Acc = std::conditional_t<TW == 32, i32x16, i32x4>;
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64 * kParts) void int8_rows_kernel(MfmaArgs a) {
         }
       }
     __builtin_amdgcn_sched_barrier(0);
-    load(i + 4, S_);
+    load(i + kAhead, S_);
   };
   int i = 0;
   for (; i + 4 <= cnt; i += 4) {
