@@ -232,15 +232,29 @@ __device__ __forceinline__ uint32_t int8_codes_divided(const float* v, float sc)
   return w;
 }
 
-// SwiGLU in float32 with the hardware reciprocal (one unit in the last place): the activation is
-// rounded to a code of seven bits next.
+// SwiGLU in float32 with the hardware reciprocal: the activation is rounded to a code of seven bits next.
+// Below a gate of -86 the reciprocal leaves the range in which the hardware gives it to a unit in the last
+// place (it flushes what is below 2^-126), and exp(-g) that of float32; 1 / (1 + exp(-g)) is exp(g) to 2^-124
+// there, taken as four factors exp(g / 4), none of which leaves the range before the activation does.  (49152 rows of 1408:
+// 65.0 us without that branch, 65.3 with it.)
 template <int IN>
 __device__ __forceinline__ void swiglu8_rcp(const uint16_t* row, int64_t inter, int64_t c8, float* act) {
   float g[8], u[8];
   unpack8<IN>(ldg16(row + 8 * c8), g);
   unpack8<IN>(ldg16(row + inter + 8 * c8), u);
+  float lowest = g[0];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) act[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[i])) * u[i];
+  for (int i = 0; i < 8; ++i) {
+    act[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[i])) * u[i];
+    lowest = fminf(lowest, g[i]);
+  }
+  if (lowest < -86.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float e = __expf(0.25f * g[i]);
+      act[i] = g[i] < -86.0f ? g[i] * e * (u[i] * e) * e * e : act[i];
+    }
+  }
 }
 
 template <int IN, bool SILU, int NT, int P>
