@@ -321,7 +321,8 @@ qg_status qg_moe_gemm(const qg_prepared* p, const void* x, const void* x_scale, 
  *             rounded to bfloat16 (nearest even), then exactly qg_quantize_e2m1_rows of those
  *             rows; out = packed e2m1 codes uint8 [rows][inter/2] (16-byte aligned)
  *             QG_A_INT8: each row quantized for the next product's int8 activations, act in
- *             float32 under the rule of qg_quantize_int8_rows; out = int8 [rows][inter]
+ *             float32 under the rule of qg_quantize_int8_rows (an act that is NaN or beyond
+ *             float32 makes its row's scale NaN); out = int8 [rows][inter]
  *   out_scale device float32 [rows] for QG_A_FP8_E4M3 and QG_A_INT8, uint8 [rows][inter/32]
  *             UE8M0 exponents for QG_A_FP4_E2M1, else ignored (may be NULL)
  * inter % 8 == 0 (and inter <= 8192 for QG_A_FP8_E4M3, <= 32768 for QG_A_INT8, inter % 32 == 0
@@ -345,11 +346,11 @@ qg_status qg_quantize_e4m3_rows(const void* x, int64_t rows, int64_t k, int32_t 
 
 /*
  * qg_quantize_int8_rows: per-token int8 quantization of 16-bit activations, the input of the int8
- * W8A8 products.  For each row r < rows of x (device [rows][k], in_type QG_A_F16 / QG_A_BF16,
- * finite):
+ * W8A8 products.  For each row r < rows of x (device [rows][k], in_type QG_A_F16 / QG_A_BF16):
  *   scale[r] = max_i |x[r][i]| / 127 in float32 (1 where that is 0, as for an all-zero row),
  *   codes[r][i] = x[r][i] / scale[r] in float32, rounded to the nearest integer, ties to even,
- *                 clamped to [-127, 127].
+ *                 clamped to [-127, 127];
+ *   a row that holds a NaN or an infinity has scale NaN and codes 0: its products are NaN.
  *   codes  device int8 [rows][k] (8-byte aligned);  scale  device float32 [rows]
  * k % 8 == 0 and k <= 32768, else QG_ERR_UNSUPPORTED.
  */

@@ -68,11 +68,15 @@ def absmax_rows(x):
 
 def absmax_int8_rows(x):
     """Per-row absmax int8: scale = max|row| / 127 in float32 (1 where that is 0), code = the quotient
-    in float32, rounded half to even, clamped to [-127, 127].  Returns (codes int8, scale float32)."""
+    in float32, rounded half to even, clamped to [-127, 127]; a row that holds a NaN or an infinity has
+    scale NaN and codes 0.  Returns (codes int8, scale float32)."""
     x32 = np.asarray(x, dtype=np.float32)
+    finite = np.isfinite(x32).all(axis=1)
+    x32 = np.where(finite[:, None], x32, np.float32(0.0))
     scale = (np.max(np.abs(x32), axis=1) / np.float32(127.0)).astype(np.float32)
     scale[scale == 0] = np.float32(1.0)
     q = np.rint((x32 / scale[:, None]).astype(np.float32))
+    scale[~finite] = np.float32(np.nan)
     return np.clip(q, -127, 127).astype(np.int8), scale
 
 

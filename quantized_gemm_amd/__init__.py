@@ -276,7 +276,8 @@ def quantize_e4m3_rows(x, rows: int, k: int, in_type: int, codes, scale, stream=
 
 
 def quantize_int8_rows(x, rows: int, k: int, in_type: int, codes, scale, stream=None):
-    """Per-token absmax int8 quantization of 16-bit rows: codes [rows][k] int8, scale [rows] float32."""
+    """Per-token absmax int8 quantization of 16-bit rows: codes [rows][k] int8, scale [rows] float32 (NaN, with
+    codes 0, for a row that holds a NaN or an infinity)."""
     st = lib().qg_quantize_int8_rows(_ptr(x), rows, k, in_type, _ptr(codes), _ptr(scale), _stream(stream))
     _check(st, "qg_quantize_int8_rows")
 

@@ -209,6 +209,9 @@ __global__ __launch_bounds__(256) void swiglu_e4m3_wave_kernel(const uint16_t* _
 // whose remainders could leave the range of float32 go through the division itself.
 // Bound by bytes: 4096 rows of 7168 bf16 17.1 us (5.1 TB/s), 49152 SwiGLU rows of 1408 65.5 us (5.3 TB/s);
 // with a division per quotient and per sigmoid 21.9 and 87 us, bound by instruction issue.
+//
+// A row that holds a NaN or an infinity has no scale: it is set to NaN and the codes to 0, so that what is
+// multiplied with the row is NaN.  The maximum keeps NaNs (one instruction for two values either way).
 __device__ __forceinline__ uint32_t int8_codes(const float* v, float sc, float inv) {
   uint32_t b[4];
 #pragma unroll
@@ -223,6 +226,7 @@ __device__ __forceinline__ uint32_t int8_codes(const float* v, float sc, float i
   return lo | (hi << 16);
 }
 __device__ __forceinline__ uint32_t int8_codes_divided(const float* v, float sc) {
+  if (sc != sc) return 0;
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -276,20 +280,21 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rows_int8_kernel(const ui
       if constexpr (SILU) swiglu8_rcp<IN>(row, k, c8, v[i]);
       else unpack8<IN>(ldg16(row + 8 * c8), v[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[i][e]));
+      for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(v[i][e]));
     }
   }
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+  for (int off = 32; off >= 1; off >>= 1) amax = __builtin_elementwise_maximum(amax, __shfl_xor(amax, off, 64));
   if constexpr (NT > 64) {
     __shared__ float s_wmax[NT / 64];
     if ((tid & 63) == 0) s_wmax[tid >> 6] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) amax = fmaxf(amax, s_wmax[w]);
+    for (int w = 0; w < NT / 64; ++w) amax = __builtin_elementwise_maximum(amax, s_wmax[w]);
   }
   float sc = amax / 127.0f;                                // correctly rounded division
   if (sc == 0.0f) sc = 1.0f;
+  if (!(amax < __builtin_inff())) sc = __builtin_nanf("");
   if (tid == 0) scale[r] = sc;
   const bool direct = !(sc >= 0x1p-100f && sc <= 0x1p100f);
   const float inv = 1.0f / sc;

@@ -1,4 +1,4 @@
-"""SwiGLU to int8 over the whole range of its inputs.
+"""Rows quantized to int8, SwiGLU among them, over the whole range of their inputs and outside it.
 
 Bars, from the arithmetic.  Gates below -86 take exp(g / 4) four times as a factor.  One such factor is 2^x with
 x = fl(fl(g / 4) log2 e): a half step of x, the 2^-26 by which the float32 constant is off times x (each times ln 2), and a
@@ -13,9 +13,10 @@ import pytest
 import torch
 
 import quantized_gemm_amd as qg
-from quantized_gemm_amd import synth
+from quantized_gemm_amd import layers, synth
 from oracle import formats as F
 from oracle import moe_layer as ML
+from oracle import quant as Q
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,81 @@ def test_the_most_negative_gates_give_zeros():
     want = np.zeros((4, 256), np.int8)
     want[:, 7] = -127
     assert np.array_equal(codes, want) and np.all(np.isfinite(scale)) and np.all(scale > 0)
+
+
+# ---- rows that hold something that is not finite -----------------------------------------------
+# They have no scale: it is NaN and the codes are 0, so that every output of such a row's product is NaN.
+
+BAD = [float("nan"), float("inf"), -float("inf")]
+
+
+def _finite_but(rows, k, seed, at):
+    """Normal rows; at: {row: (column, value)}."""
+    v = (np.random.default_rng(seed).standard_normal((rows, k)) * 3).astype(np.float32)
+    for r, (c, x) in at.items():
+        v[r, c] = x
+    return v
+
+
+def _same(codes, scale, rc, rs, bad):
+    assert np.isnan(scale[bad]).all() and (codes[bad] == 0).all()
+    good = np.setdiff1d(np.arange(len(scale)), bad)
+    assert np.array_equal(scale[good].view(np.uint32), rs[good].view(np.uint32)) and np.array_equal(codes[good], rc[good])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("k", [8, 504, 2048, 2056, 7168, 8200, 32768])
+def test_quantized_rows_that_are_not_finite(k, dtype):
+    # every position of a row lies on some thread's first or last piece
+    at = {1: (0, BAD[0]), 2: (k - 1, BAD[0]), 3: (k // 2, BAD[1]), 4: (k - 1, BAD[2]), 6: (5, -float("nan")), 9: (k // 3, BAD[1])}
+    v = _finite_but(11, k, k, at)
+    v[8] = 0
+    v[8, 3] = np.inf                                                       # nothing else in the row
+    v[7] = np.nan
+    bits = TO[dtype](v)
+    x = torch.from_numpy(bits.view(np.int16)).cuda()
+    codes = torch.full((11, k), 77, dtype=torch.int8, device="cuda")
+    scale = torch.full((11,), 77.0, device="cuda")
+    qg.quantize_int8_rows(x, 11, k, {"bf16": qg.A_BF16, "f16": qg.A_F16}[dtype], codes, scale)
+    torch.cuda.synchronize()
+    rc, rs = Q.absmax_int8_rows(F.decode_act(bits, dtype).astype(np.float32))
+    bad = np.array([1, 2, 3, 4, 6, 7, 8, 9])
+    assert np.array_equal(np.nonzero(np.isnan(rs))[0], bad)
+    _same(codes.cpu().numpy(), scale.cpu().numpy(), rc, rs, bad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("inter", [64, 1408, 4096, 16384])
+def test_swiglu_rows_that_are_not_finite(inter, dtype):
+    # in a gate, in an up, an up of infinity beside a gate that gives 0, a product past float32 (bf16 only)
+    gate, up = np.full((10, inter), 32.0, np.float32), _finite_but(10, inter, inter, {})
+    gate[1, 0], gate[2, inter - 1], gate[3, 7] = BAD
+    up[4, 1], up[5, inter // 2], up[6, inter - 2] = BAD
+    gate[7, 9], up[7, 9] = -60000.0, np.inf
+    bad = [1, 2, 3, 4, 5, 6, 7]
+    if dtype == "bf16":
+        gate[8, 3], up[8, 3] = 1e30, 1e30
+        bad.append(8)
+    bits = np.concatenate([TO[dtype](gate), TO[dtype](up)], axis=1)
+    codes, scale = _swiglu(bits, inter, dtype)
+    with np.errstate(all="ignore"):
+        _, rc, rs = ML.swiglu_int8(F.decode_act(bits, dtype))
+    _same(codes, scale, rc, rs, np.array(bad))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(5, 192, 512), (40, 192, 512), (700, 512, 640), (200, 512, 8192), (300, 4160, 2048)])
+def test_a_product_of_such_rows_is_nan_in_them_alone(m, n, k, out):
+    layer, acts = synth.dense_w8a8_int8(m=1, n=n, k=k, out=out, seed=m)
+    p, buf = layers.prepare_layer(layer)
+    bad = np.unique([1, m // 2, m - 1])
+    v = _finite_but(m, k, m, {int(r): (int(r) % k, BAD[i % 3]) for i, r in enumerate(bad)})
+    x = torch.from_numpy(TO["bf16"](v).view(np.int16)).cuda()
+    codes, scale = torch.empty((m, k), dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    qg.quantize_int8_rows(x, m, k, qg.A_BF16, codes, scale)
+    y = torch.full((m, n), 7.0, dtype={"bf16": torch.bfloat16, "f16": torch.float16}[out], device="cuda")
+    need = qg.workspace_bytes(p, m)
+    qg.gemm(p, codes, scale, y, m, torch.empty(need, dtype=torch.uint8, device="cuda") if need else None)
+    torch.cuda.synchronize()
+    nan = torch.isnan(y).cpu().numpy()
+    assert nan[bad].all() and not np.delete(nan, bad, axis=0).any()
