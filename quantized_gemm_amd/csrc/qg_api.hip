@@ -224,15 +224,14 @@ void stream_shape(StreamTile& t, int64_t n, int ncb, int kq) {
 }
 
 // Rows the few-rows int8 kernel takes.  To 32 rows it reads the weights faster than the tiles with K split
-// (us with 3 / 16 sets of weights in turn, of which the first stay in the last-level cache: N = K = 7168, 8
-// rows 9.2 / 9.6 against 12.1 / 14.4, 32 rows 10.3 / 12.8 against 13.0 / 15.3; N = 1024, K = 8192, 16 rows 4.8 /
-// 4.9 against 6.3 / 6.8); few columns leave CUs idle then, which K split over workgroups uses, so with long
-// K those win (N = 2048, K = 14336, 32 rows 9.5 / 14.7 against 10.1 / 13.1).  Above, while one round of
-// workgroups of 64 rows holds them, K is short enough for a CU that loads the activations of all of it (64
-// rows: N = K = 4096 7.4 / 8.4 against 9.1 / 10.2, N = K = 7168 12.1 / 17.2 against 14.5 / 17.3, N = 2048, K = 14336
-// 14.3 / 21 against 11.1 / 14.7) and long enough for its waves' steps in turn to pay (128 rows: N = K = 4096 8.7 /
-// 10.1 against 11.1 / 15.8, N = K = 7168 15.0 / 21.4 against 17.7 / 27.7, N = 7168, K = 2048 8.7 / 9.6 against 7.7 /
-// 9.9; 300 rows, N = 192: K = 640 4.2 against 4.1, K = 2048 4.9 against 7.3).
+// (us from the last-level cache / from HBM, against the best tile and split: N = K = 7168, 8 rows 9.5 / 9.8 against
+// 12.8 / 14.6; N = 1024, K = 8192, 8 rows 4.3 / 6.0 against 7.0 / 9.2); few columns leave CUs idle then, which K
+// split over workgroups uses, so with long K those win (N = 2048, K = 14336, 33 rows 12.3 / 16.3 against 10.8 /
+// 13.1).  Above, while one round of workgroups of 64 rows holds them, K is short enough for a CU that loads
+// the activations of all of it (64 rows: N = K = 4096 7.5 / 8.9 against 10.1 / 11.2, N = K = 7168 13.0 / 16.6 against
+// 14.9 / 16.8, N = 2048, K = 14336 14.9 / 20.8 against 11.6 / 14.2) and long enough for its waves' steps in turn to
+// pay (128 rows: N = K = 4096 9.1 / 10.6 against 10.8 / 12.9, N = K = 7168 15.7 / 20.9 against 16.3 / 21.9; 300 rows,
+// N = 192: K = 640 4.5 / 4.4 against 4.3 / 4.6, K = 2048 5.2 / 5.4 against 6.1 / 6.6).
 bool int8_rows(int64_t rows, int64_t n, int64_t k) {
   if (rows <= 32) return n > 4096 || (16 + (rows <= 8 ? 8 : rows <= 16 ? 16 : 32)) * k <= 3 << 18;
   if (rows <= 64) return n <= 8192 && k <= (n > 4096 ? 8192 : 6528);
@@ -278,11 +277,13 @@ bool rows256(int64_t rows, int64_t ntiles) {
 // int8 dense tiles.  A workgroup's K step takes `lat` us while its CU is otherwise idle, and a full
 // GPU gets through 256 of them in `full` us (bound by power and by what a CU loads per clock);
 // beginning and end cost `fixed` us plus `out` us per round of workgroups (writing the outputs).
-// Fitted to 26 shapes (33..4096 rows, 192..28672 columns, K 640..8192), which it orders within 7%:
-// at N = K = 7168 the tiles that measured best are 64 x 128 with K split in two at 64 rows (14.3 us,
-// unsplit 17, 64 x 256 split in four 16.2; the few-rows kernel 12.1), 64 x 128 at 256 (20.0; 128 x 128 23.0), 128 x 128 at 512
-// (29.2; 64 x 256 31.2, 128 x 256 38.7), 128 x 256 at 1024 (49.7; 128 x 128 52.4, 256 x 256 69.8),
-// 256 x 256 at 4096 (181; 128 x 256 189, 128 x 128 213).
+// Fitted to measured times.  With the few-rows kernel's rule above its choice is 1.5% slower than the best of
+// all candidates on average over 42 shapes (8..4096 rows, 192..28672 columns, K 640..14336), at most 10% with
+// weights from the last-level cache and 29% from HBM (128 rows, N = 2048, K = 14336: split in four 19.4 us, in eight
+// 15.1).  At N = K = 7168 the best are 64 x 128 with K split in two at 64 rows (14.9 us, unsplit 18.2, 64 x 256 split in
+// four 16.0; the few-rows kernel 13.0), 64 x 128 at 256 (19.4; 128 x 128 23.7), 128 x 128 at 512 (28.7; 64 x 256 30.6,
+// 128 x 256 39.4), 128 x 256 at 1024 (49.2; 128 x 128 53.2, 256 x 256 68.6), 256 x 256 at 4096 (174; 128 x 256 179,
+// 128 x 128 199).
 struct Int8Tile { int bm, cols; double lat, full, fixed, out; };
 constexpr Int8Tile kInt8Tiles[] = {
     {256, 256, 1.30, 1.75, 4.5, 6.0}, {128, 256, 0.66, 0.93, 3.8, 3.0}, {128, 128, 0.37, 0.54, 3.2, 1.5},
@@ -318,10 +319,10 @@ MfmaTile int8_tile(int64_t rows, int64_t n, int64_t k) {
 // least.  A few-rows workgroup (per 64 columns) by itself takes lat0 + lat us per K step, and wg0 + wg ns
 // per K step of a full GPU's time; weights arrive at 8.3 TB/s, counted once per block, 13 TB/s where all
 // of them stay in the last-level cache; 128-row tiles as above, their weights at 5.7 TB/s.  Routed rows are
-// taken as spread evenly, an expert's last block half full.  Over 58 measured products (2 to 64 experts,
-// means of 6 to 512 rows) its choice is within 2% of the best on average, 19% at most; blocks by the mean
-// alone lose where tiles are few: E = 4, N = 1024, K = 2048, a mean of 32 rows 5.8 us with 16-row blocks, 14.8
-// with 128; E = 16, N = 512, K = 1024, 32 rows 5.4 with 32, 10.1 with 128; E = 64, N = 2816, K = 4096, 37 rows 160
+// taken as spread evenly, an expert's last block half full.  Over 44 measured products (2 to 64 experts,
+// means of 1 to 1024 rows) the chosen block is 2% slower than the best on average, 21% at most; blocks by the
+// mean alone lose where tiles are few: E = 4, N = 1024, K = 2048, a mean of 32 rows 5.6 us with 16-row blocks, 15.5
+// with 128; E = 16, N = 512, K = 1024, 32 rows 5.6 with 32, 10.8 with 128; E = 64, N = 2816, K = 4096, 37 rows 160
 // with 64, 136 with 128.
 constexpr int64_t kMaxBlocks = 65535;   // of a few-rows launch: a grid axis
 struct Int8Block { int bm; double lat0, lat, wg0, wg; };

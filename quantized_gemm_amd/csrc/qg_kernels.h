@@ -36,7 +36,7 @@ struct StreamTile {
 // The MFMA-bound kernel takes the same arguments.
 typedef StreamArgs MfmaArgs;
 struct MfmaTile {
-  int bm;                    // rows per workgroup tile (128 or 256); 256 columns per tile
+  int bm;                    // rows per workgroup tile (64, 128 or 256); 256 columns per tile
   unsigned grid_x, grid_y;   // dense: grid_x = all tiles; MoE: grid_x = column tiles, grid_y = blocks
   int ksplit;                // dense: K slices (grid z), 1 = none
   int cols;                  // int8 products: columns per workgroup (128 or 256; the others 256)

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256) void swiglu_e4m3_wave_kernel(const uint16_t* _
 // takes two corrections by its exact remainder: the first leaves less than a unit in the last place, from
 // where the second gives the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990).  Divisors
 // whose remainders could leave the range of float32 go through the division itself.
-// Bound by bytes: 4096 rows of 7168 bf16 17.1 us (5.1 TB/s), 49152 SwiGLU rows of 1408 65.5 us (5.3 TB/s);
+// Bound by bytes: 4096 rows of 7168 bf16 16.4-17.0 us (5.2-5.4 TB/s), 49152 SwiGLU rows of 1408 65.3-66 us (5.2-5.3);
 // with a division per quotient and per sigmoid 21.9 and 87 us, bound by instruction issue.
 //
 // A row that holds a NaN or an infinity has no scale: it is set to NaN and the codes to 0, so that what is

@@ -21,8 +21,8 @@
 // are then reductions over lanes, and no LDS is used.  Bound by latency and instruction issue, not by
 // bytes (8192 tokens of 256 float32 logits are 8.4 MB), so larger batches take four tokens per wave, one
 // per row of 16 lanes, whose reductions are four lane moves: see moe_route_rows_kernel.
-// Measured, launches in a graph: 1 token of 128 experts 3.3 us (a launch by itself), 4096 of 128 float32
-// 4.9 us, 8192 of 256 float32 with bias and groups 10.0 us (0.84 TB/s).
+// Measured, launches in a graph: 1 token of 128 experts 3.3-3.7 us (a launch by itself), 4096 of 128 float32
+// 5.0 us, 8192 of 256 float32 with bias and groups 10.2 us (0.87 TB/s), 8192 of 512 float32 15.0 us.
 #include "qg_device.h"
 #include "qg_kernels.h"
 

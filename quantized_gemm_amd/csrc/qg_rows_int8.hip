@@ -11,10 +11,10 @@
 // four steps ahead like the activations.  At the end the waves' sums meet in LDS, as integers, so that
 // their order does not matter.
 //
-// Measured with 3 / 16 sets of weights in turn, of which the first stay in the 256 MB last-level cache:
-// N = K = 7168, 1 row 9.0 / 9.6 us (5.7 / 5.4 TB/s of weights), 16 rows 10.0 / 10.3, 32 rows 10.3 / 12.8,
-// 64 rows 12.1 / 17.2, 128 rows 15.0 / 21.4; N = K = 4096, 1 row 4.0 / 4.7, 64 rows 7.4 / 8.4, 128 rows 8.7 / 10.1.
-// MoE, E = 64 top-6, N = 2816, K = 4096: 1 token 15.0 us (6 experts, 4.6 TB/s), 64 tokens 106.6 (6.9 TB/s); the kernel
+// Measured in a graph, with 3 sets of weights in turn, which stay in the 256 MB last-level cache, / with 1 GiB of
+// them: N = K = 7168, 1 row 9.5 / 9.7 us (5.4 / 5.3 TB/s of weights), 16 rows 11.0 / 11.3, 32 rows 10.8 / 13.5,
+// 64 rows 12.8 / 16.6-18.1, 128 rows 15.7 / 21.5; N = K = 4096, 1 row 4.5 / 5.2, 64 rows 8.1 / 9.1, 128 rows 9.1 / 10.6.
+// MoE, E = 64 top-6, N = 2816, K = 4096: 1 token 15.1 us (6 experts, 4.6 TB/s), 64 tokens 106.3 (6.9 TB/s); the kernel
 // that streams weights through workgroups sharing staged activations took 17.8 and 112.2.
 #include <type_traits>
 
