@@ -20,34 +20,11 @@
 // row's absmax within one wave for rows up to 2048 wide, within a workgroup beyond.
 #include "qg_device.h"
 #include "qg_kernels.h"
+#include "qg_rows.h"
 
 namespace qg {
 
 namespace {
-
-template <int T>   // O_F16 / O_BF16
-__device__ __forceinline__ float to_f32(uint32_t bits16) {
-  if constexpr (T == O_BF16) return bf16_bits_to_f32(bits16);
-  else return f16_bits_to_f32(bits16);
-}
-
-template <int T>
-__device__ __forceinline__ void unpack8(const u32x4 v, float* f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = to_f32<T>(v[i] & 0xFFFFu);
-    f[2 * i + 1] = to_f32<T>(v[i] >> 16);
-  }
-}
-
-template <int T>
-__device__ __forceinline__ u32x4 pack8(const float* f) {
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = (uint32_t)f32_to_out<T>(f[2 * i]) | ((uint32_t)f32_to_out<T>(f[2 * i + 1]) << 16);
-  return o;
-}
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
@@ -197,45 +174,6 @@ __global__ __launch_bounds__(256) void swiglu_e4m3_wave_kernel(const uint16_t* _
   }
 }
 
-// int8 rows, as they are or as SwiGLU of [gate | up]: one row per NT threads (NT = 64: a wave per
-// row, four rows per workgroup), each keeping up to P pieces of 8 values in registers between the
-// maximum and the codes, so that the row is read once.  The quotient is rounded to float32 and
-// then to an integer, as the definition says; for a row of 16-bit values it decides every code
-// but those of exact halves as exact arithmetic does.
-//
-// The quotients of a row share their divisor, so its reciprocal is divided out once and each quotient
-// takes two corrections by its exact remainder: the first leaves less than a unit in the last place, from
-// where the second gives the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990).  Divisors
-// whose remainders could leave the range of float32 go through the division itself.
-// Bound by bytes: 4096 rows of 7168 bf16 16.4-17.0 us (5.2-5.4 TB/s), 49152 SwiGLU rows of 1408 65.3-66 us (5.2-5.3);
-// with a division per quotient and per sigmoid 21.9 and 87 us, bound by instruction issue.
-//
-// A row that holds a NaN or an infinity has no scale: it is set to NaN and the codes to 0, so that what is
-// multiplied with the row is NaN.  The maximum keeps NaNs (one instruction for two values either way).
-__device__ __forceinline__ uint32_t int8_codes(const float* v, float sc, float inv) {
-  uint32_t b[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float q = v[e] * inv;
-    q = __builtin_fmaf(__builtin_fmaf(-q, sc, v[e]), inv, q);
-    q = __builtin_fmaf(__builtin_fmaf(-q, sc, v[e]), inv, q);
-    // |q| <= 127: the sum's last bit is 1, so it rounds to an integer, whose low byte is the code
-    b[e] = __float_as_uint(q + 12582912.0f);
-  }
-  const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u);
-  return lo | (hi << 16);
-}
-__device__ __forceinline__ uint32_t int8_codes_divided(const float* v, float sc) {
-  if (sc != sc) return 0;
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float q = fminf(fmaxf(__builtin_rintf(v[e] / sc), -127.0f), 127.0f);
-    w |= ((uint32_t)(int)q & 0xFFu) << (8 * e);
-  }
-  return w;
-}
-
 // SwiGLU in float32 with the hardware reciprocal: the activation is rounded to a code of seven bits next.
 // Below a gate of -86 the reciprocal leaves the range in which the hardware gives it to a unit in the last
 // place (it flushes what is below 2^-126), and exp(-g) that of float32; 1 / (1 + exp(-g)) is exp(g) to 2^-124
@@ -261,6 +199,17 @@ __device__ __forceinline__ void swiglu8_rcp(const uint16_t* row, int64_t inter, 
   }
 }
 
+// int8 rows, as they are or as SwiGLU of [gate | up]: one row per NT threads (NT = 64: a wave per
+// row, four rows per workgroup), each keeping up to P pieces of 8 values in registers between the
+// maximum and the codes, so that the row is read once.  The quotient is rounded to float32 and
+// then to an integer, as the definition says; for a row of 16-bit values it decides every code
+// but those of exact halves as exact arithmetic does.
+//
+// Bound by bytes: 4096 rows of 7168 bf16 16.4-17.0 us (5.2-5.4 TB/s), 49152 SwiGLU rows of 1408 65.3-66 us (5.2-5.3);
+// with a division per quotient and per sigmoid 21.9 and 87 us, bound by instruction issue.
+//
+// A row that holds a NaN or an infinity has no scale: it is set to NaN and the codes to 0, so that what is
+// multiplied with the row is NaN.  The maximum keeps NaNs (one instruction for two values either way).
 template <int IN, bool SILU, int NT, int P>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rows_int8_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                        int64_t k, int8_t* __restrict__ codes,

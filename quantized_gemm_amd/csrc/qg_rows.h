@@ -1,0 +1,106 @@
+// Pieces of the kernels that work row by row on 16-bit activations: eight values to and from 16 bytes, and
+// their int8 codes.
+#pragma once
+
+#include "qg_device.h"
+
+namespace qg {
+
+template <int T>   // O_F16 / O_BF16
+__device__ __forceinline__ float to_f32(uint32_t bits16) {
+  if constexpr (T == O_BF16) return bf16_bits_to_f32(bits16);
+  else return f16_bits_to_f32(bits16);
+}
+
+template <int T>
+__device__ __forceinline__ void unpack8(const u32x4 v, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = to_f32<T>(v[i] & 0xFFFFu);
+    f[2 * i + 1] = to_f32<T>(v[i] >> 16);
+  }
+}
+
+template <int T>
+__device__ __forceinline__ u32x4 pack8(const float* f) {
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = (uint32_t)f32_to_out<T>(f[2 * i]) | ((uint32_t)f32_to_out<T>(f[2 * i + 1]) << 16);
+  return o;
+}
+
+// int8 codes of four values of a row with the scale sc and its reciprocal inv.
+//
+// The quotients of a row share their divisor, so its reciprocal is divided out once and each quotient
+// takes two corrections by its exact remainder: the first leaves less than a unit in the last place, from
+// where the second gives the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990).  Divisors
+// whose remainders could leave the range of float32 go through the division itself.
+__device__ __forceinline__ uint32_t int8_codes(const float* v, float sc, float inv) {
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float q = v[e] * inv;
+    q = __builtin_fmaf(__builtin_fmaf(-q, sc, v[e]), inv, q);
+    q = __builtin_fmaf(__builtin_fmaf(-q, sc, v[e]), inv, q);
+    // |q| <= 127: the sum's last bit is 1, so it rounds to an integer, whose low byte is the code
+    b[e] = __float_as_uint(q + 12582912.0f);
+  }
+  const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u);
+  return lo | (hi << 16);
+}
+__device__ __forceinline__ uint32_t int8_codes_divided(const float* v, float sc) {
+  if (sc != sc) return 0;
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float q = fminf(fmaxf(__builtin_rintf(v[e] / sc), -127.0f), 127.0f);
+    w |= ((uint32_t)(int)q & 0xFFu) << (8 * e);
+  }
+  return w;
+}
+
+// e4m3 codes of four values of a row, likewise; |quotient| <= 448 to a unit in the last place, which the conversion
+// (nearest even) takes to 448.  A row that is not finite has scale NaN and codes 0.
+__device__ __forceinline__ uint32_t e4m3_of(const float* q) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);   // bytes 0, 1
+  v = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], v, true);        // bytes 2, 3
+  return (uint32_t)v;
+}
+__device__ __forceinline__ uint32_t e4m3_codes(const float* v, float sc, float inv) {
+  float q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    q[e] = v[e] * inv;
+    q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], sc, v[e]), inv, q[e]);
+    q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], sc, v[e]), inv, q[e]);
+  }
+  return e4m3_of(q);
+}
+__device__ __forceinline__ uint32_t e4m3_codes_divided(const float* v, float sc) {
+  if (sc != sc) return 0;
+  float q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q[e] = fminf(fmaxf(v[e] / sc, -448.0f), 448.0f);
+  return e4m3_of(q);
+}
+
+// MXFP4 codes of 8 of a block's 32 values, whose largest magnitude (of all 32) is amax: see mxfp4_encode32.
+// Returns the UE8M0 byte; a block that is not finite has the byte of NaN (255) and codes 0.
+__device__ __forceinline__ uint32_t mxfp4_encode8(const float* v, float amax, uint32_t& codes) {
+  codes = 0;
+  if (!(amax < __builtin_inff())) return 255;
+  const int e = amax > 0.f ? max(-127, min(127, __builtin_amdgcn_frexp_expf(amax) - 3)) : -127;
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    const float q = __builtin_ldexpf(v[h], -e);
+    const float m = fabsf(q);
+    uint32_t c = (uint32_t)(m > 0.25f) + (uint32_t)(m >= 0.75f) + (uint32_t)(m > 1.25f) + (uint32_t)(m >= 1.75f) +
+                 (uint32_t)(m > 2.5f) + (uint32_t)(m >= 3.5f) + (uint32_t)(m > 5.0f);
+    if (q < 0.f && c != 0) c |= 8u;
+    codes |= c << (4 * h);
+  }
+  return (uint32_t)(e + 127);
+}
+
+}  // namespace qg
