@@ -430,6 +430,132 @@ qg_status qg_moe_combine(const void* y, const float* weights, const int32_t* top
                          int32_t num_experts, int64_t n, int32_t dtype, void* out, void* stream);
 
 /*
+ * qg_norm_rows: the norms before and after a block of a model, with the block's gate, the residual and the
+ * quantization of what the next product reads, in one pass.  For each row of k values:
+ *   h = y (the block's output), or N_post(y) where post_norm is set;
+ *   u = res + res_scale * gate * h          (without res: res_scale * gate * h; without y: res)
+ *   res_out = u;   z = N(u);   out = z in 16 bits;   codes, scale = z quantized
+ *   N(v) = (v - c) / sqrt(mean((v - c)^2) + eps) * (weight_offset + weight) + bias
+ *   c = 0 (QG_N_RMS) or mean(v) (QG_N_LAYER); without a weight the factor is 1; N_post has no bias.
+ * All of it is float32 arithmetic with one rounding at each output: z and the codes are taken from u before
+ * it is rounded to res_out's type, the codes from z before it is rounded to 16 bits.
+ *   y            device rows of k of `type` (QG_O_*), y_stride elements apart, or NULL
+ *   res, res_out device rows of k of res_type (`type`'s, or QG_L_F32), res_stride apart; res_out may be res
+ *   gate         device [k] of `type` (gate_stride 0) or rows of k gate_stride apart, or NULL (1)
+ *   post_weight, weight, bias   device [k] of `type`, or NULL
+ *   out          device rows of k of `type`, out_stride apart, or NULL; may be y (with the same stride)
+ *   codes, scale with code_type (else both NULL; contiguous rows):
+ *     QG_A_FP8_E4M3, QG_A_INT8   uint8 / int8 [rows][k], float32 [rows]: as qg_quantize_e4m3_rows and
+ *                qg_quantize_int8_rows (scale max|z| / 448 or / 127, 1 for a row of zeros); a row that holds a NaN
+ *                or an infinity has scale NaN and codes 0
+ *     QG_A_FP4_E2M1   uint8 [rows][k/2], uint8 [rows][k/32]: as qg_quantize_e2m1_rows; a block that is not
+ *                finite has exponent byte 255 (NaN) and codes 0
+ * norm 0: the residual alone (no weight, bias, out, codes).  One of res_out, out and codes at least is given.
+ * Strides: 0 = k, else at least k and a multiple of 8.  k % 8 == 0 (MXFP4: 32), k <= 32768, else
+ * QG_ERR_UNSUPPORTED.  eps >= 1e-30.
+ */
+enum { QG_N_RMS = 1, QG_N_LAYER = 2 };
+typedef struct {
+  int32_t norm;         /* QG_N_* of u; 0: none                              */
+  int32_t post_norm;    /* QG_N_* of y; 0: none                              */
+  int32_t type;         /* QG_O_*                                            */
+  int32_t res_type;     /* QG_L_*: `type`'s, or QG_L_F32                     */
+  int32_t code_type;    /* QG_A_FP8_E4M3, QG_A_INT8, QG_A_FP4_E2M1; 0: none  */
+  float eps;
+  float weight_offset;  /* 1 where weights are stored less one               */
+  float res_scale;
+  int64_t k, y_stride, res_stride, out_stride, gate_stride;
+} qg_norm_desc;
+qg_status qg_norm_rows(const qg_norm_desc* desc, int64_t rows, const void* y, const void* res, void* res_out,
+                       const void* gate, const void* post_weight, const void* weight, const void* bias, void* out,
+                       void* codes, void* scale, void* stream);
+
+/*
+ * qg_lora: low-rank adapters of many requests beside a product that they share.  For token m with adapter a and
+ * column n of slice s (a joint projection's parts each have an A of their own; one slice: s = 0):
+ *   t[r] = sum_k x[m][k] * A[a][s][r][k]                                   for r < ranks[a]
+ *   y[m][n] = base[m][n] + scales[a] * sum_{r < ranks[a]} t[r] * B[a][n][r]   one rounding, to `type`
+ * Rows of A and columns of B from ranks[a] on are not used (they may hold anything).  t is float32 and enters the
+ * second product as two 16-bit numbers (a high and a low part of it).
+ *   x          device rows of k of `type` (QG_O_*), x_stride apart
+ *   a, b       device [num_adapters][num_slices][max_rank][k] and [num_adapters][n][max_rank] of `type`
+ *   ranks      device int32 [num_adapters], taken into [0, max_rank], or NULL: max_rank
+ *   scales     device float32 [num_adapters], or NULL: 1
+ *   sorted_ids, expert_ids, num_post_pad   the batch's block map, made by qg_moe_align from one adapter id per
+ *              token (topk 1, num_experts = num_adapters, block_m); the same map serves every product of a step.
+ *              Tokens whose id is outside [0, num_adapters) have no adapter: their rows of y are not written.
+ *   base, y    device rows of n, base_stride and y_stride apart: the shared product's output; y may be base
+ *   block_m    16 or 64; qg_lora_block_m gives the better one for a batch
+ *   ws         qg_lora_workspace_bytes(desc, tokens, block_m) bytes
+ * The result does not depend on where in the batch a token stands; it does, in its last bits, on the batch's size,
+ * which sets how K is split.  max_rank <= 256 and a multiple of 8, num_adapters <= 512, num_slices <= 8, n % 8 == 0,
+ * k % 8 == 0, slice ends ascending to n, all but the last multiples of 32.
+ */
+typedef struct {
+  int32_t type;          /* QG_O_* of x, a, b, base and y                    */
+  int32_t num_adapters;
+  int32_t max_rank;
+  int32_t num_slices;
+  int64_t n, k;
+  int64_t x_stride, base_stride, y_stride;   /* elements; 0: k, n, n; multiples of 8   */
+  int64_t slice_end[8];  /* first column behind each slice                   */
+} qg_lora_desc;
+int32_t qg_lora_block_m(int64_t tokens, int32_t num_adapters);
+size_t qg_lora_workspace_bytes(const qg_lora_desc* desc, int64_t tokens, int32_t block_m);
+qg_status qg_lora(const qg_lora_desc* desc, const void* x, const void* a, const void* b, const int32_t* ranks,
+                  const float* scales, const int32_t* sorted_ids, const int32_t* expert_ids, const int32_t* num_post_pad,
+                  int64_t tokens, int32_t block_m, const void* base, void* y, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A cache of keys and values in MXFP4, in pages of page_tokens tokens.  Every token's head of head_dim values is
+ * head_dim / 32 blocks of one UE8M0 exponent and 32 e2m1 codes, by qg_quantize_e2m1_rows' rule; a block that holds a
+ * NaN or an infinity is kept as NaN.  The cache is one device buffer of qg_kv_cache_bytes bytes (the layout inside a
+ * page is the attention's own); a token's slot is page * page_tokens + its place in the page.
+ *   qg_kv_append  writes rows of keys and values (device, kv_heads * head_dim of `type`, k_stride / v_stride apart)
+ *                 to their slots (device int32 [tokens]); a token whose slot is outside the cache is skipped.  A
+ *                 call's slots are distinct: one given twice holds any mix of its rows.
+ *   qg_kv_read    writes the slots' keys and values back as contiguous rows of `type` (f16: values above 65504 are
+ *                 infinite; zeros for a slot outside the cache)
+ * head_dim 64, 128 or 256; page_tokens a power of two from 16 to 256; num_pages * page_tokens < 2^31.
+ */
+typedef struct {
+  int32_t type;          /* QG_O_* of the rows, and of queries and outputs   */
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_tokens;
+  int64_t num_pages;
+} qg_kv_desc;
+size_t qg_kv_cache_bytes(const qg_kv_desc* desc);
+qg_status qg_kv_append(const qg_kv_desc* desc, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       const int32_t* slots, int64_t tokens, void* cache, void* stream);
+qg_status qg_kv_read(const qg_kv_desc* desc, const void* cache, const int32_t* slots, int64_t tokens, void* k, void* v,
+                     void* stream);
+
+/*
+ * qg_attention: attention over that cache.  Sequence b has seq_lens[b] cached tokens, its newest queries' own
+ * among them; its n queries stand at its last n places, and each sees the tokens up to its own place:
+ *   out[i] = sum_t w_t V[t] / sum_t w_t,  w_t = exp(scale * q[i] . K[t]),  t <= seq_lens[b] - n + i
+ * per query head; query head h reads key head h / (q_heads / kv_heads).  A query that sees no token gives zeros.
+ * Softmax and sums are float32; bf16 weights are rounded to bf16 before they multiply the values, f16 ones keep
+ * 16 bits and more.
+ *   q, out       device rows of q_heads * head_dim of `type`, q_stride and out_stride apart (0: contiguous)
+ *   block_table  device int32, rows of table_stride >= max_len / page_tokens pages (rounded up): page j of sequence b
+ *                holds its tokens j * page_tokens and on.  Tokens of a page outside [0, num_pages) are not seen.
+ *   seq_lens     device int32 [batch], taken into [0, max_len]
+ *   q_offsets    device int32 [batch + 1]: sequence b's queries are rows q_offsets[b] .. q_offsets[b + 1] - 1 of q and
+ *                out, at most max_q of them; NULL: one query per sequence (max_q 1, tokens == batch)
+ *   tokens       rows of q and out.  Rows that belong to no sequence are neither read nor written.
+ *   ws           qg_attention_workspace_bytes(...) bytes (0: none needed)
+ * The result depends on batch, max_q and max_len (which set how the tokens are split) in its last bits only.
+ */
+size_t qg_attention_workspace_bytes(const qg_kv_desc* desc, int32_t q_heads, int64_t batch, int64_t max_q, int64_t tokens,
+                                    int64_t max_len);
+qg_status qg_attention(const qg_kv_desc* desc, const void* q, int64_t q_stride, int32_t q_heads, const void* cache,
+                       const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens, const int32_t* q_offsets,
+                       int64_t batch, int64_t max_q, int64_t tokens, int64_t max_len, float scale, void* out,
+                       int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qg_dequant: writes expert `expert` of a prepared layer back as dense float32
  * [N][K] = code value (minus zero point) times scale, read through the same
  * unpack routines the GEMM kernels use.  Every such value is exact in float32

@@ -6,7 +6,8 @@ library's HIP kernels.  The entry points mirror include/qg.h one to one:
 ``prepared_bytes``, ``prepare``, ``workspace_bytes``, ``gemm``, ``moe_block_m``,
 ``moe_capacity``, ``moe_align``, ``moe_grouped_map``, ``moe_gemm``, ``moe_swiglu``,
 ``moe_combine``, ``moe_route``, ``quantize_e4m3_rows``, ``quantize_int8_rows``,
-``quantize_e2m1_rows``, ``dequant``, ``status_str``, ``version`` and the measurement helpers
+``quantize_e2m1_rows``, ``norm_rows``, ``lora_block_m``, ``lora_workspace_bytes``, ``lora``, ``kv_cache_bytes``,
+``kv_append``, ``kv_read``, ``attention_workspace_bytes``, ``attention``, ``dequant``, ``status_str``, ``version`` and the measurement helpers
 ``ceiling_read`` and ``ceiling_mfma``.
 
 There is no fallback: if libqg.so is missing or cannot be loaded, every call raises.
@@ -28,12 +29,15 @@ C_NATIVE, C_W_TO_FP8, C_BATCH_INVARIANT = 0, 1, 4
 MOE_CONTIGUOUS, MOE_MASKED = 1, 2
 R_SOFTMAX, R_SIGMOID = 1, 2
 L_F16, L_BF16, L_F32 = 1, 2, 3
+N_RMS, N_LAYER = 1, 2
 
 STATUS = {0: "QG_OK", 1: "QG_ERR_INVALID_ARG", 2: "QG_ERR_UNSUPPORTED", 3: "QG_ERR_ARCH_MISMATCH",
           4: "QG_ERR_NOT_PREPARED", 5: "QG_ERR_WORKSPACE", 6: "QG_ERR_CAPACITY", 7: "QG_ERR_HIP"}
 EXPORTS = ["qg_prepared_bytes", "qg_prepare", "qg_workspace_bytes", "qg_gemm", "qg_moe_block_m", "qg_moe_capacity",
            "qg_moe_align", "qg_moe_grouped_map", "qg_moe_gemm", "qg_moe_swiglu", "qg_moe_combine",
-           "qg_quantize_e4m3_rows", "qg_quantize_int8_rows", "qg_quantize_e2m1_rows", "qg_moe_route", "qg_dequant",
+           "qg_quantize_e4m3_rows", "qg_quantize_int8_rows", "qg_quantize_e2m1_rows", "qg_moe_route", "qg_norm_rows",
+           "qg_lora_block_m", "qg_lora_workspace_bytes", "qg_lora", "qg_kv_cache_bytes", "qg_kv_append", "qg_kv_read",
+           "qg_attention_workspace_bytes", "qg_attention", "qg_dequant",
            "qg_ceiling_read", "qg_ceiling_mfma", "qg_ceiling_lds",
            "qg_gemm_noalloc", "qg_noalloc_scratch_bytes",
            "qg_status_str", "qg_version"]
@@ -56,6 +60,25 @@ class RouteDesc(ctypes.Structure):
     _fields_ = [("scoring", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
                 ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
                 ("renormalize", ctypes.c_int32), ("weight_scale", ctypes.c_float)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("res_type", ctypes.c_int32), ("code_type", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("res_scale", ctypes.c_float), ("k", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("res_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64)]
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("num_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
+                ("num_slices", ctypes.c_int32), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("base_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("slice_end", ctypes.c_int64 * 8)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("num_pages", ctypes.c_int64)]
 
 
 class Prepared(ctypes.Structure):
@@ -100,6 +123,20 @@ def lib():
         L.qg_quantize_int8_rows.argtypes, L.qg_quantize_int8_rows.restype = [vp, i64, i64, i32, vp, vp, vp], i32
         L.qg_moe_route.argtypes = [ctypes.POINTER(RouteDesc), vp, i32, i64, vp, i64, vp, vp, vp]
         L.qg_moe_route.restype = i32
+        f32 = ctypes.c_float
+        pn, pl, pk = ctypes.POINTER(NormDesc), ctypes.POINTER(LoraDesc), ctypes.POINTER(KvDesc)
+        L.qg_norm_rows.argtypes, L.qg_norm_rows.restype = [pn, i64] + [vp] * 11, i32
+        L.qg_lora_block_m.argtypes, L.qg_lora_block_m.restype = [i64, i32], i32
+        L.qg_lora_workspace_bytes.argtypes, L.qg_lora_workspace_bytes.restype = [pl, i64, i32], sz
+        L.qg_lora.argtypes = [pl] + [vp] * 8 + [i64, i32, vp, vp, vp, sz, vp]
+        L.qg_lora.restype = i32
+        L.qg_kv_cache_bytes.argtypes, L.qg_kv_cache_bytes.restype = [pk], sz
+        L.qg_kv_append.argtypes, L.qg_kv_append.restype = [pk, vp, i64, vp, i64, vp, i64, vp, vp], i32
+        L.qg_kv_read.argtypes, L.qg_kv_read.restype = [pk, vp, vp, i64, vp, vp, vp], i32
+        L.qg_attention_workspace_bytes.argtypes = [pk, i32, i64, i64, i64, i64]
+        L.qg_attention_workspace_bytes.restype = sz
+        L.qg_attention.argtypes = [pk, vp, i64, i32, vp, vp, i64, vp, vp, i64, i64, i64, i64, f32, vp, i64, vp, sz, vp]
+        L.qg_attention.restype = i32
         L.qg_dequant.argtypes, L.qg_dequant.restype = [pp, i32, vp, vp], i32
         u64 = ctypes.c_uint64
         L.qg_gemm_noalloc.argtypes, L.qg_gemm_noalloc.restype = [pp, vp, vp, vp, i64, vp], i32
@@ -300,6 +337,83 @@ def quantize_e2m1_rows(x, rows: int, k: int, in_type: int, codes, scales, stream
     """MXFP4 quantization of 16-bit rows: codes [rows][k/2] uint8 (packed e2m1), scales [rows][k/32] uint8."""
     st = lib().qg_quantize_e2m1_rows(_ptr(x), rows, k, in_type, _ptr(codes), _ptr(scales), _stream(stream))
     _check(st, "qg_quantize_e2m1_rows")
+
+
+def make_norm_desc(norm, type, k, eps, post_norm=0, res_type=None, code_type=0, weight_offset=0.0, res_scale=1.0,
+                   y_stride=0, res_stride=0, out_stride=0, gate_stride=0) -> NormDesc:
+    """norm, post_norm: N_RMS, N_LAYER or 0; type: O_*; res_type: L_* (default: type's); code_type: A_* or 0."""
+    res = (L_F16 if type == O_F16 else L_BF16) if res_type is None else res_type
+    return NormDesc(norm, post_norm, type, res, code_type, eps, weight_offset, res_scale, k, y_stride, res_stride, out_stride,
+                    gate_stride)
+
+
+def norm_rows(desc: NormDesc, rows: int, y, residual, residual_out=None, out=None, codes=None, scale=None, *, weight=None,
+              bias=None, gate=None, post_weight=None, stream=None):
+    """u = residual + res_scale * gate * [N_post](y) -> residual_out; N(u) -> out (16 bits) and/or codes and scale."""
+    st = lib().qg_norm_rows(ctypes.byref(desc), rows, _ptr(y), _ptr(residual), _ptr(residual_out), _ptr(gate),
+                            _ptr(post_weight), _ptr(weight), _ptr(bias), _ptr(out), _ptr(codes), _ptr(scale), _stream(stream))
+    _check(st, "qg_norm_rows")
+
+
+def make_lora_desc(type, num_adapters, max_rank, k, slice_ends, x_stride=0, base_stride=0, y_stride=0) -> LoraDesc:
+    """slice_ends: the columns behind each slice, the last one n ([n] for a single projection)."""
+    ends = [int(e) for e in slice_ends]
+    return LoraDesc(type, num_adapters, max_rank, len(ends), ends[-1] if ends else 0, k, x_stride, base_stride, y_stride,
+                    (ctypes.c_int64 * 8)(*ends[:8]))
+
+
+def lora_block_m(tokens: int, num_adapters: int) -> int:
+    """Block size of the map (moe_align with topk 1) that lora takes for a batch."""
+    return lib().qg_lora_block_m(tokens, num_adapters)
+
+
+def lora_workspace_bytes(desc: LoraDesc, tokens: int, block_m: int) -> int:
+    return lib().qg_lora_workspace_bytes(ctypes.byref(desc), tokens, block_m)
+
+
+def lora(desc: LoraDesc, x, a, b, sorted_ids, expert_ids, num_post_pad, tokens: int, block_m: int, base, y, ws, ranks=None,
+         scales=None, stream=None):
+    """y = base + scales * (x A^T) B^T for the tokens of the block map, each with its own adapter's A and B."""
+    st = lib().qg_lora(ctypes.byref(desc), _ptr(x), _ptr(a), _ptr(b), _ptr(ranks), _ptr(scales), _ptr(sorted_ids),
+                       _ptr(expert_ids), _ptr(num_post_pad), tokens, block_m, _ptr(base), _ptr(y), _ptr(ws),
+                       0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "qg_lora")
+
+
+def make_kv_desc(type, kv_heads, head_dim, page_tokens, num_pages) -> KvDesc:
+    return KvDesc(type, kv_heads, head_dim, page_tokens, num_pages)
+
+
+def kv_cache_bytes(desc: KvDesc) -> int:
+    return lib().qg_kv_cache_bytes(ctypes.byref(desc))
+
+
+def kv_append(desc: KvDesc, k, v, slots, tokens: int, cache, k_stride: int = 0, v_stride: int = 0, stream=None):
+    """Rows of keys and values into the MXFP4 cache, each token at its slot (int32; outside the cache: skipped)."""
+    st = lib().qg_kv_append(ctypes.byref(desc), _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), tokens, _ptr(cache),
+                            _stream(stream))
+    _check(st, "qg_kv_append")
+
+
+def kv_read(desc: KvDesc, cache, slots, tokens: int, k, v, stream=None):
+    """The keys and values at the slots, as contiguous 16-bit rows."""
+    st = lib().qg_kv_read(ctypes.byref(desc), _ptr(cache), _ptr(slots), tokens, _ptr(k), _ptr(v), _stream(stream))
+    _check(st, "qg_kv_read")
+
+
+def attention_workspace_bytes(desc: KvDesc, q_heads: int, batch: int, max_q: int, tokens: int, max_len: int) -> int:
+    return lib().qg_attention_workspace_bytes(ctypes.byref(desc), q_heads, batch, max_q, tokens, max_len)
+
+
+def attention(desc: KvDesc, q, q_heads: int, cache, block_table, seq_lens, batch: int, max_len: int, scale: float, out, ws=None,
+              q_offsets=None, max_q: int = 1, tokens: int | None = None, q_stride: int = 0, out_stride: int = 0, stream=None):
+    """Causal attention of each sequence's newest queries over its tokens in the MXFP4 cache; block_table [batch][pages]
+    int32; tokens: rows of q (default: its first dimension)."""
+    st = lib().qg_attention(ctypes.byref(desc), _ptr(q), q_stride, q_heads, _ptr(cache), _ptr(block_table), block_table.shape[-1],
+                            _ptr(seq_lens), _ptr(q_offsets), batch, max_q, q.shape[0] if tokens is None else tokens, max_len,
+                            scale, _ptr(out), out_stride, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                            _stream(stream))
+    _check(st, "qg_attention")
 
 
 def dequant(p: Prepared, expert: int, out, stream=None):

@@ -1,0 +1,489 @@
+// Attention over a paged cache of keys and values in MXFP4 (qg_kernels.h has its layout):
+//
+//   out[i] = softmax(scale q[i] K^T) V per query head over the tokens that query i sees: those up to its own place
+//
+// One pass over the cached tokens with the running maximum and sum of the softmax.  The rows of a tile are the
+// queries of one key head: (token, head of the group), 16 or a multiple of them.  A wave takes 32 tokens a step:
+//
+//   S^T = K q^T    MFMA 16x16x32, first operand two tiles of 16 tokens: a lane's 16 (D = 128) bytes of a key are one
+//                  block of 32 values and one scale, converted in registers; lane (row, c) gets the scores of
+//                  tokens 4 c .. 4 c + 3 and 16 + 4 c .. 16 + 4 c + 3 of query `row`
+//   O^T += V^T P^T the same lanes' weights are the second operand as they stand, in that order of tokens; the first
+//                  is made from words of 8 codes of one token each: converted in pairs of values, then
+//                  regrouped into pairs of tokens
+//
+// so that no score or weight leaves its lane.  Codes times their power of two are exact in bf16, whatever the
+// queries' type.  bf16 queries multiply as they are and weights are rounded to bf16 (their sum, taken in float32
+// before, is not): an error of at most 2^-9 of each weight, of the size of the output's own rounding.  f16 has
+// three bits more, so f16 queries and weights are taken as a high and a low bf16 part, which hold all of them.
+//
+// The maximum only moves when a score is more than 2^8 times above it: weights stay below 2^8 and the exchange
+// between lanes and the rescaling of O are rare.
+#include <type_traits>
+
+#include "qg_device.h"
+#include "qg_kernels.h"
+#include "qg_rows.h"
+
+namespace qg {
+
+namespace {
+
+constexpr int kAttnWaves = 4;
+constexpr float kLazy = 8.0f;
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ u32x4 bf16_low(const float* v, u32x4 hi) {
+  float lo[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float h = bf16_bits_to_f32(e & 1 ? hi[e >> 1] >> 16 : hi[e >> 1] & 0xFFFFu);
+    lo[e] = v[e] - h;
+  }
+  return u32x4{pack2<A_BF16>(lo[0], lo[1]), pack2<A_BF16>(lo[2], lo[3]), pack2<A_BF16>(lo[4], lo[5]), pack2<A_BF16>(lo[6], lo[7])};
+}
+__device__ __forceinline__ u32x4 bf16_high(const float* v) {
+  return u32x4{pack2<A_BF16>(v[0], v[1]), pack2<A_BF16>(v[2], v[3]), pack2<A_BF16>(v[4], v[5]), pack2<A_BF16>(v[6], v[7])};
+}
+template <int B>
+__device__ __forceinline__ uint32_t cvt_pair(uint32_t w, float s) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
+}
+// UE8M0 byte b of a word -> its power of two; 0 is 2^-127, 255 NaN.
+__device__ __forceinline__ float power_of(uint32_t word, int b) {
+  const uint32_t e = (word >> (8 * b)) & 0xFFu;
+  return __uint_as_float(e == 255 ? 0x7FC00000u : max(e << 23, 0x00400000u));
+}
+
+// What a lane loads of a step: 32 tokens.
+template <int D>
+struct Step {
+  static constexpr int KW = D / 32;                 // words of a key per lane
+  static constexpr int VU = D == 256 ? 2 : 1;       // 16-byte units of four tokens per tile and lane
+  uint32_t k[2][KW];
+  uint32_t ks[2];                                   // exponent bytes of the keys' blocks
+  u32x4 v[2][VU];
+  uint32_t vs[2];                                   // exponent bytes of four tokens
+  bool ok[2];                                       // the tile's page is in the cache
+};
+
+template <int T, int D, int RT, bool SHARE>
+__global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) {
+  constexpr bool HILO = T == O_F16;
+  constexpr int KW = D / 32, NJ = D / 16;           // MFMAs of a score tile; tiles of 16 output values
+  constexpr int OP = D + 4;
+  __shared__ __attribute__((aligned(16))) float so[SHARE ? kAttnWaves * 16 * OP : 1];
+  __shared__ float sm[SHARE ? kAttnWaves : 1][16], sl[SHARE ? kAttnWaves : 1][16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, c = lane >> 4;
+
+  // ---- the tile: sequence, key head, rows, tokens -------------------------------------
+  // (key heads and sequences fastest: tiles that read the same keys run on the same XCD)
+  const int heads = a.batch * a.kv_heads;
+  const int bh = blockIdx.x % heads, rest = blockIdx.x / heads;
+  const int split = rest % a.nsplit, tile = rest / a.nsplit;
+  const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
+  int64_t q0 = b;
+  int nq = 1;
+  if (a.q_offsets) {
+    q0 = max(0, a.q_offsets[b]);
+    nq = (int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0);
+    nq = min(nq, a.max_q);
+  }
+  const int row_count = nq * a.group;
+  const int row0 = (SHARE ? tile : tile * kAttnWaves + wave) * 16 * RT;
+  if ((SHARE ? row0 : tile * kAttnWaves * 16 * RT) >= row_count) return;
+  const bool idle = row0 >= row_count;              // (not SHARE: this wave only; no barriers then)
+  if (idle) return;
+  const int len = max(0, min(a.lens[b], a.max_len));
+  int sees[RT], qrow[RT];                           // tokens that row 16 t + r sees; its query
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int row = min(row0 + 16 * t + r, row_count - 1);
+    qrow[t] = row / a.group;
+    sees[t] = max(0, len - nq + qrow[t] + 1);
+  }
+  const int last_row = min(row0 + 16 * RT, row_count) - 1;
+  const int most = __builtin_amdgcn_readfirstlane(max(0, len - nq + last_row / a.group + 1));
+  const int least = __builtin_amdgcn_readfirstlane(max(0, len - nq + row0 / a.group + 1));
+  const int steps = (most + 31) / 32, per = (steps + a.nsplit - 1) / a.nsplit;
+  const int begin = split * per, end = min(steps, begin + per);
+
+  // ---- queries ---------------------------------------------------------------------------
+  u32x4 qf[RT][KW], ql[HILO ? RT : 1][HILO ? KW : 1];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int row = min(row0 + 16 * t + r, row_count - 1);
+    const int head = hk * a.group + row - qrow[t] * a.group;
+    const uint16_t* p = (const uint16_t*)a.q + (q0 + qrow[t]) * a.q_stride + head * D + c * (D / 4);
+#pragma unroll
+    for (int j = 0; j < KW; ++j) {
+      qf[t][j] = ldg16(p + 8 * j);
+      if constexpr (HILO) {
+        float v[8];
+        unpack8<O_F16>(qf[t][j], v);
+        qf[t][j] = bf16_high(v);
+        ql[t][j] = bf16_low(v, qf[t][j]);
+      }
+    }
+  }
+
+  const int page = 1 << a.page_shift;
+  const int64_t half = (int64_t)page * (D / 2), tail = (int64_t)page * (D / 32), head_bytes = 2 * (half + tail);
+  const int32_t* const table = a.table + (int64_t)b * a.table_stride;
+  const int last_page = max(0, len - 1) >> a.page_shift;
+  auto load = [&](int step, Step<D>& s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t0 = 32 * step + 16 * h;
+      const int id = table[min(t0 >> a.page_shift, last_page)];
+      s.ok[h] = id >= 0 && id < a.num_pages;
+      const uint8_t* base = a.cache + ((int64_t)(s.ok[h] ? id : 0) * a.kv_heads + hk) * head_bytes;
+      const int t = t0 & (page - 1);
+      const uint8_t* kp = base + (t + r) * (D / 2) + c * (D / 8);
+      if constexpr (KW == 2) {
+        const u32x2 w = *(const u32x2*)kp;
+        s.k[h][0] = w[0];
+        s.k[h][1] = w[1];
+      } else {
+#pragma unroll
+        for (int j = 0; j < KW; j += 4) {
+          const u32x4 w = ldg16(kp + 4 * j);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s.k[h][j + e] = w[e];
+        }
+      }
+      const uint8_t* ksp = base + 2 * half + (t + r) * (D / 32);
+      if constexpr (D == 256) s.ks[h] = *(const uint16_t*)(ksp + 2 * c);
+      else s.ks[h] = ksp[D == 128 ? c : c >> 1];
+      const int t4 = (t >> 2) + c;
+      const uint8_t* vp = base + half + (int64_t)t4 * (D / 8) * 16;
+      if constexpr (D == 256) {
+        s.v[h][0] = ldg16(vp + 32 * r);
+        s.v[h][1] = ldg16(vp + 32 * r + 16);
+      } else {
+        s.v[h][0] = ldg16(vp + 16 * (D == 128 ? r : r >> 1));
+      }
+      const int blk = D == 256 ? r >> 1 : D == 128 ? r >> 2 : r >> 3;
+      s.vs[h] = *(const uint32_t*)(base + 2 * half + tail + (t4 * (D / 32) + blk) * 4);
+    }
+  };
+
+  f32x4 acc[RT][NJ];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    m[t] = kNegInf;
+    l[t] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  auto compute = [&](int step, Step<D>& s) __attribute__((always_inline)) {
+    // scores: lane (r, c) has tokens 4 c + i (h = 0) and 16 + 4 c + i (h = 1) of each row tile's row r
+    f32x4 sc[RT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 kf[KW];
+#pragma unroll
+      for (int j = 0; j < KW; ++j) {
+        const float p = power_of(s.ks[h], D == 256 ? j >> 2 : 0);
+        kf[j] = u32x4{cvt_pair<0>(s.k[h][j], p), cvt_pair<1>(s.k[h][j], p), cvt_pair<2>(s.k[h][j], p), cvt_pair<3>(s.k[h][j], p)};
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KW; ++j) {
+          x = mfma16x16x32<A_BF16>(kf[j], qf[t][j], x);
+          if constexpr (HILO) x = mfma16x16x32<A_BF16>(kf[j], ql[t][j], x);
+        }
+        sc[t][h] = x * a.scale_log2;
+      }
+    }
+    const bool cut = 32 * step + 32 > least || !s.ok[0] || !s.ok[1];   // some row does not see some of the tokens
+    if (cut) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!s.ok[h] || 32 * step + 16 * h + 4 * c + i >= sees[t]) sc[t][h][i] = kNegInf;
+    }
+    // weights
+    u32x4 pf[RT], pl[HILO ? RT : 1];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float top = sc[t][0][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, sc[t][e >> 2][e & 3]);
+      if (__any(top > m[t] + kLazy || (m[t] == kNegInf && top > kNegInf))) {
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float up = fmaxf(m[t], top);
+        const float f = up == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - up);
+        m[t] = up;
+        l[t] *= f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[t][j] *= f;
+      }
+      const float base = m[t] == kNegInf ? 0.f : m[t];
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(sc[t][e >> 2][e & 3] - base);
+        l[t] += p[e];
+      }
+      pf[t] = bf16_high(p);
+      if constexpr (HILO) pl[t] = bf16_low(p, pf[t]);
+    }
+    // values: tokens that some row does not see must not reach its sums, weight 0 or not
+    float vp[2][4];
+    bool bad[2][4];
+    bool any_bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vp[h][i] = power_of(s.vs[h], i);
+        bad[h][i] = false;
+        if (cut) {
+          const int tok = 32 * step + 16 * h + 4 * c + i;
+          if (!s.ok[h] || tok >= most) vp[h][i] = 0.f;                  // seen by no row: what is there does not matter
+          bad[h][i] = vp[h][i] != vp[h][i];                             // seen by some: its NaN goes to those only
+          if (bad[h][i]) vp[h][i] = 0.f;
+          any_bad |= bad[h][i];
+        }
+      }
+    auto values = [&](auto use) __attribute__((always_inline)) {
+      constexpr int WORDS = D == 256 ? 2 : 1, PAIRS = D == 64 ? 2 : 4;
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) {
+        uint32_t word[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) word[h][i] = D == 64 ? s.v[h][0][i] >> (16 * (r & 1)) : s.v[h][w][i];
+        auto pair = [&](auto B_) __attribute__((always_inline)) {
+          constexpr int B = decltype(B_)::value;
+          uint32_t x[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[h][i] = cvt_pair<B>(word[h][i], vp[h][i]);
+          u32x4 even, odd;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            even[e] = __builtin_amdgcn_perm(x[e >> 1][2 * (e & 1) + 1], x[e >> 1][2 * (e & 1)], 0x05040100u);
+            odd[e] = __builtin_amdgcn_perm(x[e >> 1][2 * (e & 1) + 1], x[e >> 1][2 * (e & 1)], 0x07060302u);
+          }
+          use(8 * w + 2 * B, even);
+          use(8 * w + 2 * B + 1, odd);
+        };
+        pair(std::integral_constant<int, 0>{});
+        pair(std::integral_constant<int, 1>{});
+        if constexpr (PAIRS == 4) {
+          pair(std::integral_constant<int, 2>{});
+          pair(std::integral_constant<int, 3>{});
+        }
+      }
+    };
+    values([&](int j, u32x4 vf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        acc[t][j] = mfma16x16x32<A_BF16>(vf, pf[t], acc[t][j]);
+        if constexpr (HILO) acc[t][j] = mfma16x16x32<A_BF16>(vf, pl[t], acc[t][j]);
+      }
+    });
+    if (__any(any_bad)) {
+      // rare: which sums have a NaN among the values their row sees
+      u32x4 nan;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        nan[e] = (bad[e >> 1][2 * (e & 1)] ? 0x3F80u : 0u) | (bad[e >> 1][2 * (e & 1) + 1] ? 0x3F800000u : 0u);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        float seen[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) seen[e] = 32 * step + 16 * (e >> 2) + 4 * c + (e & 3) < sees[t] ? 1.f : 0.f;
+        // the count's row rho stands for the values NJ rho .. NJ rho + NJ - 1, which share their blocks
+        const f32x4 count = mfma16x16x32<A_BF16>(nan, bf16_high(seen), f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (count[i] > 0.f) acc[t][j][i] = __builtin_nanf("");
+      }
+    }
+  };
+
+  // ---- the tokens, one step's loads ahead ------------------------------------------------
+  constexpr int STRIDE = SHARE ? kAttnWaves : 1;
+  int step = begin + (SHARE ? wave : 0);
+  if (step < end) {
+    Step<D> now, next;
+    load(step, now);
+    for (; step < end; step += STRIDE) {
+      if (step + STRIDE < end) load(step + STRIDE, next);
+      compute(step, now);
+      now = next;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+  }
+
+  // ---- out: lane (r, c) has values NJ (4 c + i) + j of row r -----------------------------
+  const int64_t part_rows = a.rows;
+  auto store = [&](int row, int d, const float* v, float sum, float top) __attribute__((always_inline)) {
+    // eight (D = 64: four) values of a row, from d on
+    constexpr int N = NJ < 8 ? NJ : 8;
+    const int qi = row / a.group, head = hk * a.group + row - qi * a.group;
+    if (a.nsplit > 1) {
+      float* o = a.part + ((int64_t)split * part_rows + (q0 + qi) * a.q_heads + head) * D + d;
+#pragma unroll
+      for (int e = 0; e < N; e += 4) *(f32x4*)(o + e) = *(const f32x4*)(v + e);
+      if (d == 0) {
+        float* ml = a.part + (int64_t)a.nsplit * part_rows * D + ((int64_t)split * part_rows + (q0 + qi) * a.q_heads + head) * 2;
+        ml[0] = top;
+        ml[1] = sum;
+      }
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;          // a row that sees nothing: zeros
+      uint16_t* o = (uint16_t*)a.out + (q0 + qi) * a.out_stride + head * D + d;
+      uint32_t w[N / 2];
+#pragma unroll
+      for (int e = 0; e < N; e += 2) w[e / 2] = pack2<T == O_F16 ? A_F16 : A_BF16>(v[e] * inv, v[e + 1] * inv);
+      if constexpr (N == 8) *(u32x4*)o = u32x4{w[0], w[1], w[2], w[3]};
+      else *(u32x2*)o = u32x2{w[0], w[1]};
+    }
+  };
+  if constexpr (SHARE) {
+    // the waves' sums of the same rows, brought to one maximum, in the waves' order
+    static_assert(RT == 1, "one row tile");
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; j += 4)
+        *(f32x4*)&so[(wave * 16 + r) * OP + NJ * (4 * c + i) + j] = f32x4{acc[0][j][i], acc[0][j + 1][i], acc[0][j + 2][i], acc[0][j + 3][i]};
+    if (c == 0) {
+      sm[wave][r] = m[0];
+      sl[wave][r] = l[0];
+    }
+    __syncthreads();
+    constexpr int N = NJ < 8 ? NJ : 8, PIECES = D / N;
+    for (int i = tid; i < 16 * PIECES; i += 64 * kAttnWaves) {
+      const int row = i / PIECES, d = (i - row * PIECES) * N;
+      if (row0 + row >= row_count) continue;
+      float top = sm[0][row];
+#pragma unroll
+      for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, sm[w][row]);
+      float sum = 0.f, v[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        const float f = sm[w][row] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(sm[w][row] - top);
+        sum += sl[w][row] * f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = __builtin_fmaf(so[(w * 16 + row) * OP + d + e], f, v[e]);
+      }
+      store(row0 + row, d, v, sum, top);
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int row = row0 + 16 * t + r;
+      if (row >= row_count) continue;
+      constexpr int N = NJ < 8 ? NJ : 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; j += N) {
+          float v[N];
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] = acc[t][j + e][i];
+          store(row, NJ * (4 * c + i) + j, v, l[t], m[t]);
+        }
+    }
+  }
+}
+
+// The splits' sums of a row, brought to one maximum, in their order: D / 4 lanes per row, four values each.
+template <int T, int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+  constexpr int LPR = D / 4;
+  const int b = blockIdx.y;
+  int64_t q0 = b;
+  int nq = 1;
+  if (a.q_offsets) {
+    q0 = max(0, a.q_offsets[b]);
+    nq = min((int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0), a.max_q);
+  }
+  const int i = (int)blockIdx.x * (256 / LPR) + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
+  if (i >= nq * a.q_heads) return;
+  const int64_t row = q0 * a.q_heads + i;
+  const float* ml = a.part + (int64_t)a.nsplit * a.rows * D + row * 2;
+  float top = kNegInf;
+  for (int s = 0; s < a.nsplit; ++s) top = fmaxf(top, ml[(int64_t)s * a.rows * 2]);
+  float sum = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.nsplit; ++s) {
+    const float ms = ml[(int64_t)s * a.rows * 2];
+    const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - top);
+    sum += ml[(int64_t)s * a.rows * 2 + 1] * f;
+    v += *(const f32x4*)(a.part + ((int64_t)s * a.rows + row) * D + d) * f;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  constexpr int AF = T == O_F16 ? A_F16 : A_BF16;
+  const int qi = i / a.q_heads, head = i - qi * a.q_heads;
+  *(u32x2*)((uint16_t*)a.out + (q0 + qi) * a.out_stride + head * D + d) =
+      u32x2{pack2<AF>(v[0] * inv, v[1] * inv), pack2<AF>(v[2] * inv, v[3] * inv)};
+}
+
+// Row tiles of a wave where every wave has rows of its own: as many as its registers hold beside the sums.
+constexpr int many_rows(int type, int dim) { return dim == 64 ? 4 : (dim == 128 ? 4 : 2) / (type == O_BF16 ? 1 : 2); }
+
+template <int T, int D>
+void launch_one(const AttnArgs& a, hipStream_t st) {
+  constexpr int RT = many_rows(T, D);
+  const int64_t rows = (int64_t)a.max_q * a.group, heads = (int64_t)a.batch * a.kv_heads * a.nsplit;
+  if (rows <= 16) {
+    hipLaunchKernelGGL((attention_kernel<T, D, 1, true>), dim3((unsigned)(heads * ((rows + 15) / 16))), dim3(64 * kAttnWaves), 0, st, a);
+  } else {
+    constexpr int PER = 16 * RT * kAttnWaves;
+    hipLaunchKernelGGL((attention_kernel<T, D, RT, false>), dim3((unsigned)(heads * ((rows + PER - 1) / PER))), dim3(64 * kAttnWaves), 0,
+                       st, a);
+  }
+  if (a.nsplit > 1) {
+    constexpr int RPB = 256 / (D / 4);
+    const unsigned grid = (unsigned)(((int64_t)a.max_q * a.q_heads + RPB - 1) / RPB);
+    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3(grid, a.batch), dim3(256), 0, st, a);
+  }
+}
+
+}  // namespace
+
+// Parts of the cached tokens per tile: enough workgroups for the GPU, each with 256 tokens or more.
+int attn_splits(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
+  const int64_t rows = max_q * (q_heads / kv_heads);
+  const int64_t per = rows <= 16 ? 16 : 16 * kAttnWaves * many_rows(type, dim);
+  const int64_t tiles = batch * kv_heads * ((rows + per - 1) / per);
+  int64_t want = (1024 + tiles - 1) / tiles, most = (max_len + 255) / 256;
+  if (want > most) want = most;
+  return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+bool launch_attention(const AttnArgs& a, int type, hipStream_t st) {
+  if (a.dim == 64) type == O_BF16 ? launch_one<O_BF16, 64>(a, st) : launch_one<O_F16, 64>(a, st);
+  else if (a.dim == 128) type == O_BF16 ? launch_one<O_BF16, 128>(a, st) : launch_one<O_F16, 128>(a, st);
+  else if (a.dim == 256) type == O_BF16 ? launch_one<O_BF16, 256>(a, st) : launch_one<O_F16, 256>(a, st);
+  else return false;
+  return true;
+}
+
+}  // namespace qg

@@ -124,4 +124,67 @@ bool launch_grouped_map(const int32_t* arr, bool masked, int experts, int64_t ro
 void launch_moe_align(const int32_t* ids, int tk, int experts, int block_m, int32_t* sorted_ids, int64_t cap_sorted,
                       int32_t* expert_ids, int64_t cap_blocks, int32_t* num_post_pad, hipStream_t st);
 
+// Norms around a block (qg_norm.hip).  norm, post: 0 none, kNormRms or kNormLayer; code: 0 none, A_FP8, A_INT8 or
+// A_FP4; strides in elements.
+constexpr int kNormRms = 1, kNormLayer = 2;
+constexpr int64_t kNormRowMax = 1024 * 4 * 8;
+struct NormArgs {
+  const void *y, *res, *gate, *post_weight, *weight, *bias;
+  void *res_out, *out, *codes, *scale;
+  int64_t rows, k, y_stride, res_stride, out_stride, gate_stride;
+  int64_t row0;
+  int norm, post, code;
+  float eps, weight_offset, res_scale;
+};
+void launch_norm_rows(const NormArgs& a, int type, bool res32, hipStream_t st);
+
+// Low-rank adapters (qg_lora.hip); strides in elements.
+constexpr int kLoraMaxSlices = 8, kLoraMaxRank = 256;
+struct LoraArgs {
+  const void *x, *a, *b, *base;
+  void* y;
+  const int32_t *ranks, *sorted_ids, *expert_ids, *num_post_pad;
+  const float* scales;
+  float* part;               // [ksplit][cap_rows][rank_pitch]
+  int64_t x_stride, base_stride, y_stride, cap_rows;
+  int64_t n;
+  int tokens, k, max_rank, slices;
+  int rank_rows;             // of an adapter: slices * max_rank
+  int rank_pitch;            // rank_rows, padded to 16
+  int ksplit;
+  int col_tiles;             // of the second product
+  int slice_end[kLoraMaxSlices];
+};
+bool launch_lora(const LoraArgs& a, int type, int block_m, unsigned blocks, hipStream_t st);
+
+// The paged MXFP4 cache (qg_kv.hip) and the attention that reads it (qg_attention.hip).  A (page, head) has
+// `page` tokens of D values, laid out as the attention's lanes read them:
+//   keys    codes [page][D / 2], a token's codes in order, even values in the low nibbles
+//   values  codes [page / 4][D / 8][4] words of 8 codes: four tokens' codes of the same 8 values side by side
+//   keys    scales [page][D / 32];  values  scales [page / 4][D / 32][4]
+struct KvArgs {
+  const void *k, *v;         // rows in
+  void *k_out, *v_out;       // rows out
+  uint8_t* cache;
+  const int32_t* slots;
+  int64_t tokens, k_stride, v_stride, num_slots;
+  int heads, dim, page_shift;
+};
+void launch_kv_append(const KvArgs& a, int type, hipStream_t st);
+void launch_kv_read(const KvArgs& a, int type, hipStream_t st);
+inline int64_t kv_head_bytes(int64_t page, int64_t dim) { return page * (dim + dim / 16); }
+
+struct AttnArgs {
+  const uint8_t* cache;
+  const int32_t *table, *lens, *q_offsets;
+  const void* q;
+  void* out;
+  float* part;               // [split][row] sums of D values, then [split][row][2] maxima and sums of weights
+  int64_t table_stride, q_stride, out_stride, num_pages, tokens, rows;   // rows: tokens * q_heads
+  int batch, q_heads, kv_heads, group, dim, page_shift, max_q, max_len, nsplit;
+  float scale_log2;          // scale * log2(e)
+};
+int attn_splits(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type);
+bool launch_attention(const AttnArgs& a, int type, hipStream_t st);
+
 }  // namespace qg

@@ -1,0 +1,118 @@
+// Rows of keys and values into a paged cache in MXFP4, and back.
+//
+// A row's head of D values is D / 32 blocks, each one power of two (UE8M0) and 32 e2m1 codes, by the rule of
+// mxfp4_encode32: nothing is rounded but the values to their codes.  A block that is not finite keeps
+// the exponent byte of NaN.  A thread takes 8 values (one word of codes), four threads a block.
+//
+// Bound by bytes (4.1 of rows and 1.06 of codes per pair of values); a decoding batch by the launch.
+#include "qg_device.h"
+#include "qg_kernels.h"
+#include "qg_rows.h"
+
+namespace qg {
+
+namespace {
+
+template <int M>
+__device__ __forceinline__ float neighbour(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), M, 0xF, 0xF, true));
+}
+
+// Where 8 values (word w) of a token's head are: codes and exponent byte.
+struct KvPlace { uint8_t *codes, *scale; };
+__device__ __forceinline__ KvPlace place_of(const KvArgs& a, bool value, int64_t slot, int head, int w) {
+  const int page = 1 << a.page_shift, dim = a.dim;
+  const int64_t half = (int64_t)page * (dim / 2), tail = (int64_t)page * (dim / 32);
+  uint8_t* const base = a.cache + ((slot >> a.page_shift) * a.heads + head) * (2 * (half + tail));
+  const int t = (int)(slot & (page - 1));
+  KvPlace p;
+  if (value) {
+    p.codes = base + half + (((int64_t)(t >> 2) * (dim / 8) + w) * 4 + (t & 3)) * 4;
+    p.scale = base + 2 * half + tail + ((t >> 2) * (dim / 32) + (w >> 2)) * 4 + (t & 3);
+  } else {
+    p.codes = base + (int64_t)t * (dim / 2) + 4 * w;
+    p.scale = base + 2 * half + t * (dim / 32) + (w >> 2);
+  }
+  return p;
+}
+
+// Thread i: token i / per, then (keys or values, head, word).
+template <int T>
+__global__ __launch_bounds__(256) void kv_append_kernel(KvArgs a) {
+  const int words = a.dim >> 3, half = a.heads * words, per = 2 * half;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t token = i / per;
+  if (token >= a.tokens) return;
+  const int c = (int)(i - token * per);
+  const bool value = c >= half;
+  const int hw = value ? c - half : c, head = hw / words, w = hw - head * words;
+  const int64_t slot = a.slots[token];
+  float v[8];
+  unpack8<T>(ldg16(value ? (const uint16_t*)a.v + token * a.v_stride + 8 * hw : (const uint16_t*)a.k + token * a.k_stride + 8 * hw), v);
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(v[e]));
+  amax = __builtin_elementwise_maximum(amax, neighbour<0xB1>(amax));
+  amax = __builtin_elementwise_maximum(amax, neighbour<0x4E>(amax));
+  uint32_t codes;
+  const uint32_t e8 = mxfp4_encode8(v, amax, codes);
+  if (slot < 0 || slot >= a.num_slots) return;
+  const KvPlace p = place_of(a, value, slot, head, w);
+  *(uint32_t*)p.codes = codes;
+  if ((w & 3) == 0) *p.scale = (uint8_t)e8;
+}
+
+template <int T>
+__global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a) {
+  constexpr int AF = T == O_F16 ? A_F16 : A_BF16;
+  const int words = a.dim >> 3, half = a.heads * words, per = 2 * half;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t token = i / per;
+  if (token >= a.tokens) return;
+  const int c = (int)(i - token * per);
+  const bool value = c >= half;
+  const int hw = value ? c - half : c, head = hw / words, w = hw - head * words;
+  const int64_t slot = a.slots[token];
+  u32x4 o = {0, 0, 0, 0};
+  if (slot >= 0 && slot < a.num_slots) {
+    const KvPlace p = place_of(a, value, slot, head, w);
+    o = fp4_to_16<AF>(*(const uint32_t*)p.codes, scale_bits_to_f32<S_UE8M0>(*p.scale));
+  }
+  uint16_t* const row = (uint16_t*)(value ? a.v_out : a.k_out) + token * (int64_t)(a.heads * a.dim);
+  *(u32x4*)(row + 8 * hw) = o;
+}
+
+}  // namespace
+
+// a launch takes fewer than 2^32 threads
+template <typename F>
+static void in_parts(const KvArgs& all, int type, F one) {
+  const int64_t per = (int64_t)2 * all.heads * (all.dim / 8), most = ((int64_t)1 << 31) / per;
+  for (int64_t t = 0; t < all.tokens; t += most) {
+    KvArgs a = all;
+    a.tokens = all.tokens - t < most ? all.tokens - t : most;
+    a.slots += t;
+    const int64_t width = (int64_t)all.heads * all.dim;
+    if (a.k) a.k = (const uint16_t*)a.k + t * a.k_stride;
+    if (a.v) a.v = (const uint16_t*)a.v + t * a.v_stride;
+    if (a.k_out) a.k_out = (uint16_t*)a.k_out + t * width;
+    if (a.v_out) a.v_out = (uint16_t*)a.v_out + t * width;
+    one(a, dim3((unsigned)((a.tokens * per + 255) / 256)));
+  }
+}
+
+void launch_kv_append(const KvArgs& a, int type, hipStream_t st) {
+  in_parts(a, type, [&](const KvArgs& p, dim3 grid) {
+    if (type == O_BF16) hipLaunchKernelGGL(kv_append_kernel<O_BF16>, grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL(kv_append_kernel<O_F16>, grid, dim3(256), 0, st, p);
+  });
+}
+
+void launch_kv_read(const KvArgs& a, int type, hipStream_t st) {
+  in_parts(a, type, [&](const KvArgs& p, dim3 grid) {
+    if (type == O_BF16) hipLaunchKernelGGL(kv_read_kernel<O_BF16>, grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL(kv_read_kernel<O_F16>, grid, dim3(256), 0, st, p);
+  });
+}
+
+}  // namespace qg
