@@ -237,7 +237,8 @@ static qg_status check_attention(const qg_kv_desc* d, int32_t q_heads, int64_t b
 size_t qg_attention_workspace_bytes(const qg_kv_desc* d, int32_t q_heads, int64_t batch, int64_t max_q, int64_t tokens,
                                     int64_t max_len) {
   if (check_attention(d, q_heads, batch, max_q, tokens, max_len) != QG_OK || batch == 0) return 0;
-  const int splits = attn_splits(batch, q_heads, d->kv_heads, max_q, max_len, d->head_dim, d->type == QG_O_F16 ? O_F16 : O_BF16);
+  const int splits =
+      attn_split(batch, q_heads, d->kv_heads, max_q, max_len, d->head_dim, d->type == QG_O_F16 ? O_F16 : O_BF16).parts;
   return splits > 1 ? (size_t)splits * (size_t)tokens * (size_t)q_heads * (size_t)(d->head_dim + 2) * sizeof(float) : 0;
 }
 
@@ -259,12 +260,15 @@ qg_status qg_attention(const qg_kv_desc* d, const void* q, int64_t q_stride, int
       (((uintptr_t)block_table | (uintptr_t)seq_lens | (uintptr_t)q_offsets) & 3u) != 0)
     return QG_ERR_INVALID_ARG;
   const int type = d->type == QG_O_F16 ? O_F16 : O_BF16;
-  a.nsplit = attn_splits(batch, q_heads, d->kv_heads, max_q, max_len, d->head_dim, type);
+  const AttnSplit split = attn_split(batch, q_heads, d->kv_heads, max_q, max_len, d->head_dim, type);
+  a.nsplit = split.parts;
+  a.chunk = split.chunk;
   if (a.nsplit > 1 &&
       (!ws || !aligned16(ws) || ws_bytes < qg_attention_workspace_bytes(d, q_heads, batch, max_q, tokens, max_len)))
     return QG_ERR_WORKSPACE;
   a.group = q_heads / d->kv_heads;
-  if (batch * d->kv_heads * a.nsplit * ((max_q * a.group + 15) / 16) > (1 << 23)) return QG_ERR_UNSUPPORTED;   // < 2^32 threads
+  if (batch * d->kv_heads * a.nsplit * ((max_q * a.group + 15) / 16) > (1 << 23) || max_q * q_heads >= (1 << 24))
+    return QG_ERR_UNSUPPORTED;                      // launches of fewer than 2^32 threads
   s = check_arch();
   if (s != QG_OK) return s;
   a.cache = (const uint8_t*)cache; a.table = block_table; a.lens = seq_lens; a.q_offsets = q_offsets;
@@ -272,7 +276,8 @@ qg_status qg_attention(const qg_kv_desc* d, const void* q, int64_t q_stride, int
   a.table_stride = table_stride; a.num_pages = d->num_pages; a.tokens = tokens; a.rows = tokens * q_heads;
   a.batch = (int)batch; a.q_heads = q_heads; a.kv_heads = d->kv_heads; a.dim = d->head_dim;
   a.page_shift = log2_of(d->page_tokens); a.max_q = (int)max_q; a.max_len = (int)max_len;
-  a.scale_log2 = scale * 1.44269504088896f;
+  a.scale_log2 = fabsf(scale) * 1.44269504088896f;
+  a.q_sign = scale < 0 ? 0x80008000u : 0;
   QG_LOG("attention batch=%lld heads=%d/%d dim=%d max_q=%lld max_len=%lld -> splits=%d", (long long)batch, q_heads,
          d->kv_heads, d->head_dim, (long long)max_q, (long long)max_len, a.nsplit);
   if (!launch_attention(a, type, (hipStream_t)stream)) return QG_ERR_UNSUPPORTED;

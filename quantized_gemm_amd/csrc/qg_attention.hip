@@ -19,6 +19,7 @@
 //
 // The maximum only moves when a score is more than 2^8 times above it: weights stay below 2^8 and the exchange
 // between lanes and the rescaling of O are rare.
+#include <algorithm>
 #include <type_traits>
 
 #include "qg_device.h"
@@ -30,6 +31,7 @@ namespace qg {
 namespace {
 
 constexpr int kAttnWaves = 4;
+constexpr int kMaxParts = 64;
 constexpr float kLazy = 8.0f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -49,11 +51,9 @@ template <int B>
 __device__ __forceinline__ uint32_t cvt_pair(uint32_t w, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
 }
-// UE8M0 byte b of a word -> its power of two; 0 is 2^-127, 255 NaN.
-__device__ __forceinline__ float power_of(uint32_t word, int b) {
-  const uint32_t e = (word >> (8 * b)) & 0xFFu;
-  return __uint_as_float(e == 255 ? 0x7FC00000u : max(e << 23, 0x00400000u));
-}
+// UE8M0 byte b of a word -> the conversion's scale.  It takes the exponent field alone: 0 is 2^-127, 255 NaN.
+__device__ __forceinline__ uint32_t power_bits(uint32_t word, int b) { return ((word >> (8 * b)) & 0xFFu) << 23; }
+constexpr uint32_t kNanPower = 0x7F800000u;
 
 // What a lane loads of a step: 32 tokens.
 template <int D>
@@ -67,8 +67,12 @@ struct Step {
   bool ok[2];                                       // the tile's page is in the cache
 };
 
+// Parts that `steps` steps are taken in, `chunk` steps each; a row that sees nothing is one part.
+__device__ __forceinline__ int parts_of(int steps, int chunk) { return max(1, (steps + chunk - 1) / chunk); }
+
+// (two waves per SIMD at least: with 256 registers or fewer the sums stay where the vector unit reads them)
 template <int T, int D, int RT, bool SHARE>
-__global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(SHARE ? 2 : 1))) void attention_kernel(AttnArgs a) {
   constexpr bool HILO = T == O_F16;
   constexpr int KW = D / 32, NJ = D / 16;           // MFMAs of a score tile; tiles of 16 output values
   constexpr int OP = D + 4;
@@ -107,8 +111,9 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
   const int last_row = min(row0 + 16 * RT, row_count) - 1;
   const int most = __builtin_amdgcn_readfirstlane(max(0, len - nq + last_row / a.group + 1));
   const int least = __builtin_amdgcn_readfirstlane(max(0, len - nq + row0 / a.group + 1));
-  const int steps = (most + 31) / 32, per = (steps + a.nsplit - 1) / a.nsplit;
-  const int begin = split * per, end = min(steps, begin + per);
+  const int steps = (most + 31) / 32, parts = parts_of(steps, a.chunk);
+  if (split >= parts) return;                       // (the same for all waves that share rows)
+  const int begin = split * a.chunk, end = min(steps, begin + a.chunk);
 
   // ---- queries ---------------------------------------------------------------------------
   u32x4 qf[RT][KW], ql[HILO ? RT : 1][HILO ? KW : 1];
@@ -119,7 +124,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
     const uint16_t* p = (const uint16_t*)a.q + (q0 + qrow[t]) * a.q_stride + head * D + c * (D / 4);
 #pragma unroll
     for (int j = 0; j < KW; ++j) {
-      qf[t][j] = ldg16(p + 8 * j);
+      qf[t][j] = ldg16(p + 8 * j) ^ a.q_sign;
       if constexpr (HILO) {
         float v[8];
         unpack8<O_F16>(qf[t][j], v);
@@ -133,40 +138,50 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
   const int64_t half = (int64_t)page * (D / 2), tail = (int64_t)page * (D / 32), head_bytes = 2 * (half + tail);
   const int32_t* const table = a.table + (int64_t)b * a.table_stride;
   const int last_page = max(0, len - 1) >> a.page_shift;
-  auto load = [&](int step, Step<D>& s) __attribute__((always_inline)) {
+  constexpr int STRIDE = SHARE ? kAttnWaves : 1;
+  const int first = begin + (SHARE ? wave : 0), count = first < end ? (end - first + STRIDE - 1) / STRIDE : 0;   // this wave's steps
+  const uint32_t k_at = r * (D / 2) + c * (D / 8), ks_at = r * (D / 32) + (D == 256 ? 2 * c : D == 128 ? c : c >> 1);
+  const uint32_t v_at = c * (2 * D) + 16 * (D == 256 ? 2 * r : D == 128 ? r : r >> 1);
+  const uint32_t vs_at = 4 * (c * (D / 32) + (D == 256 ? r >> 1 : D == 128 ? r >> 2 : r >> 3));
+  // page of half h of this wave's step n, in lane 2 (n - ids0) + h: the loads of a step wait for no other load
+  int ids = 0, ids0 = 0;
+  auto load_ids = [&](int n0) __attribute__((always_inline)) {
+    ids0 = n0;
+    const int t0 = 32 * (first + STRIDE * min(n0 + (lane >> 1), count - 1)) + 16 * (lane & 1);
+    ids = table[min(t0 >> a.page_shift, last_page)];
+  };
+  auto load = [&](int n, Step<D>& s) __attribute__((always_inline)) {
+    n = min(n, count - 1);                          // (past the end: the last once more)
+    const int step = first + STRIDE * n;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t0 = 32 * step + 16 * h;
-      const int id = table[min(t0 >> a.page_shift, last_page)];
+      const int id = __builtin_amdgcn_readlane(ids, 2 * (n - ids0) + h);
       s.ok[h] = id >= 0 && id < a.num_pages;
-      const uint8_t* base = a.cache + ((int64_t)(s.ok[h] ? id : 0) * a.kv_heads + hk) * head_bytes;
+      // (wave-uniform addresses, and per lane the offsets that stay)
       const int t = t0 & (page - 1);
-      const uint8_t* kp = base + (t + r) * (D / 2) + c * (D / 8);
+      const uint8_t* const base = a.cache + ((int64_t)(s.ok[h] ? id : 0) * a.kv_heads + hk) * head_bytes;
+      const uint8_t* const kb = base + t * (D / 2);
+      const uint8_t* const vb = base + half + t * (D / 2);
+      const uint8_t* const ksb = base + 2 * half + t * (D / 32);
+      const uint8_t* const vsb = base + 2 * half + tail + t * (D / 32);
       if constexpr (KW == 2) {
-        const u32x2 w = *(const u32x2*)kp;
+        const u32x2 w = *(const u32x2*)(kb + k_at);
         s.k[h][0] = w[0];
         s.k[h][1] = w[1];
       } else {
 #pragma unroll
         for (int j = 0; j < KW; j += 4) {
-          const u32x4 w = ldg16(kp + 4 * j);
+          const u32x4 w = ldg16(kb + k_at + 4 * j);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s.k[h][j + e] = w[e];
         }
       }
-      const uint8_t* ksp = base + 2 * half + (t + r) * (D / 32);
-      if constexpr (D == 256) s.ks[h] = *(const uint16_t*)(ksp + 2 * c);
-      else s.ks[h] = ksp[D == 128 ? c : c >> 1];
-      const int t4 = (t >> 2) + c;
-      const uint8_t* vp = base + half + (int64_t)t4 * (D / 8) * 16;
-      if constexpr (D == 256) {
-        s.v[h][0] = ldg16(vp + 32 * r);
-        s.v[h][1] = ldg16(vp + 32 * r + 16);
-      } else {
-        s.v[h][0] = ldg16(vp + 16 * (D == 128 ? r : r >> 1));
-      }
-      const int blk = D == 256 ? r >> 1 : D == 128 ? r >> 2 : r >> 3;
-      s.vs[h] = *(const uint32_t*)(base + 2 * half + tail + (t4 * (D / 32) + blk) * 4);
+      if constexpr (D == 256) s.ks[h] = *(const uint16_t*)(ksb + ks_at);
+      else s.ks[h] = ksb[ks_at];
+      s.v[h][0] = ldg16(vb + v_at);
+      if constexpr (D == 256) s.v[h][1] = ldg16(vb + v_at + 16);
+      s.vs[h] = *(const uint32_t*)(vsb + vs_at);
     }
   };
 
@@ -188,7 +203,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
       u32x4 kf[KW];
 #pragma unroll
       for (int j = 0; j < KW; ++j) {
-        const float p = power_of(s.ks[h], D == 256 ? j >> 2 : 0);
+        const float p = __uint_as_float(power_bits(s.ks[h], D == 256 ? j >> 2 : 0));
         kf[j] = u32x4{cvt_pair<0>(s.k[h][j], p), cvt_pair<1>(s.k[h][j], p), cvt_pair<2>(s.k[h][j], p), cvt_pair<3>(s.k[h][j], p)};
       }
 #pragma unroll
@@ -199,7 +214,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
           x = mfma16x16x32<A_BF16>(kf[j], qf[t][j], x);
           if constexpr (HILO) x = mfma16x16x32<A_BF16>(kf[j], ql[t][j], x);
         }
-        sc[t][h] = x * a.scale_log2;
+        sc[t][h] = x;
       }
     }
     const bool cut = 32 * step + 32 > least || !s.ok[0] || !s.ok[1];   // some row does not see some of the tokens
@@ -219,7 +234,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
       float top = sc[t][0][0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, sc[t][e >> 2][e & 3]);
-      if (__any(top > m[t] + kLazy || (m[t] == kNegInf && top > kNegInf))) {
+      top *= a.scale_log2;
+      if (__any(top > m[t] + kLazy)) {              // (from -inf on, too)
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
         const float up = fmaxf(m[t], top);
@@ -233,27 +249,27 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
       float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(sc[t][e >> 2][e & 3] - base);
+        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][e >> 2][e & 3], a.scale_log2, -base));
         l[t] += p[e];
       }
       pf[t] = bf16_high(p);
       if constexpr (HILO) pl[t] = bf16_low(p, pf[t]);
     }
     // values: tokens that some row does not see must not reach its sums, weight 0 or not
-    float vp[2][4];
+    uint32_t vp[2][4];
     bool bad[2][4];
     bool any_bad = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        vp[h][i] = power_of(s.vs[h], i);
+        vp[h][i] = power_bits(s.vs[h], i);
         bad[h][i] = false;
         if (cut) {
           const int tok = 32 * step + 16 * h + 4 * c + i;
-          if (!s.ok[h] || tok >= most) vp[h][i] = 0.f;                  // seen by no row: what is there does not matter
-          bad[h][i] = vp[h][i] != vp[h][i];                             // seen by some: its NaN goes to those only
-          if (bad[h][i]) vp[h][i] = 0.f;
+          if (!s.ok[h] || tok >= most) vp[h][i] = 0;                    // seen by no row: what is there does not matter
+          bad[h][i] = vp[h][i] == kNanPower;                            // seen by some: its NaN goes to those only
+          if (bad[h][i]) vp[h][i] = 0;
           any_bad |= bad[h][i];
         }
       }
@@ -272,7 +288,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[h][i] = cvt_pair<B>(word[h][i], vp[h][i]);
+            for (int i = 0; i < 4; ++i) x[h][i] = cvt_pair<B>(word[h][i], __uint_as_float(vp[h][i]));
           u32x4 even, odd;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -319,16 +335,32 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
     }
   };
 
-  // ---- the tokens, one step's loads ahead ------------------------------------------------
-  constexpr int STRIDE = SHARE ? kAttnWaves : 1;
-  int step = begin + (SHARE ? wave : 0);
-  if (step < end) {
-    Step<D> now, next;
-    load(step, now);
-    for (; step < end; step += STRIDE) {
-      if (step + STRIDE < end) load(step + STRIDE, next);
-      compute(step, now);
-      now = next;
+  // ---- the tokens, two steps' loads ahead (where registers allow) ------------------------
+  constexpr bool TWO = D < 256 && RT == 1;
+  if (count > 0) {
+    Step<D> s0, s1;
+    load_ids(0);
+    load(0, s0);
+    if constexpr (TWO) {
+      Step<D> s2;
+      load(1, s1);
+      for (int n = 0; n < count; n += 3) {
+        if (n - ids0 >= 27) load_ids(n);            // (32 steps' pages at a time, of which this turn takes five)
+        load(n + 2, s2);
+        compute(first + STRIDE * n, s0);
+        load(n + 3, s0);
+        if (n + 1 < count) compute(first + STRIDE * (n + 1), s1);
+        load(n + 4, s1);
+        if (n + 2 < count) compute(first + STRIDE * (n + 2), s2);
+      }
+    } else {
+      for (int n = 0; n < count; n += 2) {
+        if (n - ids0 >= 29) load_ids(n);
+        load(n + 1, s1);
+        compute(first + STRIDE * n, s0);
+        load(n + 2, s0);
+        if (n + 1 < count) compute(first + STRIDE * (n + 1), s1);
+      }
     }
   }
 #pragma unroll
@@ -343,7 +375,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
     // eight (D = 64: four) values of a row, from d on
     constexpr int N = NJ < 8 ? NJ : 8;
     const int qi = row / a.group, head = hk * a.group + row - qi * a.group;
-    if (a.nsplit > 1) {
+    if (parts > 1) {
       float* o = a.part + ((int64_t)split * part_rows + (q0 + qi) * a.q_heads + head) * D + d;
 #pragma unroll
       for (int e = 0; e < N; e += 4) *(f32x4*)(o + e) = *(const f32x4*)(v + e);
@@ -413,69 +445,92 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attention_kernel(AttnArgs a) 
   }
 }
 
-// The splits' sums of a row, brought to one maximum, in their order: D / 4 lanes per row, four values each.
+// A row's parts, brought to one maximum, in a fixed order.  One workgroup per row: D / 4 threads take four values
+// each, 1024 / D groups of them every so many-th part, so that a long sequence's parts are read side by side.
 template <int T, int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-  constexpr int LPR = D / 4;
-  const int b = blockIdx.y;
+  constexpr int LPR = D / 4, GROUPS = 256 / LPR;
+  __shared__ float weight[kMaxParts];
+  __shared__ __attribute__((aligned(16))) float sums[GROUPS][D];
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
   int64_t q0 = b;
   int nq = 1;
   if (a.q_offsets) {
     q0 = max(0, a.q_offsets[b]);
     nq = min((int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0), a.max_q);
   }
-  const int i = (int)blockIdx.x * (256 / LPR) + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
-  if (i >= nq * a.q_heads) return;
-  const int64_t row = q0 * a.q_heads + i;
+  const int qi = (int)blockIdx.x / a.q_heads, head = (int)blockIdx.x - qi * a.q_heads;
+  if (qi >= nq) return;
+  // as many parts as the row's tile was taken in
+  const int row_count = nq * a.group, in_group = qi * a.group + head % a.group;
+  const int last_row = min((in_group / a.tile_rows + 1) * a.tile_rows, row_count) - 1;
+  const int len = max(0, min(a.lens[b], a.max_len));
+  const int most = max(0, len - nq + last_row / a.group + 1);
+  const int parts = parts_of((most + 31) / 32, a.chunk);
+  if (parts == 1) return;                           // written already
+  const int64_t row = (q0 + qi) * a.q_heads + head;
   const float* ml = a.part + (int64_t)a.nsplit * a.rows * D + row * 2;
-  float top = kNegInf;
-  for (int s = 0; s < a.nsplit; ++s) top = fmaxf(top, ml[(int64_t)s * a.rows * 2]);
-  float sum = 0.f;
+  // every wave: maximum and sum of all parts (64 or fewer, one per lane)
+  const float ms = lane < parts ? ml[(int64_t)lane * a.rows * 2] : kNegInf;
+  const float ls = lane < parts ? ml[(int64_t)lane * a.rows * 2 + 1] : 0.f;
+  float top = ms;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - top);
+  float sum = ls * f;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (tid < 64) weight[lane] = f;
+  __syncthreads();
+  const int g = tid / LPR, d = (tid % LPR) * 4;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float ms = ml[(int64_t)s * a.rows * 2];
-    const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - top);
-    sum += ml[(int64_t)s * a.rows * 2 + 1] * f;
-    v += *(const f32x4*)(a.part + ((int64_t)s * a.rows + row) * D + d) * f;
-  }
+#pragma unroll 4
+  for (int s = g; s < parts; s += GROUPS) v += *(const f32x4*)(a.part + ((int64_t)s * a.rows + row) * D + d) * weight[s];
+  *(f32x4*)&sums[g][d] = v;
+  __syncthreads();
+  if (g != 0) return;
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) v += *(const f32x4*)&sums[i][d];
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   constexpr int AF = T == O_F16 ? A_F16 : A_BF16;
-  const int qi = i / a.q_heads, head = i - qi * a.q_heads;
   *(u32x2*)((uint16_t*)a.out + (q0 + qi) * a.out_stride + head * D + d) =
       u32x2{pack2<AF>(v[0] * inv, v[1] * inv), pack2<AF>(v[2] * inv, v[3] * inv)};
 }
 
 // Row tiles of a wave where every wave has rows of its own: as many as its registers hold beside the sums.
+constexpr bool shares_rows(int64_t rows) { return rows <= 16; }
 constexpr int many_rows(int type, int dim) { return dim == 64 ? 4 : (dim == 128 ? 4 : 2) / (type == O_BF16 ? 1 : 2); }
 
 template <int T, int D>
-void launch_one(const AttnArgs& a, hipStream_t st) {
+void launch_one(AttnArgs a, hipStream_t st) {
   constexpr int RT = many_rows(T, D);
   const int64_t rows = (int64_t)a.max_q * a.group, heads = (int64_t)a.batch * a.kv_heads * a.nsplit;
-  if (rows <= 16) {
+  if (shares_rows(rows)) {
+    a.tile_rows = 16;
     hipLaunchKernelGGL((attention_kernel<T, D, 1, true>), dim3((unsigned)(heads * ((rows + 15) / 16))), dim3(64 * kAttnWaves), 0, st, a);
   } else {
     constexpr int PER = 16 * RT * kAttnWaves;
+    a.tile_rows = 16 * RT;
     hipLaunchKernelGGL((attention_kernel<T, D, RT, false>), dim3((unsigned)(heads * ((rows + PER - 1) / PER))), dim3(64 * kAttnWaves), 0,
                        st, a);
   }
-  if (a.nsplit > 1) {
-    constexpr int RPB = 256 / (D / 4);
-    const unsigned grid = (unsigned)(((int64_t)a.max_q * a.q_heads + RPB - 1) / RPB);
-    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3(grid, a.batch), dim3(256), 0, st, a);
-  }
+  if (a.nsplit > 1)
+    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(a.max_q * a.q_heads), a.batch), dim3(256), 0, st, a);
 }
 
 }  // namespace
 
-// Parts of the cached tokens per tile: enough workgroups for the GPU, each with 256 tokens or more.
-int attn_splits(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
+// Parts of 32 * chunk tokens: of equal work whatever the sequences' lengths, as many as fill the GPU if all sequences had the
+// maximum, none shorter than 512 tokens (what a part costs beside its tokens).
+AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
   const int64_t rows = max_q * (q_heads / kv_heads);
-  const int64_t per = rows <= 16 ? 16 : 16 * kAttnWaves * many_rows(type, dim);
-  const int64_t tiles = batch * kv_heads * ((rows + per - 1) / per);
-  int64_t want = (1024 + tiles - 1) / tiles, most = (max_len + 255) / 256;
-  if (want > most) want = most;
-  return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+  const bool share = shares_rows(rows);
+  const int64_t per = share ? 16 : 16 * kAttnWaves * many_rows(type, dim);
+  const int64_t tiles = batch * kv_heads * ((rows + per - 1) / per), steps = std::max<int64_t>(1, (max_len + 31) / 32);
+  const int64_t want = share ? 4096 : 1024;
+  int64_t chunk = std::max({steps * tiles / want, (int64_t)16, (steps + kMaxParts - 1) / kMaxParts});
+  chunk = std::min((chunk + 3) / 4 * 4, (steps + 3) / 4 * 4);
+  return AttnSplit{(int)((steps + chunk - 1) / chunk), (int)chunk};
 }
 
 bool launch_attention(const AttnArgs& a, int type, hipStream_t st) {

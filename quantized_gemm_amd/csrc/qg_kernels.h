@@ -181,10 +181,14 @@ struct AttnArgs {
   void* out;
   float* part;               // [split][row] sums of D values, then [split][row][2] maxima and sums of weights
   int64_t table_stride, q_stride, out_stride, num_pages, tokens, rows;   // rows: tokens * q_heads
-  int batch, q_heads, kv_heads, group, dim, page_shift, max_q, max_len, nsplit;
-  float scale_log2;          // scale * log2(e)
+  int batch, q_heads, kv_heads, group, dim, page_shift, max_q, max_len;
+  int nsplit, chunk;         // parts at most, and steps of 32 tokens of a part
+  int tile_rows;             // rows of a wave
+  float scale_log2;          // |scale| * log2(e)
+  uint32_t q_sign;           // 0x80008000 where scale is negative: turned into the queries
 };
-int attn_splits(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type);
+struct AttnSplit { int parts, chunk; };
+AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type);
 bool launch_attention(const AttnArgs& a, int type, hipStream_t st);
 
 }  // namespace qg

@@ -85,21 +85,23 @@ __device__ __forceinline__ uint32_t e4m3_codes_divided(const float* v, float sc)
   return e4m3_of(q);
 }
 
-// MXFP4 codes of 8 of a block's 32 values, whose largest magnitude (of all 32) is amax: see mxfp4_encode32.
+// MXFP4 codes of 8 of a block's 32 values, whose largest magnitude (of all 32) is amax: the rule of mxfp4_encode32.  The
+// conversion divides by the power of two and rounds to the nearest code, halves to the even one, 6 at most; it keeps
+// the sign of values that round to zero, which is taken out.
 // Returns the UE8M0 byte; a block that is not finite has the byte of NaN (255) and codes 0.
 __device__ __forceinline__ uint32_t mxfp4_encode8(const float* v, float amax, uint32_t& codes) {
   codes = 0;
   if (!(amax < __builtin_inff())) return 255;
+  // (exponents below -126 would need scales that float32 holds as subnormals: brought up by 2^32 first)
   const int e = amax > 0.f ? max(-127, min(127, __builtin_amdgcn_frexp_expf(amax) - 3)) : -127;
-#pragma unroll
-  for (int h = 0; h < 8; ++h) {
-    const float q = __builtin_ldexpf(v[h], -e);
-    const float m = fabsf(q);
-    uint32_t c = (uint32_t)(m > 0.25f) + (uint32_t)(m >= 0.75f) + (uint32_t)(m > 1.25f) + (uint32_t)(m >= 1.75f) +
-                 (uint32_t)(m > 2.5f) + (uint32_t)(m >= 3.5f) + (uint32_t)(m > 5.0f);
-    if (q < 0.f && c != 0) c |= 8u;
-    codes |= c << (4 * h);
-  }
+  const bool low = e < -126;
+  const float up = low ? 0x1p32f : 1.0f, s = __uint_as_float((uint32_t)(e + 127 + (low ? 32 : 0)) << 23);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0] * up, v[1] * up, s, 0);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2] * up, v[3] * up, s, 1);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[4] * up, v[5] * up, s, 2);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[6] * up, v[7] * up, s, 3);
+  const uint32_t some = (codes | (codes >> 1) | (codes >> 2)) & 0x11111111u;      // bit 0 of each code that is not zero
+  codes &= 0x77777777u | (some << 3);
   return (uint32_t)(e + 127);
 }
 

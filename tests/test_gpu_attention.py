@@ -71,6 +71,29 @@ def test_append_and_read_back_are_exact(dim, page, dtype):
     assert torch.equal(before, cache)
 
 
+def test_powers_of_two_at_the_ends_of_the_range():
+    # bf16 blocks of every exponent it has, subnormal ones too, and rounding at every border of every code
+    d = qg.make_kv_desc(qg.O_BF16, 1, 64, 256, 2)
+    cache = torch.zeros(qg.kv_cache_bytes(d), dtype=torch.uint8, device="cuda")
+    n = 280
+    m = np.array([4.0, 7.96875, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.251, 0.749, 1.251, 1.749, 2.51, 3.49, 5.03])
+    row = np.concatenate([m, -m, m[::-1], -m])
+    x = torch.from_numpy(row[None, :] * np.exp2(np.arange(n)[:, None] - 150.0)).to(torch.bfloat16).cuda()   # (the largest: infinite)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    qg.kv_append(d, x, x, slots, n, cache)
+    back = [torch.empty((n, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    qg.kv_read(d, cache, slots, n, *back)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        want = LO.mxfp4_values(_d(x))
+    finite = np.isfinite(_d(x)).all(axis=1)
+    assert finite.sum() > 270
+    # (a code of 2^-127 may be half of bf16's smallest number: compared as bf16 rounds it)
+    want = torch.from_numpy(want).to(torch.bfloat16).double().numpy()
+    for b in back:
+        assert np.array_equal(_d(b)[finite], want[finite])
+
+
 def test_append_writes_its_slots_only():
     d = qg.make_kv_desc(qg.O_BF16, 2, 64, 16, 5)
     rng = np.random.default_rng(1)
