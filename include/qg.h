@@ -485,7 +485,7 @@ qg_status qg_norm_rows(const qg_norm_desc* desc, int64_t rows, const void* y, co
  *              token (topk 1, num_experts = num_adapters, block_m); the same map serves every product of a step.
  *              Tokens whose id is outside [0, num_adapters) have no adapter: their rows of y are not written.
  *   base, y    device rows of n, base_stride and y_stride apart: the shared product's output; y may be base
- *   block_m    16 or 64; qg_lora_block_m gives the better one for a batch
+ *   block_m    16, 64 or 128; qg_lora_block_m gives the best for a batch
  *   ws         qg_lora_workspace_bytes(desc, tokens, block_m) bytes
  * The result does not depend on where in the batch a token stands; it does, in its last bits, on the batch's size,
  * which sets how K is split.  max_rank <= 256 and a multiple of 8, num_adapters <= 512, num_slices <= 8, n % 8 == 0,
@@ -546,6 +546,7 @@ qg_status qg_kv_read(const qg_kv_desc* desc, const void* cache, const int32_t* s
  *                out, at most max_q of them; NULL: one query per sequence (max_q 1, tokens == batch)
  *   tokens       rows of q and out.  Rows that belong to no sequence are neither read nor written.
  *   ws           qg_attention_workspace_bytes(...) bytes (0: none needed)
+ * q_heads is a multiple of kv_heads, at most 256 times it; batch and max_q <= 65535.
  * The result depends on batch, max_q and max_len (which set how the tokens are split) in its last bits only.
  */
 size_t qg_attention_workspace_bytes(const qg_kv_desc* desc, int32_t q_heads, int64_t batch, int64_t max_q, int64_t tokens,

@@ -16,6 +16,12 @@ namespace {
 constexpr int64_t kMaxStride = (int64_t)1 << 32;
 constexpr int kCUs = 256;
 
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
 bool type16(int32_t t) { return t == QG_O_F16 || t == QG_O_BF16; }
 
 // A row stride in elements: 0 means `width`; else at least that, in steps of 8 (16 bytes and more).
@@ -51,13 +57,17 @@ qg_status check_lora(const qg_lora_desc* d) {
   return d->slice_end[d->num_slices - 1] == d->n ? QG_OK : QG_ERR_INVALID_ARG;
 }
 
-// Parts of K: enough workgroups for the GPU, each with 512 of K (two lines of every row per wave) or more.
-int lora_split(const qg_lora_desc* d, int64_t tokens, int64_t block_m) {
-  const int64_t rows = (int64_t)d->num_slices * d->max_rank;
-  const int64_t blocks = std::max<int64_t>(1, tokens / block_m) * ((rows + 63) / 64);
-  int64_t sp = 1;
-  while (sp < 16 && blocks * sp < 2 * kCUs && d->k >= 512 * (sp * 2)) sp *= 2;
-  return (int)sp;
+bool lora_block(int32_t m) { return m == 16 || m == 64 || m == 128; }
+
+// Parts of K, each of 512 (blocks of 16 with more than 32 rank rows: 1024) or more: as many workgroups as are on the GPU at once, and
+// no few more, which would take as long again.  With more than 64 rank rows that is one per CU (8192 tokens, K = 4096, 256
+// rank rows: 3 parts 45 us, 4 parts 59, 5 parts 55, 7 parts 50, and each part's sums are written and read again), else
+// two (16 rank rows: 2 parts 28.6 us, 3 parts 22.7, 5 parts 22.9; 64 rank rows 32.8, 25.8, 26.4).
+int lora_split(const qg_lora_desc* d, int64_t tokens, int32_t block_m) {
+  const int rows = d->num_slices * d->max_rank, group = lora_group(block_m, rows);
+  const int64_t tiles = (tokens / lora_tile(block_m, rows) + 1) * ((rows + group - 1) / group);
+  const int64_t want = (block_m > 16 && rows > 64 ? 1 : 2) * kCUs / tiles, most = std::min<int64_t>(8, d->k / (block_m == 16 && rows > 32 ? 1024 : 512));
+  return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
 qg_status check_kv(const qg_kv_desc* d) {
@@ -67,12 +77,6 @@ qg_status check_kv(const qg_kv_desc* d) {
   if (d->page_tokens < 16 || d->page_tokens > 256 || (d->page_tokens & (d->page_tokens - 1)) != 0) return QG_ERR_UNSUPPORTED;
   if (d->kv_heads > 1024 || d->num_pages * d->page_tokens > ((int64_t)1 << 31) - 1) return QG_ERR_UNSUPPORTED;
   return QG_OK;
-}
-
-int log2_of(int v) {
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
 }
 
 KvArgs kv_args(const qg_kv_desc* d, const int32_t* slots, int64_t tokens, const void* cache) {
@@ -136,15 +140,26 @@ qg_status qg_norm_rows(const qg_norm_desc* d, int64_t rows, const void* y, const
 
 int32_t qg_lora_block_m(int64_t tokens, int32_t num_adapters) {
   if (tokens < 0 || num_adapters <= 0) return 0;
-  return tokens >= (int64_t)32 * num_adapters ? 64 : 16;
+  return tokens >= (int64_t)256 * num_adapters ? 128 : tokens >= (int64_t)32 * num_adapters ? 64 : 16;
 }
 
-size_t qg_lora_workspace_bytes(const qg_lora_desc* d, int64_t tokens, int32_t block_m) {
-  if (check_lora(d) != QG_OK || tokens <= 0 || (block_m != 16 && block_m != 64)) return 0;
+// Workspace: the parts of K's sums and, for blocks of 64 and 128 tokens, their 16-bit parts and scales.
+static size_t lora_workspace(const qg_lora_desc* d, int64_t tokens, int32_t block_m, LoraArgs* a) {
   int64_t rows;
   block_capacity(tokens, d->num_adapters, block_m, &rows);
   const int64_t pitch = ((int64_t)d->num_slices * d->max_rank + 15) / 16 * 16;
-  return (size_t)lora_split(d, tokens, block_m) * (size_t)rows * (size_t)pitch * sizeof(float);
+  const size_t part = (size_t)lora_split(d, tokens, block_m) * (size_t)rows * (size_t)pitch * sizeof(float);
+  const size_t both = block_m == 16 ? 0 : (size_t)d->num_slices * (size_t)rows * (size_t)lora_padded_rank(d->max_rank) * 4;
+  if (a && a->part) {
+    a->t16 = (uint16_t*)((uint8_t*)a->part + part);            // (rows are multiples of 16: every part starts at 16 bytes)
+    a->t_scale = (float*)((uint8_t*)a->part + part + both);
+  }
+  return part + both + (block_m == 16 ? 0 : (size_t)d->num_slices * (size_t)rows * sizeof(float));
+}
+
+size_t qg_lora_workspace_bytes(const qg_lora_desc* d, int64_t tokens, int32_t block_m) {
+  if (check_lora(d) != QG_OK || tokens <= 0 || !lora_block(block_m)) return 0;
+  return lora_workspace(d, tokens, block_m, nullptr);
 }
 
 qg_status qg_lora(const qg_lora_desc* d, const void* x, const void* a_weight, const void* b_weight, const int32_t* ranks,
@@ -153,7 +168,7 @@ qg_status qg_lora(const qg_lora_desc* d, const void* x, const void* a_weight, co
   qg_status s = check_lora(d);
   if (s != QG_OK) return s;
   if (tokens < 0) return QG_ERR_INVALID_ARG;
-  if (block_m != 16 && block_m != 64) return QG_ERR_UNSUPPORTED;
+  if (!lora_block(block_m)) return QG_ERR_UNSUPPORTED;
   if (tokens > (int64_t)1 << 24) return QG_ERR_UNSUPPORTED;
   if (tokens == 0) return QG_OK;
   if (!x || !a_weight || !b_weight || !sorted_ids || !expert_ids || !num_post_pad || !base || !y) return QG_ERR_INVALID_ARG;
@@ -163,7 +178,7 @@ qg_status qg_lora(const qg_lora_desc* d, const void* x, const void* a_weight, co
   if (!ws || !aligned16(ws) || ws_bytes < qg_lora_workspace_bytes(d, tokens, block_m)) return QG_ERR_WORKSPACE;
   LoraArgs a{};
   const int64_t blocks = block_capacity(tokens, d->num_adapters, block_m, &a.cap_rows);
-  if (blocks * (d->n / 128 + d->num_slices) >= (int64_t)1 << 24) return QG_ERR_UNSUPPORTED;   // a launch takes fewer than 2^32 threads
+  if (blocks * std::max(1, block_m / 64) * (d->n / 128 + d->num_slices) >= (int64_t)1 << 23) return QG_ERR_UNSUPPORTED;   // a launch takes fewer than 2^32 threads
   s = check_arch();
   if (s != QG_OK) return s;
   stride_of(d->x_stride, d->k, &a.x_stride);
@@ -176,11 +191,12 @@ qg_status qg_lora(const qg_lora_desc* d, const void* x, const void* a_weight, co
   a.rank_rows = d->num_slices * d->max_rank;
   a.rank_pitch = (a.rank_rows + 15) / 16 * 16;
   a.ksplit = lora_split(d, tokens, block_m);
+  lora_workspace(d, tokens, block_m, &a);
+  a.block_shift = log2_of(block_m);
   for (int i = 0; i < d->num_slices; ++i) a.slice_end[i] = (int)d->slice_end[i];
   QG_LOG("lora tokens=%lld n=%lld k=%lld rank=%d x %d -> block=%d ksplit=%d", (long long)tokens, (long long)d->n,
          (long long)d->k, d->num_slices, d->max_rank, block_m, a.ksplit);
-  if (!launch_lora(a, d->type == QG_O_F16 ? O_F16 : O_BF16, block_m, (unsigned)blocks, (hipStream_t)stream))
-    return QG_ERR_UNSUPPORTED;
+  launch_lora(a, d->type == QG_O_F16 ? O_F16 : O_BF16, (unsigned)blocks, (hipStream_t)stream);
   return launched();
 }
 
@@ -230,7 +246,7 @@ static qg_status check_attention(const qg_kv_desc* d, int32_t q_heads, int64_t b
   const qg_status s = check_kv(d);
   if (s != QG_OK) return s;
   if (q_heads <= 0 || q_heads % d->kv_heads != 0 || batch < 0 || max_q <= 0 || tokens < 0 || max_len < 0) return QG_ERR_INVALID_ARG;
-  if (q_heads > 4096 || batch > 65535 || max_q > (1 << 24) || tokens > (1 << 24) || max_len > (1 << 30)) return QG_ERR_UNSUPPORTED;
+  if (q_heads / d->kv_heads > 256 || batch > 65535 || max_q > (1 << 24) || tokens > (1 << 24) || max_len > (1 << 30)) return QG_ERR_UNSUPPORTED;
   return QG_OK;
 }
 
@@ -267,8 +283,10 @@ qg_status qg_attention(const qg_kv_desc* d, const void* q, int64_t q_stride, int
       (!ws || !aligned16(ws) || ws_bytes < qg_attention_workspace_bytes(d, q_heads, batch, max_q, tokens, max_len)))
     return QG_ERR_WORKSPACE;
   a.group = q_heads / d->kv_heads;
-  if (batch * d->kv_heads * a.nsplit * ((max_q * a.group + 15) / 16) > (1 << 23) || max_q * q_heads >= (1 << 24))
-    return QG_ERR_UNSUPPORTED;                      // launches of fewer than 2^32 threads
+  a.group_inv = (uint32_t)((((uint64_t)1 << 32) + a.group - 1) / a.group);
+  // grid axes of 65535 workgroups, launches of fewer than 2^32 threads
+  const int64_t tiles = split.row_tiles * split.parts;
+  if (tiles > 65535 || tiles * batch * d->kv_heads >= ((int64_t)1 << 24) || max_q > 65535) return QG_ERR_UNSUPPORTED;
   s = check_arch();
   if (s != QG_OK) return s;
   a.cache = (const uint8_t*)cache; a.table = block_table; a.lens = seq_lens; a.q_offsets = q_offsets;

@@ -47,6 +47,9 @@ __device__ __forceinline__ u32x4 bf16_low(const float* v, u32x4 hi) {
 __device__ __forceinline__ u32x4 bf16_high(const float* v) {
   return u32x4{pack2<A_BF16>(v[0], v[1]), pack2<A_BF16>(v[2], v[3]), pack2<A_BF16>(v[4], v[5]), pack2<A_BF16>(v[6], v[7])};
 }
+// 16 bytes; ONCE: no other tile reads them
+template <bool ONCE>
+__device__ __forceinline__ u32x4 ldg(const void* p) { return ONCE ? ldg16_stream(p) : ldg16(p); }
 template <int B>
 __device__ __forceinline__ uint32_t cvt_pair(uint32_t w, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
@@ -67,8 +70,10 @@ struct Step {
   bool ok[2];                                       // the tile's page is in the cache
 };
 
-// Parts that `steps` steps are taken in, `chunk` steps each; a row that sees nothing is one part.
-__device__ __forceinline__ int parts_of(int steps, int chunk) { return max(1, (steps + chunk - 1) / chunk); }
+// row / group for rows below 2^24 and groups of at most 256: group_inv = ceil(2^32 / group)
+__device__ __forceinline__ int over_group(int row, const AttnArgs& a) {
+  return a.group == 1 ? row : (int)__umulhi((uint32_t)row, a.group_inv);
+}
 
 // (two waves per SIMD at least: with 256 registers or fewer the sums stay where the vector unit reads them)
 template <int T, int D, int RT, bool SHARE>
@@ -83,11 +88,13 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   const int r = lane & 15, c = lane >> 4;
 
   // ---- the tile: sequence, key head, rows, tokens -------------------------------------
-  // (key heads and sequences fastest: tiles that read the same keys run on the same XCD)
-  const int heads = a.batch * a.kv_heads;
-  const int bh = blockIdx.x % heads, rest = blockIdx.x / heads;
-  const int split = rest % a.nsplit, tile = rest / a.nsplit;
-  const int b = bh / a.kv_heads, hk = bh - b * a.kv_heads;
+  // (key heads and sequences fastest: tiles that read the same keys run on the same XCD where their number allows)
+  const int hk = blockIdx.x, b = blockIdx.y;
+  int split = 0, tile = blockIdx.z;
+  if (a.nsplit > 1) {
+    tile = (int)blockIdx.z / a.nsplit;
+    split = (int)blockIdx.z - tile * a.nsplit;
+  }
   int64_t q0 = b;
   int nq = 1;
   if (a.q_offsets) {
@@ -105,15 +112,15 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int row = min(row0 + 16 * t + r, row_count - 1);
-    qrow[t] = row / a.group;
+    qrow[t] = over_group(row, a);
     sees[t] = max(0, len - nq + qrow[t] + 1);
   }
   const int last_row = min(row0 + 16 * RT, row_count) - 1;
-  const int most = __builtin_amdgcn_readfirstlane(max(0, len - nq + last_row / a.group + 1));
-  const int least = __builtin_amdgcn_readfirstlane(max(0, len - nq + row0 / a.group + 1));
-  const int steps = (most + 31) / 32, parts = parts_of(steps, a.chunk);
-  if (split >= parts) return;                       // (the same for all waves that share rows)
-  const int begin = split * a.chunk, end = min(steps, begin + a.chunk);
+  const int most = __builtin_amdgcn_readfirstlane(max(0, len - nq + over_group(last_row, a) + 1));
+  const int least = __builtin_amdgcn_readfirstlane(max(0, len - nq + over_group(row0, a) + 1));
+  const int steps = (most + 31) >> 5, begin = split * a.chunk, end = min(steps, begin + a.chunk);
+  if (split > 0 && begin >= steps) return;          // (the same for all waves that share rows)
+  const bool whole = steps <= a.chunk;              // one part: the outputs themselves
 
   // ---- queries ---------------------------------------------------------------------------
   u32x4 qf[RT][KW], ql[HILO ? RT : 1][HILO ? KW : 1];
@@ -172,15 +179,15 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
       } else {
 #pragma unroll
         for (int j = 0; j < KW; j += 4) {
-          const u32x4 w = ldg16(kb + k_at + 4 * j);
+          const u32x4 w = ldg<SHARE>(kb + k_at + 4 * j);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s.k[h][j + e] = w[e];
         }
       }
       if constexpr (D == 256) s.ks[h] = *(const uint16_t*)(ksb + ks_at);
       else s.ks[h] = ksb[ks_at];
-      s.v[h][0] = ldg16(vb + v_at);
-      if constexpr (D == 256) s.v[h][1] = ldg16(vb + v_at + 16);
+      s.v[h][0] = ldg<SHARE>(vb + v_at);
+      if constexpr (D == 256) s.v[h][1] = ldg<SHARE>(vb + v_at + 16);
       s.vs[h] = *(const uint32_t*)(vsb + vs_at);
     }
   };
@@ -336,7 +343,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   };
 
   // ---- the tokens, two steps' loads ahead (where registers allow) ------------------------
-  constexpr bool TWO = D < 256 && RT == 1;
+  constexpr bool TWO = false;
   if (count > 0) {
     Step<D> s0, s1;
     load_ids(0);
@@ -374,8 +381,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   auto store = [&](int row, int d, const float* v, float sum, float top) __attribute__((always_inline)) {
     // eight (D = 64: four) values of a row, from d on
     constexpr int N = NJ < 8 ? NJ : 8;
-    const int qi = row / a.group, head = hk * a.group + row - qi * a.group;
-    if (parts > 1) {
+    const int qi = over_group(row, a), head = hk * a.group + row - qi * a.group;
+    if (!whole) {
       float* o = a.part + ((int64_t)split * part_rows + (q0 + qi) * a.q_heads + head) * D + d;
 #pragma unroll
       for (int e = 0; e < N; e += 4) *(f32x4*)(o + e) = *(const f32x4*)(v + e);
@@ -459,20 +466,20 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     q0 = max(0, a.q_offsets[b]);
     nq = min((int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0), a.max_q);
   }
-  const int qi = (int)blockIdx.x / a.q_heads, head = (int)blockIdx.x - qi * a.q_heads;
+  const int head = blockIdx.x, qi = blockIdx.z;
   if (qi >= nq) return;
   // as many parts as the row's tile was taken in
-  const int row_count = nq * a.group, in_group = qi * a.group + head % a.group;
-  const int last_row = min((in_group / a.tile_rows + 1) * a.tile_rows, row_count) - 1;
+  const int row_count = nq * a.group, in_group = qi * a.group + head - over_group(head, a) * a.group;
+  const int last_row = min((in_group & -a.tile_rows) + a.tile_rows, row_count) - 1;   // (a power of two)
   const int len = max(0, min(a.lens[b], a.max_len));
-  const int most = max(0, len - nq + last_row / a.group + 1);
-  const int parts = parts_of((most + 31) / 32, a.chunk);
-  if (parts == 1) return;                           // written already
+  const int most = max(0, len - nq + over_group(last_row, a) + 1);
+  const int steps = (most + 31) >> 5;
+  if (steps <= a.chunk) return;                     // one part: written already
   const int64_t row = (q0 + qi) * a.q_heads + head;
   const float* ml = a.part + (int64_t)a.nsplit * a.rows * D + row * 2;
   // every wave: maximum and sum of all parts (64 or fewer, one per lane)
-  const float ms = lane < parts ? ml[(int64_t)lane * a.rows * 2] : kNegInf;
-  const float ls = lane < parts ? ml[(int64_t)lane * a.rows * 2 + 1] : 0.f;
+  const float ms = lane * a.chunk < steps ? ml[(int64_t)lane * a.rows * 2] : kNegInf;
+  const float ls = lane * a.chunk < steps ? ml[(int64_t)lane * a.rows * 2 + 1] : 0.f;
   float top = ms;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
@@ -485,7 +492,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   const int g = tid / LPR, d = (tid % LPR) * 4;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int s = g; s < parts; s += GROUPS) v += *(const f32x4*)(a.part + ((int64_t)s * a.rows + row) * D + d) * weight[s];
+  for (int s = g; s * a.chunk < steps; s += GROUPS) v += *(const f32x4*)(a.part + ((int64_t)s * a.rows + row) * D + d) * weight[s];
   *(f32x4*)&sums[g][d] = v;
   __syncthreads();
   if (g != 0) return;
@@ -501,21 +508,19 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 constexpr bool shares_rows(int64_t rows) { return rows <= 16; }
 constexpr int many_rows(int type, int dim) { return dim == 64 ? 4 : (dim == 128 ? 4 : 2) / (type == O_BF16 ? 1 : 2); }
 
+constexpr int tile_of(int type, int dim, bool share) { return share ? 16 : 16 * kAttnWaves * many_rows(type, dim); }   // of a workgroup
+
 template <int T, int D>
 void launch_one(AttnArgs a, hipStream_t st) {
   constexpr int RT = many_rows(T, D);
-  const int64_t rows = (int64_t)a.max_q * a.group, heads = (int64_t)a.batch * a.kv_heads * a.nsplit;
-  if (shares_rows(rows)) {
-    a.tile_rows = 16;
-    hipLaunchKernelGGL((attention_kernel<T, D, 1, true>), dim3((unsigned)(heads * ((rows + 15) / 16))), dim3(64 * kAttnWaves), 0, st, a);
-  } else {
-    constexpr int PER = 16 * RT * kAttnWaves;
-    a.tile_rows = 16 * RT;
-    hipLaunchKernelGGL((attention_kernel<T, D, RT, false>), dim3((unsigned)(heads * ((rows + PER - 1) / PER))), dim3(64 * kAttnWaves), 0,
-                       st, a);
-  }
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  const bool share = shares_rows(rows);
+  a.tile_rows = share ? 16 : 16 * RT;
+  const dim3 grid(a.kv_heads, a.batch, (unsigned)((rows + tile_of(T, D, share) - 1) / tile_of(T, D, share) * a.nsplit));
+  if (share) hipLaunchKernelGGL((attention_kernel<T, D, 1, true>), grid, dim3(64 * kAttnWaves), 0, st, a);
+  else hipLaunchKernelGGL((attention_kernel<T, D, RT, false>), grid, dim3(64 * kAttnWaves), 0, st, a);
   if (a.nsplit > 1)
-    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3((unsigned)(a.max_q * a.q_heads), a.batch), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3(a.q_heads, a.batch, a.max_q), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -525,12 +530,12 @@ void launch_one(AttnArgs a, hipStream_t st) {
 AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
   const int64_t rows = max_q * (q_heads / kv_heads);
   const bool share = shares_rows(rows);
-  const int64_t per = share ? 16 : 16 * kAttnWaves * many_rows(type, dim);
-  const int64_t tiles = batch * kv_heads * ((rows + per - 1) / per), steps = std::max<int64_t>(1, (max_len + 31) / 32);
-  const int64_t want = share ? 4096 : 1024;
+  const int64_t per = tile_of(type, dim, share), row_tiles = (rows + per - 1) / per;
+  const int64_t tiles = batch * kv_heads * row_tiles, steps = std::max<int64_t>(1, (max_len + 31) / 32);
+  const int64_t want = share ? 2048 : 1024;
   int64_t chunk = std::max({steps * tiles / want, (int64_t)16, (steps + kMaxParts - 1) / kMaxParts});
   chunk = std::min((chunk + 3) / 4 * 4, (steps + 3) / 4 * 4);
-  return AttnSplit{(int)((steps + chunk - 1) / chunk), (int)chunk};
+  return AttnSplit{(int)((steps + chunk - 1) / chunk), (int)chunk, row_tiles};
 }
 
 bool launch_attention(const AttnArgs& a, int type, hipStream_t st) {

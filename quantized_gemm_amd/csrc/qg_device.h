@@ -378,6 +378,11 @@ __device__ __forceinline__ void bload16_lds(__amdgpu_buffer_rsrc_t r, void* lds,
 __device__ __forceinline__ void bload4_lds(__amdgpu_buffer_rsrc_t r, void* lds, int off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, off, 0, 0, 0);
 }
+// 16 bytes per lane from anywhere in memory straight into LDS: lane l writes lds + 16 l (lds wave-uniform).
+__device__ __forceinline__ void gload16_lds(const void* p, void* lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
 __device__ __forceinline__ u32x2 bload8(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
 }

@@ -146,16 +146,23 @@ struct LoraArgs {
   const int32_t *ranks, *sorted_ids, *expert_ids, *num_post_pad;
   const float* scales;
   float* part;               // [ksplit][cap_rows][rank_pitch]
+  uint16_t* t16;             // blocks of 64 and 128: [slice][cap_rows][2][padded rank], the sums' two 16-bit parts
+  float* t_scale;            // [slice][cap_rows]
   int64_t x_stride, base_stride, y_stride, cap_rows;
   int64_t n;
   int tokens, k, max_rank, slices;
   int rank_rows;             // of an adapter: slices * max_rank
   int rank_pitch;            // rank_rows, padded to 16
   int ksplit;
-  int col_tiles;             // of the second product
+  int block_shift;           // log2 of the map's block
+  int col_tiles;             // of the second product's workgroups
+  int col_pairs;             // pairs of 16-column tiles per wave
   int slice_end[kLoraMaxSlices];
 };
-bool launch_lora(const LoraArgs& a, int type, int block_m, unsigned blocks, hipStream_t st);
+int lora_tile(int block_m, int rank_rows);    // tokens of a workgroup of the first product
+int lora_group(int block_m, int rank_rows);   // and its rank rows, at most
+int lora_padded_rank(int max_rank);           // of the second product
+void launch_lora(const LoraArgs& a, int type, unsigned blocks, hipStream_t st);
 
 // The paged MXFP4 cache (qg_kv.hip) and the attention that reads it (qg_attention.hip).  A (page, head) has
 // `page` tokens of D values, laid out as the attention's lanes read them:
@@ -184,10 +191,11 @@ struct AttnArgs {
   int batch, q_heads, kv_heads, group, dim, page_shift, max_q, max_len;
   int nsplit, chunk;         // parts at most, and steps of 32 tokens of a part
   int tile_rows;             // rows of a wave
+  uint32_t group_inv;        // ceil(2^32 / group)
   float scale_log2;          // |scale| * log2(e)
   uint32_t q_sign;           // 0x80008000 where scale is negative: turned into the queries
 };
-struct AttnSplit { int parts, chunk; };
+struct AttnSplit { int parts, chunk; int64_t row_tiles; };
 AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type);
 bool launch_attention(const AttnArgs& a, int type, hipStream_t st);
 

@@ -92,7 +92,7 @@ def _ids(tokens, e, seed=0, none=0.2):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("rank", [8, 16, 24, 32, 48, 64, 128, 256])
-@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("block", [16, 64, 128])
 def test_ranks(dtype, rank, block):
     Case(37, 200, [104], rank, _ids(37, 3), dtype, adapters=3, block=block).run().check()
     Case(70, 1416, [64, 160, 296], rank, _ids(70, 2, none=0.0), dtype, adapters=2, block=block, scales=[0.5, -2.0]).run().check()
@@ -100,7 +100,7 @@ def test_ranks(dtype, rank, block):
 
 @pytest.mark.parametrize("tokens", [1, 2, 15, 16, 17, 64, 65, 129, 500])
 def test_token_counts(tokens):
-    for block in (16, 64):
+    for block in (16, 64, 128):
         Case(tokens, 264, [136], 16, _ids(tokens, 5), adapters=5, block=block).run().check()
     Case(tokens, 264, [32, 136], 40, _ids(tokens, 5), adapters=5, pad=8).run().check()
 
@@ -110,6 +110,14 @@ def test_token_counts(tokens):
 def test_sizes(k, n):
     Case(5, k, [n], 16, [0, 1, 0, 1, 1], scales=[1.5, 0.25]).run().check()
     Case(90, k, [n], 32, _ids(90, 2), "f16", adapters=2, block=64).run().check()
+
+
+@pytest.mark.parametrize("k", [64, 128, 192, 256, 320, 1088, 4096])
+@pytest.mark.parametrize("rank,slices", [(72, [136]), (128, [64]), (64, [32, 64, 136]), (256, [64]), (136, [64, 128, 192])])
+def test_many_ranks_for_many_tokens(k, rank, slices):
+    # the first product's steps of 64, from one on; rank rows that end inside a wave's and a workgroup's share
+    for dtype, block in (("bf16", 64), ("f16", 64), ("bf16", 128), ("f16", 128)):
+        Case(150, k, slices, rank, _ids(150, 3), dtype, adapters=3, block=block, ranks=[rank, rank - 7, 3], pad=8).run().check()
 
 
 @pytest.mark.parametrize("ranks", [[0, 1, 5, 8], [16, 15, 9, 7], [-3, 100, 16, 2]])

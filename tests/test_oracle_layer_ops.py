@@ -114,7 +114,7 @@ def test_lora_rejects_on_the_host():
         assert _lora(**kw) == 2, kw
     need = qg.lora_workspace_bytes(qg.make_lora_desc(qg.O_BF16, 3, 16, 64, [64]), 4, 16)
     assert need > 0 and _lora(ws_bytes=need - 1) == 5 and _lora(ptrs={"ws": None}) == 5 and _lora(ptrs={"ws": ODD}) == 5
-    assert qg.lora_block_m(1, 8) == 16 and qg.lora_block_m(4096, 8) == 64 and qg.lora_block_m(-1, 8) == 0
+    assert qg.lora_block_m(1, 8) == 16 and qg.lora_block_m(1024, 8) == 64 and qg.lora_block_m(4096, 8) == 128 and qg.lora_block_m(-1, 8) == 0
     assert qg.lora_block_m(4, 0) == 0
 
 
@@ -163,7 +163,7 @@ def test_kv_and_attention_reject_on_the_host():
                dict(out=ODD), dict(cache=ODD), dict(table=ctypes.c_void_p(4098)), dict(lens=ctypes.c_void_p(4098)),
                dict(offs=ctypes.c_void_p(4098)), dict(d=None)):
         assert attn(**kw) == 1, kw
-    for kw in (dict(heads=8192), dict(batch=65536, tokens=65536), dict(offs=FAKE, tokens=(1 << 24) + 1)):
+    for kw in (dict(heads=2 * 257), dict(batch=65536, tokens=65536), dict(offs=FAKE, tokens=(1 << 24) + 1)):
         assert attn(**kw) == 2, kw
     long = dict(max_len=4096, table_stride=256)
     need = qg.attention_workspace_bytes(qg.make_kv_desc(**dict(good)), 4, 2, 1, 2, 4096)
