@@ -47,9 +47,6 @@ __device__ __forceinline__ u32x4 bf16_low(const float* v, u32x4 hi) {
 __device__ __forceinline__ u32x4 bf16_high(const float* v) {
   return u32x4{pack2<A_BF16>(v[0], v[1]), pack2<A_BF16>(v[2], v[3]), pack2<A_BF16>(v[4], v[5]), pack2<A_BF16>(v[6], v[7])};
 }
-// 16 bytes; ONCE: no other tile reads them
-template <bool ONCE>
-__device__ __forceinline__ u32x4 ldg(const void* p) { return ONCE ? ldg16_stream(p) : ldg16(p); }
 template <int B>
 __device__ __forceinline__ uint32_t cvt_pair(uint32_t w, float s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
@@ -75,14 +72,43 @@ __device__ __forceinline__ int over_group(int row, const AttnArgs& a) {
   return a.group == 1 ? row : (int)__umulhi((uint32_t)row, a.group_inv);
 }
 
+// Values d .. d + N - 1 of a row (a query and its head), and with the first of them its sum of weights and maximum: the
+// outputs, or one part's.
+template <int T, int D, int N>
+__device__ __forceinline__ void store_row(const AttnArgs& a, int hk, int split, int64_t q0, int row, int d, const float* v, float sum,
+                                          float top, bool whole) {
+  const int qi = over_group(row, a), head = hk * a.group + row - qi * a.group;
+  if (!whole) {
+    const int64_t at = (int64_t)split * a.rows + (q0 + qi) * a.q_heads + head;
+#pragma unroll
+    for (int e = 0; e < N; e += 4) *(f32x4*)(a.part + at * D + d + e) = *(const f32x4*)(v + e);
+    if (d == 0) {
+      float* const ml = a.part + (int64_t)a.nsplit * a.rows * D + at * 2;
+      ml[0] = top;
+      ml[1] = sum;
+    }
+  } else {
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;            // a row that sees nothing: zeros
+    uint16_t* const o = (uint16_t*)a.out + (q0 + qi) * a.out_stride + head * D + d;
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int e = 0; e < N; e += 2) w[e / 2] = pack2<T == O_F16 ? A_F16 : A_BF16>(v[e] * inv, v[e + 1] * inv);
+    if constexpr (N == 8) *(u32x4*)o = u32x4{w[0], w[1], w[2], w[3]};
+    else *(u32x2*)o = u32x2{w[0], w[1]};
+  }
+}
+
+// Up to 16 rows per key head (decoding): one row tile, whose tokens the workgroup's waves take in turn, each with a maximum
+// and sums of its own until the end.  Bound by reading the codes, each once.
 // (two waves per SIMD at least: with 256 registers or fewer the sums stay where the vector unit reads them)
-template <int T, int D, int RT, bool SHARE>
-__global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(SHARE ? 2 : 1))) void attention_kernel(AttnArgs a) {
+template <int T, int D>
+__global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(2))) void attention_kernel(AttnArgs a) {
   constexpr bool HILO = T == O_F16;
+  constexpr int RT = 1;
   constexpr int KW = D / 32, NJ = D / 16;           // MFMAs of a score tile; tiles of 16 output values
   constexpr int OP = D + 4;
-  __shared__ __attribute__((aligned(16))) float so[SHARE ? kAttnWaves * 16 * OP : 1];
-  __shared__ float sm[SHARE ? kAttnWaves : 1][16], sl[SHARE ? kAttnWaves : 1][16];
+  __shared__ __attribute__((aligned(16))) float so[kAttnWaves * 16 * OP];
+  __shared__ float sm[kAttnWaves][16], sl[kAttnWaves][16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, c = lane >> 4;
@@ -103,10 +129,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
     nq = min(nq, a.max_q);
   }
   const int row_count = nq * a.group;
-  const int row0 = (SHARE ? tile : tile * kAttnWaves + wave) * 16 * RT;
-  if ((SHARE ? row0 : tile * kAttnWaves * 16 * RT) >= row_count) return;
-  const bool idle = row0 >= row_count;              // (not SHARE: this wave only; no barriers then)
-  if (idle) return;
+  const int row0 = tile * 16;
+  if (row0 >= row_count) return;
   const int len = max(0, min(a.lens[b], a.max_len));
   int sees[RT], qrow[RT];                           // tokens that row 16 t + r sees; its query
 #pragma unroll
@@ -119,7 +143,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   const int most = __builtin_amdgcn_readfirstlane(max(0, len - nq + over_group(last_row, a) + 1));
   const int least = __builtin_amdgcn_readfirstlane(max(0, len - nq + over_group(row0, a) + 1));
   const int steps = (most + 31) >> 5, begin = split * a.chunk, end = min(steps, begin + a.chunk);
-  if (split > 0 && begin >= steps) return;          // (the same for all waves that share rows)
+  if (split > 0 && begin >= steps) return;          // (the same for all waves)
   const bool whole = steps <= a.chunk;              // one part: the outputs themselves
 
   // ---- queries ---------------------------------------------------------------------------
@@ -145,8 +169,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   const int64_t half = (int64_t)page * (D / 2), tail = (int64_t)page * (D / 32), head_bytes = 2 * (half + tail);
   const int32_t* const table = a.table + (int64_t)b * a.table_stride;
   const int last_page = max(0, len - 1) >> a.page_shift;
-  constexpr int STRIDE = SHARE ? kAttnWaves : 1;
-  const int first = begin + (SHARE ? wave : 0), count = first < end ? (end - first + STRIDE - 1) / STRIDE : 0;   // this wave's steps
+  constexpr int STRIDE = kAttnWaves;
+  const int first = begin + wave, count = first < end ? (end - first + STRIDE - 1) / STRIDE : 0;   // this wave's steps
   const uint32_t k_at = r * (D / 2) + c * (D / 8), ks_at = r * (D / 32) + (D == 256 ? 2 * c : D == 128 ? c : c >> 1);
   const uint32_t v_at = c * (2 * D) + 16 * (D == 256 ? 2 * r : D == 128 ? r : r >> 1);
   const uint32_t vs_at = 4 * (c * (D / 32) + (D == 256 ? r >> 1 : D == 128 ? r >> 2 : r >> 3));
@@ -179,15 +203,15 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
       } else {
 #pragma unroll
         for (int j = 0; j < KW; j += 4) {
-          const u32x4 w = ldg<SHARE>(kb + k_at + 4 * j);
+          const u32x4 w = ldg16_stream(kb + k_at + 4 * j);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s.k[h][j + e] = w[e];
         }
       }
       if constexpr (D == 256) s.ks[h] = *(const uint16_t*)(ksb + ks_at);
       else s.ks[h] = ksb[ks_at];
-      s.v[h][0] = ldg<SHARE>(vb + v_at);
-      if constexpr (D == 256) s.v[h][1] = ldg<SHARE>(vb + v_at + 16);
+      s.v[h][0] = ldg16_stream(vb + v_at);
+      if constexpr (D == 256) s.v[h][1] = ldg16_stream(vb + v_at + 16);
       s.vs[h] = *(const uint32_t*)(vsb + vs_at);
     }
   };
@@ -342,32 +366,18 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
     }
   };
 
-  // ---- the tokens, two steps' loads ahead (where registers allow) ------------------------
-  constexpr bool TWO = false;
+  // ---- the tokens, one step's loads ahead (two take registers that a third wave per SIMD needs: 64 sequences of up
+  // to 8192 tokens 75 against 66 us) --------------------------------------------------------
   if (count > 0) {
     Step<D> s0, s1;
     load_ids(0);
     load(0, s0);
-    if constexpr (TWO) {
-      Step<D> s2;
-      load(1, s1);
-      for (int n = 0; n < count; n += 3) {
-        if (n - ids0 >= 27) load_ids(n);            // (32 steps' pages at a time, of which this turn takes five)
-        load(n + 2, s2);
-        compute(first + STRIDE * n, s0);
-        load(n + 3, s0);
-        if (n + 1 < count) compute(first + STRIDE * (n + 1), s1);
-        load(n + 4, s1);
-        if (n + 2 < count) compute(first + STRIDE * (n + 2), s2);
-      }
-    } else {
-      for (int n = 0; n < count; n += 2) {
-        if (n - ids0 >= 29) load_ids(n);
-        load(n + 1, s1);
-        compute(first + STRIDE * n, s0);
-        load(n + 2, s0);
-        if (n + 1 < count) compute(first + STRIDE * (n + 1), s1);
-      }
+    for (int n = 0; n < count; n += 2) {
+      if (n - ids0 >= 29) load_ids(n);              // (32 steps' pages at a time, of which this turn takes three)
+      load(n + 1, s1);
+      compute(first + STRIDE * n, s0);
+      load(n + 2, s0);
+      if (n + 1 < count) compute(first + STRIDE * (n + 1), s1);
     }
   }
 #pragma unroll
@@ -377,79 +387,321 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   }
 
   // ---- out: lane (r, c) has values NJ (4 c + i) + j of row r -----------------------------
-  const int64_t part_rows = a.rows;
-  auto store = [&](int row, int d, const float* v, float sum, float top) __attribute__((always_inline)) {
-    // eight (D = 64: four) values of a row, from d on
-    constexpr int N = NJ < 8 ? NJ : 8;
-    const int qi = over_group(row, a), head = hk * a.group + row - qi * a.group;
-    if (!whole) {
-      float* o = a.part + ((int64_t)split * part_rows + (q0 + qi) * a.q_heads + head) * D + d;
+  // the waves' sums of the same rows, brought to one maximum, in the waves' order
 #pragma unroll
-      for (int e = 0; e < N; e += 4) *(f32x4*)(o + e) = *(const f32x4*)(v + e);
-      if (d == 0) {
-        float* ml = a.part + (int64_t)a.nsplit * part_rows * D + ((int64_t)split * part_rows + (q0 + qi) * a.q_heads + head) * 2;
-        ml[0] = top;
-        ml[1] = sum;
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; j += 4)
+      *(f32x4*)&so[(wave * 16 + r) * OP + NJ * (4 * c + i) + j] = f32x4{acc[0][j][i], acc[0][j + 1][i], acc[0][j + 2][i], acc[0][j + 3][i]};
+  if (c == 0) {
+    sm[wave][r] = m[0];
+    sl[wave][r] = l[0];
+  }
+  __syncthreads();
+  constexpr int N = NJ < 8 ? NJ : 8, PIECES = D / N;
+  for (int i = tid; i < 16 * PIECES; i += 64 * kAttnWaves) {
+    const int row = i / PIECES, d = (i - row * PIECES) * N;
+    if (row0 + row >= row_count) continue;
+    float top = sm[0][row];
+#pragma unroll
+    for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, sm[w][row]);
+    float sum = 0.f, v[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const float f = sm[w][row] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(sm[w][row] - top);
+      sum += sl[w][row] * f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = __builtin_fmaf(so[(w * 16 + row) * OP + d + e], f, v[e]);
+    }
+    store_row<T, D, N>(a, hk, split, q0, row0 + row, d, v, sum, top, whole);
+  }
+}
+
+// Many rows per key head (prompts): every wave has 16 RT rows of its own, and the workgroup's waves share the work of making
+// operands of 32 tokens' codes: each converts a quarter of them, once for all rows of the workgroup, into an LDS image in the
+// order that lanes read (1 KiB per operand, 16 bytes per lane side by side), two images in turn, one barrier per 32
+// tokens.  Converted by every wave for itself the operands cost as many instructions as the softmax of 64 rows (RT = 4, 2048
+// rows, D = 128: 281 us).  RT is what leaves room for two waves per SIMD, one multiplying while the other
+// takes exponentials: those bound it, about as much as the products do.
+template <int T, int D, int RT>
+__global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(2))) void attention_rows_kernel(AttnArgs a) {
+  constexpr bool HILO = T == O_F16;
+  constexpr int KW = D / 32, NJ = D / 16;
+  constexpr int KQ = D == 64 ? 1 : KW / 4, VQ = D == 64 ? 1 : NJ / 8;   // words of a key, and pairs of output tiles, that a wave converts
+  __shared__ __attribute__((aligned(16))) u32x4 image[2][2 * KW + NJ][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, c = lane >> 4;
+  const int hk = blockIdx.x, b = blockIdx.y;
+  int split = 0, tile = blockIdx.z;
+  if (a.nsplit > 1) {
+    tile = (int)blockIdx.z / a.nsplit;
+    split = (int)blockIdx.z - tile * a.nsplit;
+  }
+  int64_t q0 = b;
+  int nq = 1;
+  if (a.q_offsets) {
+    q0 = max(0, a.q_offsets[b]);
+    nq = (int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0);
+    nq = min(nq, a.max_q);
+  }
+  constexpr int ROWS = 16 * RT * kAttnWaves;
+  const int row_count = nq * a.group, tile0 = tile * ROWS, row0 = tile0 + wave * 16 * RT;
+  if (tile0 >= row_count) return;
+  const int len = max(0, min(a.lens[b], a.max_len));
+  // tokens that rows see: all of the workgroup's (fewest, most), this wave's
+  auto seen_by = [&](int row) __attribute__((always_inline)) {
+    return __builtin_amdgcn_readfirstlane(max(0, len - nq + over_group(min(row, row_count - 1), a) + 1));
+  };
+  const int all_least = seen_by(tile0), all_most = seen_by(tile0 + ROWS - 1);
+  const int least = seen_by(row0), most = row0 < row_count ? seen_by(row0 + 16 * RT - 1) : 0;
+  const int steps = (all_most + 31) >> 5, begin = split * a.chunk, end = min(steps, begin + a.chunk);
+  if (split > 0 && begin >= steps) return;
+  const bool whole = steps <= a.chunk;
+  int sees[RT];
+  u32x4 qf[RT][KW], ql[HILO ? RT : 1][HILO ? KW : 1];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int row = min(row0 + 16 * t + r, row_count - 1), qi = over_group(row, a);
+    sees[t] = max(0, len - nq + qi + 1);
+    const int head = hk * a.group + row - qi * a.group;
+    const uint16_t* p = (const uint16_t*)a.q + (q0 + qi) * a.q_stride + head * D + c * (D / 4);
+#pragma unroll
+    for (int j = 0; j < KW; ++j) {
+      qf[t][j] = ldg16(p + 8 * j) ^ a.q_sign;
+      if constexpr (HILO) {
+        float v[8];
+        unpack8<O_F16>(qf[t][j], v);
+        qf[t][j] = bf16_high(v);
+        ql[t][j] = bf16_low(v, qf[t][j]);
       }
-    } else {
-      const float inv = sum == 0.f ? 0.f : 1.0f / sum;          // a row that sees nothing: zeros
-      uint16_t* o = (uint16_t*)a.out + (q0 + qi) * a.out_stride + head * D + d;
-      uint32_t w[N / 2];
+    }
+  }
+
+  const int page = 1 << a.page_shift;
+  const int64_t half = (int64_t)page * (D / 2), tail = (int64_t)page * (D / 32), head_bytes = 2 * (half + tail);
+  const int32_t* const table = a.table + (int64_t)b * a.table_stride;
+  const int last_page = max(0, len - 1) >> a.page_shift;
+  // this wave's quarter: words KQ wave .. of each lane's part of a key (D = 64: of two, waves 0 and 1), pairs VQ wave .. of
+  // the output tiles (D = 64: of two, likewise)
+  const int part = D == 64 ? wave & 1 : wave;
+  const uint32_t k_at = r * (D / 2) + c * (D / 8) + 4 * KQ * part, ks_at = r * (D / 32) + (D == 256 ? 2 * c : D == 128 ? c : c >> 1);
+  const uint32_t v_at = c * (2 * D) + 16 * (D == 256 ? 2 * r + (part >> 1) : D == 128 ? r : r >> 1);
+  const uint32_t vs_at = 4 * (c * (D / 32) + (D == 256 ? r >> 1 : D == 128 ? r >> 2 : r >> 3));
+  struct Raw { uint32_t k[2][KQ], ks[2], vs[2]; u32x4 v[2]; bool ok[2]; };
+  auto load = [&](int step, Raw& s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < N; e += 2) w[e / 2] = pack2<T == O_F16 ? A_F16 : A_BF16>(v[e] * inv, v[e + 1] * inv);
-      if constexpr (N == 8) *(u32x4*)o = u32x4{w[0], w[1], w[2], w[3]};
-      else *(u32x2*)o = u32x2{w[0], w[1]};
+    for (int h = 0; h < 2; ++h) {
+      const int t0 = 32 * step + 16 * h, id = table[min(t0 >> a.page_shift, last_page)];
+      s.ok[h] = id >= 0 && id < a.num_pages;
+      const int t = t0 & (page - 1);
+      const uint8_t* const base = a.cache + ((int64_t)(s.ok[h] ? id : 0) * a.kv_heads + hk) * head_bytes;
+      const uint8_t* const kb = base + t * (D / 2);
+      const uint8_t* const ksb = base + 2 * half + t * (D / 32);
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) s.k[h][i] = *(const uint32_t*)(kb + k_at + 4 * i);
+      if constexpr (D == 256) s.ks[h] = *(const uint16_t*)(ksb + ks_at);
+      else s.ks[h] = ksb[ks_at];
+      s.v[h] = ldg16(base + half + t * (D / 2) + v_at);
+      s.vs[h] = *(const uint32_t*)(base + 2 * half + tail + t * (D / 32) + vs_at);
     }
   };
-  if constexpr (SHARE) {
-    // the waves' sums of the same rows, brought to one maximum, in the waves' order
-    static_assert(RT == 1, "one row tile");
+  // (NaN among values that some row of the workgroup does not see: kept apart, see attention_kernel)
+  struct Odd { u32x4 nan; bool any; };
+  auto convert = [&](int step, const Raw& s, u32x4 (*to)[64], Odd& odd) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) {
+        const int j = KQ * part + i;                // (D = 256: words 0-3 are of the first block)
+        const float p = __uint_as_float(D == 256 ? ((s.ks[h] >> (part >= 2 ? 8 : 0)) & 0xFFu) << 23 : power_bits(s.ks[h], 0));
+        if (D != 64 || wave < 2)
+          to[h * KW + j][lane] = u32x4{cvt_pair<0>(s.k[h][i], p), cvt_pair<1>(s.k[h][i], p), cvt_pair<2>(s.k[h][i], p), cvt_pair<3>(s.k[h][i], p)};
+      }
+    uint32_t vp[2][4];
+    odd.nan = u32x4{0, 0, 0, 0};
+    bool bad = false;
+    const bool cut = 32 * step + 32 > all_least || !s.ok[0] || !s.ok[1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vp[h][i] = power_bits(s.vs[h], i);
+        if (cut) {
+          if (!s.ok[h] || 32 * step + 16 * h + 4 * c + i >= all_most) vp[h][i] = 0;
+          if (vp[h][i] == kNanPower) {
+            vp[h][i] = 0;
+            bad = true;
+            odd.nan[2 * h + (i >> 1)] |= i & 1 ? 0x3F800000u : 0x3F80u;
+          }
+        }
+      }
+    odd.any = cut && __any(bad);
+#pragma unroll
+    for (int i = 0; i < VQ; ++i) {
+      // pair `part` of the word (D = 64: of its half; D = 256: two pairs of the word that part / 2 names)
+      const int pair = D == 256 ? 2 * (part & 1) + i : part, shift = 8 * pair + (D == 64 ? 16 * (r & 1) : 0);
+      uint32_t x[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[h][e] = cvt_pair<0>(s.v[h][e] >> shift, __uint_as_float(vp[h][e]));
+      u32x4 even, odd_v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        even[e] = __builtin_amdgcn_perm(x[e >> 1][2 * (e & 1) + 1], x[e >> 1][2 * (e & 1)], 0x05040100u);
+        odd_v[e] = __builtin_amdgcn_perm(x[e >> 1][2 * (e & 1) + 1], x[e >> 1][2 * (e & 1)], 0x07060302u);
+      }
+      const int j = D == 256 ? 8 * (part >> 1) + 2 * pair : 2 * pair;
+      if (D != 64 || wave >= 2) {
+        to[2 * KW + j][lane] = even;
+        to[2 * KW + j + 1][lane] = odd_v;
+      }
+    }
+  };
+
+  f32x4 acc[RT][NJ];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    m[t] = kNegInf;
+    l[t] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  auto compute = [&](int step, const u32x4 (*from)[64], const bool (&ok)[2], const Odd& odd) __attribute__((always_inline)) {
+    f32x4 sc[RT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < KW; ++j) {
+        const u32x4 kf = from[h * KW + j][lane];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          sc[t][h] = mfma16x16x32<A_BF16>(kf, qf[t][j], j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sc[t][h]);
+          if constexpr (HILO) sc[t][h] = mfma16x16x32<A_BF16>(kf, ql[t][j], sc[t][h]);
+        }
+      }
+    if (32 * step + 32 > least || !ok[0] || !ok[1]) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!ok[h] || 32 * step + 16 * h + 4 * c + i >= sees[t]) sc[t][h][i] = kNegInf;
+    }
+    float top[RT];
+    bool up = false;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      top[t] = sc[t][0][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], sc[t][e >> 2][e & 3]);
+      top[t] *= a.scale_log2;
+      up |= top[t] > m[t] + kLazy;
+    }
+    if (__any(up)) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        float x = fmaxf(top[t], __shfl_xor(top[t], 16, 64));
+        x = fmaxf(m[t], fmaxf(x, __shfl_xor(x, 32, 64)));
+        const float f = x == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[t] - x);
+        m[t] = x;
+        l[t] *= f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[t][j] *= f;
+      }
+    }
+    u32x4 pf[RT], pl[HILO ? RT : 1];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const float base = m[t] == kNegInf ? 0.f : m[t];
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][e >> 2][e & 3], a.scale_log2, -base));
+      l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      pf[t] = bf16_high(p);
+      if constexpr (HILO) pl[t] = bf16_low(p, pf[t]);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const u32x4 vf = from[2 * KW + j][lane];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        acc[t][j] = mfma16x16x32<A_BF16>(vf, pf[t], acc[t][j]);
+        if constexpr (HILO) acc[t][j] = mfma16x16x32<A_BF16>(vf, pl[t], acc[t][j]);
+      }
+    }
+    if (odd.any) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        float seen[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) seen[e] = 32 * step + 16 * (e >> 2) + 4 * c + (e & 3) < sees[t] ? 1.f : 0.f;
+        const f32x4 count = mfma16x16x32<A_BF16>(odd.nan, bf16_high(seen), f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (count[i] > 0.f) acc[t][j][i] = __builtin_nanf("");
+      }
+    }
+  };
+  // step n's image is made while step n - 1 is multiplied, from codes loaded a step earlier still
+  if (begin < end) {
+    Raw raw;
+    Odd odd, odd_next;
+    bool ok[2], ok_next[2];
+    load(begin, raw);
+    convert(begin, raw, image[0], odd);
+    ok[0] = raw.ok[0];
+    ok[1] = raw.ok[1];
+    load(min(begin + 1, end - 1), raw);
+    __syncthreads();
+    for (int step = begin; step < end; ++step) {
+      const int at = (step - begin) & 1;
+      if (step + 1 < end) {
+        convert(step + 1, raw, image[at ^ 1], odd_next);
+        ok_next[0] = raw.ok[0];
+        ok_next[1] = raw.ok[1];
+        load(min(step + 2, end - 1), raw);
+      }
+      if (32 * step < most) compute(step, image[at], ok, odd);
+      odd = odd_next;
+      ok[0] = ok_next[0];
+      ok[1] = ok_next[1];
+      __syncthreads();
+    }
+  }
+  if (row0 >= row_count) return;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+    const int row = row0 + 16 * t + r;
+    if (row >= row_count) continue;
+    constexpr int N = NJ < 8 ? NJ : 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; j += 4)
-        *(f32x4*)&so[(wave * 16 + r) * OP + NJ * (4 * c + i) + j] = f32x4{acc[0][j][i], acc[0][j + 1][i], acc[0][j + 2][i], acc[0][j + 3][i]};
-    if (c == 0) {
-      sm[wave][r] = m[0];
-      sl[wave][r] = l[0];
-    }
-    __syncthreads();
-    constexpr int N = NJ < 8 ? NJ : 8, PIECES = D / N;
-    for (int i = tid; i < 16 * PIECES; i += 64 * kAttnWaves) {
-      const int row = i / PIECES, d = (i - row * PIECES) * N;
-      if (row0 + row >= row_count) continue;
-      float top = sm[0][row];
+      for (int j = 0; j < NJ; j += N) {
+        float v[N];
 #pragma unroll
-      for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, sm[w][row]);
-      float sum = 0.f, v[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) {
-        const float f = sm[w][row] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(sm[w][row] - top);
-        sum += sl[w][row] * f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = __builtin_fmaf(so[(w * 16 + row) * OP + d + e], f, v[e]);
+        for (int e = 0; e < N; ++e) v[e] = acc[t][j + e][i];
+        store_row<T, D, N>(a, hk, split, q0, row, NJ * (4 * c + i) + j, v, l[t], m[t], whole);
       }
-      store(row0 + row, d, v, sum, top);
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int row = row0 + 16 * t + r;
-      if (row >= row_count) continue;
-      constexpr int N = NJ < 8 ? NJ : 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; j += N) {
-          float v[N];
-#pragma unroll
-          for (int e = 0; e < N; ++e) v[e] = acc[t][j + e][i];
-          store(row, NJ * (4 * c + i) + j, v, l[t], m[t]);
-        }
-    }
   }
+}
+
+// Steps that a row's tile was taken in: its parts are those of a.chunk steps each.
+__device__ __forceinline__ int steps_of(const AttnArgs& a, int b, int nq, int qi, int head) {
+  const int row_count = nq * a.group, in_group = qi * a.group + head - over_group(head, a) * a.group;
+  const int last_row = min(in_group - in_group % a.tile_rows + a.tile_rows, row_count) - 1;
+  const int len = max(0, min(a.lens[b], a.max_len));
+  return (max(0, len - nq + over_group(last_row, a) + 1) + 31) >> 5;
 }
 
 // A row's parts, brought to one maximum, in a fixed order.  One workgroup per row: D / 4 threads take four values
@@ -468,12 +720,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   }
   const int head = blockIdx.x, qi = blockIdx.z;
   if (qi >= nq) return;
-  // as many parts as the row's tile was taken in
-  const int row_count = nq * a.group, in_group = qi * a.group + head - over_group(head, a) * a.group;
-  const int last_row = min((in_group & -a.tile_rows) + a.tile_rows, row_count) - 1;   // (a power of two)
-  const int len = max(0, min(a.lens[b], a.max_len));
-  const int most = max(0, len - nq + over_group(last_row, a) + 1);
-  const int steps = (most + 31) >> 5;
+  const int steps = steps_of(a, b, nq, qi, head);
   if (steps <= a.chunk) return;                     // one part: written already
   const int64_t row = (q0 + qi) * a.q_heads + head;
   const float* ml = a.part + (int64_t)a.nsplit * a.rows * D + row * 2;
@@ -504,23 +751,63 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
       u32x2{pack2<AF>(v[0] * inv, v[1] * inv), pack2<AF>(v[2] * inv, v[3] * inv)};
 }
 
-// Row tiles of a wave where every wave has rows of its own: as many as its registers hold beside the sums.
-constexpr bool shares_rows(int64_t rows) { return rows <= 16; }
-constexpr int many_rows(int type, int dim) { return dim == 64 ? 4 : (dim == 128 ? 4 : 2) / (type == O_BF16 ? 1 : 2); }
+// The same for many rows of few parts: D / 4 lanes per row, 1024 / D rows per workgroup.
+template <int T, int D>
+__global__ __launch_bounds__(256) void attention_join_rows_kernel(AttnArgs a) {
+  constexpr int LPR = D / 4, RPB = 256 / LPR;
+  const int b = blockIdx.y, qi = blockIdx.z;
+  int64_t q0 = b;
+  int nq = 1;
+  if (a.q_offsets) {
+    q0 = max(0, a.q_offsets[b]);
+    nq = min((int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0), a.max_q);
+  }
+  const int head = (int)blockIdx.x * RPB + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
+  if (qi >= nq || head >= a.q_heads) return;
+  const int steps = steps_of(a, b, nq, qi, head);
+  if (steps <= a.chunk) return;                     // one part: written already
+  const int64_t row = (q0 + qi) * a.q_heads + head;
+  const float* const ml = a.part + (int64_t)a.nsplit * a.rows * D + row * 2;
+  float top = kNegInf, sum = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s * a.chunk < steps; ++s) {
+    const float ms = ml[(int64_t)s * a.rows * 2], ls = ml[(int64_t)s * a.rows * 2 + 1];
+    const f32x4 o = *(const f32x4*)(a.part + ((int64_t)s * a.rows + row) * D + d);
+    const float up = fmaxf(top, ms);
+    const float f0 = top == kNegInf ? 0.f : __builtin_amdgcn_exp2f(top - up), f1 = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - up);
+    sum = sum * f0 + ls * f1;
+    v = v * f0 + o * f1;
+    top = up;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  constexpr int AF = T == O_F16 ? A_F16 : A_BF16;
+  *(u32x2*)((uint16_t*)a.out + (q0 + qi) * a.out_stride + head * D + d) =
+      u32x2{pack2<AF>(v[0] * inv, v[1] * inv), pack2<AF>(v[2] * inv, v[3] * inv)};
+}
 
-constexpr int tile_of(int type, int dim, bool share) { return share ? 16 : 16 * kAttnWaves * many_rows(type, dim); }   // of a workgroup
+// Row tiles of a wave of attention_rows_kernel.
+constexpr int many_rows(int type, int dim) {
+  return dim == 256 ? 1 : type == O_BF16 ? (dim == 64 ? 4 : 3) : (dim == 64 ? 3 : 2);
+}
+constexpr bool shares_rows(int64_t rows) { return rows <= 16; }
+constexpr int tile_of(int type, int dim, bool share) { return share ? 16 : 16 * kAttnWaves * many_rows(type, dim); }   // rows of a workgroup
 
 template <int T, int D>
 void launch_one(AttnArgs a, hipStream_t st) {
-  constexpr int RT = many_rows(T, D);
   const int64_t rows = (int64_t)a.max_q * a.group;
   const bool share = shares_rows(rows);
-  a.tile_rows = share ? 16 : 16 * RT;
-  const dim3 grid(a.kv_heads, a.batch, (unsigned)((rows + tile_of(T, D, share) - 1) / tile_of(T, D, share) * a.nsplit));
-  if (share) hipLaunchKernelGGL((attention_kernel<T, D, 1, true>), grid, dim3(64 * kAttnWaves), 0, st, a);
-  else hipLaunchKernelGGL((attention_kernel<T, D, RT, false>), grid, dim3(64 * kAttnWaves), 0, st, a);
-  if (a.nsplit > 1)
+  a.tile_rows = tile_of(T, D, share);
+  const dim3 grid(a.kv_heads, a.batch, (unsigned)((rows + a.tile_rows - 1) / a.tile_rows * a.nsplit));
+  if (share) hipLaunchKernelGGL((attention_kernel<T, D>), grid, dim3(64 * kAttnWaves), 0, st, a);
+  else hipLaunchKernelGGL((attention_rows_kernel<T, D, many_rows(T, D)>), grid, dim3(64 * kAttnWaves), 0, st, a);
+  if (a.nsplit == 1) return;
+  // a workgroup per row while the rows are few
+  constexpr int RPB = 1024 / D;
+  if ((int64_t)a.batch * a.max_q * a.q_heads <= 4096)
     hipLaunchKernelGGL((attention_join_kernel<T, D>), dim3(a.q_heads, a.batch, a.max_q), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((attention_join_rows_kernel<T, D>), dim3((a.q_heads + RPB - 1) / RPB, a.batch, a.max_q), dim3(256), 0, st, a);
 }
 
 }  // namespace
