@@ -435,10 +435,12 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int hk = blockIdx.x, b = blockIdx.y;
-  int split = 0, tile = blockIdx.z;
+  // (the last queries first: they see the most tokens)
+  int split = 0, tile = (int)(gridDim.z - 1 - blockIdx.z);
   if (a.nsplit > 1) {
-    tile = (int)blockIdx.z / a.nsplit;
-    split = (int)blockIdx.z - tile * a.nsplit;
+    const int tiles = (int)gridDim.z / a.nsplit, z = (int)blockIdx.z / a.nsplit;
+    tile = tiles - 1 - z;
+    split = (int)blockIdx.z - z * a.nsplit;
   }
   int64_t q0 = b;
   int nq = 1;
@@ -491,10 +493,16 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   const uint32_t v_at = c * (2 * D) + 16 * (D == 256 ? 2 * r + (part >> 1) : D == 128 ? r : r >> 1);
   const uint32_t vs_at = 4 * (c * (D / 32) + (D == 256 ? r >> 1 : D == 128 ? r >> 2 : r >> 3));
   struct Raw { uint32_t k[2][KQ], ks[2], vs[2]; u32x4 v[2]; bool ok[2]; };
+  // (pages in lanes, as in attention_kernel)
+  int ids = 0, ids0 = 0;
+  auto load_ids = [&](int step) __attribute__((always_inline)) {
+    ids0 = step;
+    ids = table[min((32 * (step + (lane >> 1)) + 16 * (lane & 1)) >> a.page_shift, last_page)];
+  };
   auto load = [&](int step, Raw& s) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int t0 = 32 * step + 16 * h, id = table[min(t0 >> a.page_shift, last_page)];
+      const int t0 = 32 * step + 16 * h, id = __builtin_amdgcn_readlane(ids, 2 * (step - ids0) + h);
       s.ok[h] = id >= 0 && id < a.num_pages;
       const int t = t0 & (page - 1);
       const uint8_t* const base = a.cache + ((int64_t)(s.ok[h] ? id : 0) * a.kv_heads + hk) * head_bytes;
@@ -508,8 +516,11 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
       s.vs[h] = *(const uint32_t*)(base + 2 * half + tail + t * (D / 32) + vs_at);
     }
   };
-  // (NaN among values that some row of the workgroup does not see: kept apart, see attention_kernel)
-  struct Odd { u32x4 nan; bool any; };
+  // a step's exponent bytes of values, where NaN is among them that some row of the workgroup does not see: see attention_kernel
+  struct Odd { uint32_t vs[2]; bool any, ok[2]; };
+  auto odd_value = [&](int step, const Odd& o, int h, int i) __attribute__((always_inline)) {
+    return ((o.vs[h] >> (8 * i)) & 0xFFu) == 0xFFu && o.ok[h] && 32 * step + 16 * h + 4 * c + i < all_most;
+  };
   auto convert = [&](int step, const Raw& s, u32x4 (*to)[64], Odd& odd) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -521,24 +532,26 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
           to[h * KW + j][lane] = u32x4{cvt_pair<0>(s.k[h][i], p), cvt_pair<1>(s.k[h][i], p), cvt_pair<2>(s.k[h][i], p), cvt_pair<3>(s.k[h][i], p)};
       }
     uint32_t vp[2][4];
-    odd.nan = u32x4{0, 0, 0, 0};
-    bool bad = false;
-    const bool cut = 32 * step + 32 > all_least || !s.ok[0] || !s.ok[1];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      odd.vs[h] = s.vs[h];
+      odd.ok[h] = s.ok[h];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        vp[h][i] = power_bits(s.vs[h], i);
-        if (cut) {
-          if (!s.ok[h] || 32 * step + 16 * h + 4 * c + i >= all_most) vp[h][i] = 0;
-          if (vp[h][i] == kNanPower) {
-            vp[h][i] = 0;
-            bad = true;
-            odd.nan[2 * h + (i >> 1)] |= i & 1 ? 0x3F800000u : 0x3F80u;
-          }
+      for (int i = 0; i < 4; ++i) vp[h][i] = power_bits(s.vs[h], i);
+    }
+    odd.any = false;
+    if (32 * step + 32 > all_least || !s.ok[0] || !s.ok[1]) {
+      bool bad = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool o = odd_value(step, odd, h, i);
+          bad |= o;
+          if (o || !s.ok[h] || 32 * step + 16 * h + 4 * c + i >= all_most) vp[h][i] = 0;
         }
-      }
-    odd.any = cut && __any(bad);
+      odd.any = __any(bad);
+    }
 #pragma unroll
     for (int i = 0; i < VQ; ++i) {
       // pair `part` of the word (D = 64: of its half; D = 256: two pairs of the word that part / 2 names)
@@ -571,27 +584,32 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  auto compute = [&](int step, const u32x4 (*from)[64], const bool (&ok)[2], const Odd& odd) __attribute__((always_inline)) {
+  auto compute = [&](int step, const u32x4 (*from)[64], const Odd& odd) __attribute__((always_inline)) {
+    // operands are read AHEAD of the products that take them
+    constexpr int AHEAD = 3, NK = 2 * KW;
+    u32x4 ring[AHEAD + 1];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) ring[i] = from[i][lane];
     f32x4 sc[RT][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < NK; ++i) {
+      const int h = i / KW, j = i % KW;
+      ring[(i + AHEAD) % (AHEAD + 1)] = from[i + AHEAD][lane];     // (the first ones of the values at the end)
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < KW; ++j) {
-        const u32x4 kf = from[h * KW + j][lane];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          sc[t][h] = mfma16x16x32<A_BF16>(kf, qf[t][j], j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sc[t][h]);
-          if constexpr (HILO) sc[t][h] = mfma16x16x32<A_BF16>(kf, ql[t][j], sc[t][h]);
-        }
+      for (int t = 0; t < RT; ++t) {
+        sc[t][h] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], qf[t][j], j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sc[t][h]);
+        if constexpr (HILO) sc[t][h] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], ql[t][j], sc[t][h]);
       }
-    if (32 * step + 32 > least || !ok[0] || !ok[1]) {
+    }
+    if (32 * step + 32 > least || !odd.ok[0] || !odd.ok[1]) {
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (!ok[h] || 32 * step + 16 * h + 4 * c + i >= sees[t]) sc[t][h][i] = kNegInf;
+            if (!odd.ok[h] || 32 * step + 16 * h + 4 * c + i >= sees[t]) sc[t][h][i] = kNegInf;
     }
     float top[RT];
     bool up = false;
@@ -628,20 +646,26 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const u32x4 vf = from[2 * KW + j][lane];
+      const int i = NK + j;
+      if (j + AHEAD < NJ) ring[(i + AHEAD) % (AHEAD + 1)] = from[i + AHEAD][lane];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        acc[t][j] = mfma16x16x32<A_BF16>(vf, pf[t], acc[t][j]);
-        if constexpr (HILO) acc[t][j] = mfma16x16x32<A_BF16>(vf, pl[t], acc[t][j]);
+        acc[t][j] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], pf[t], acc[t][j]);
+        if constexpr (HILO) acc[t][j] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], pl[t], acc[t][j]);
       }
     }
     if (odd.any) {
+      u32x4 nan = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (odd_value(step, odd, e >> 2, e & 3)) nan[e >> 1] |= e & 1 ? 0x3F800000u : 0x3F80u;
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         float seen[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) seen[e] = 32 * step + 16 * (e >> 2) + 4 * c + (e & 3) < sees[t] ? 1.f : 0.f;
-        const f32x4 count = mfma16x16x32<A_BF16>(odd.nan, bf16_high(seen), f32x4{0.f, 0.f, 0.f, 0.f});
+        const f32x4 count = mfma16x16x32<A_BF16>(nan, bf16_high(seen), f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -654,25 +678,22 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   if (begin < end) {
     Raw raw;
     Odd odd, odd_next;
-    bool ok[2], ok_next[2];
+    load_ids(begin);
     load(begin, raw);
     convert(begin, raw, image[0], odd);
-    ok[0] = raw.ok[0];
-    ok[1] = raw.ok[1];
     load(min(begin + 1, end - 1), raw);
+    odd_next = odd;
     __syncthreads();
     for (int step = begin; step < end; ++step) {
       const int at = (step - begin) & 1;
       if (step + 1 < end) {
         convert(step + 1, raw, image[at ^ 1], odd_next);
-        ok_next[0] = raw.ok[0];
-        ok_next[1] = raw.ok[1];
-        load(min(step + 2, end - 1), raw);
+        const int later = min(step + 2, end - 1);
+        if (later - ids0 >= 32) load_ids(later);
+        load(later, raw);
       }
-      if (32 * step < most) compute(step, image[at], ok, odd);
+      if (32 * step < most) compute(step, image[at], odd);
       odd = odd_next;
-      ok[0] = ok_next[0];
-      ok[1] = ok_next[1];
       __syncthreads();
     }
   }
@@ -812,15 +833,17 @@ void launch_one(AttnArgs a, hipStream_t st) {
 
 }  // namespace
 
-// Parts of 32 * chunk tokens: of equal work whatever the sequences' lengths, as many as fill the GPU if all sequences had the
-// maximum, none shorter than 512 tokens (what a part costs beside its tokens).
+// Parts of 32 * chunk tokens: of equal work whatever the sequences' lengths.  Decoding: as many as fill the GPU if all
+// sequences had the maximum, none shorter than 512 tokens (what a part costs beside its tokens).  Many rows: only while a
+// workgroup per tile leaves CUs without two (a prompt of 4608 tokens, 768 tiles: whole 255 us, in parts 424; 4
+// sequences with 512 new tokens each, 352 tiles: whole 270 us, in parts 225 and 18 to join them).
 AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
   const int64_t rows = max_q * (q_heads / kv_heads);
   const bool share = shares_rows(rows);
   const int64_t per = tile_of(type, dim, share), row_tiles = (rows + per - 1) / per;
   const int64_t tiles = batch * kv_heads * row_tiles, steps = std::max<int64_t>(1, (max_len + 31) / 32);
-  const int64_t want = share ? 2048 : 1024;
-  int64_t chunk = std::max({steps * tiles / want, (int64_t)16, (steps + kMaxParts - 1) / kMaxParts});
+  int64_t chunk = std::max({steps * tiles / (share ? 2048 : 1024), (int64_t)16, (steps + kMaxParts - 1) / kMaxParts});
+  if (!share && tiles >= 512) chunk = steps;
   chunk = std::min((chunk + 3) / 4 * 4, (steps + 3) / 4 * 4);
   return AttnSplit{(int)((steps + chunk - 1) / chunk), (int)chunk, row_tiles};
 }
