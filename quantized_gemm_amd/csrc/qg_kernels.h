@@ -132,7 +132,6 @@ struct NormArgs {
   const void *y, *res, *gate, *post_weight, *weight, *bias;
   void *res_out, *out, *codes, *scale;
   int64_t rows, k, y_stride, res_stride, out_stride, gate_stride;
-  int64_t row0;
   int norm, post, code;
   float eps, weight_offset, res_scale;
 };

@@ -9,7 +9,13 @@
 // second sum over registers), which loses nothing where the mean is far from zero.
 //
 // Bound by bytes.  A row stays in registers between the sums (P pieces of 8 values per thread), so that each
-// input is read once; NT threads share a row, and a sum over them is a wave's exchange plus one barrier.
+// input is read once; NT threads share a row, and a sum over them is a wave's exchange plus one barrier.  Rows of 1025 to
+// 8192 values are taken in turn by a workgroup (KEEP), the next one's loads on their way during one's sums, and weights and
+// a shared gate stay in registers.  Longer rows lack the registers for it (2048 rows of 16384 values: 57 us, in turn 150),
+// and shorter ones need no barrier to wait at (65536 rows of 512: 47 us, in turn 53); those are one to a workgroup or part
+// of it, and read the weights again.  Measured: 16384 rows of 4096, both norms, gate and residual, 135 us (3.5 TB/s; 155
+// with a workgroup per row); 4096 rows of 7168 to e4m3 53 us (68); one row of 7168 to e4m3 4.7 us (6.7); 65536 rows of 128
+// 14 us (29 with a whole wave to a row).
 #include "qg_device.h"
 #include "qg_kernels.h"
 #include "qg_rows.h"
@@ -24,11 +30,15 @@ __device__ __forceinline__ float neighbour(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), M, 0xF, 0xF, true));
 }
 
+// Words that the waves of a row leave their sums in.
+template <int NT>
+constexpr int kSlots = NT > 64 ? NT / 64 : 1;
+
 // A sum or a NaN-keeping maximum over the NT threads of a row; `slot`: NT / 64 words of LDS of its own.
 template <int NT, bool MAX>
 __device__ __forceinline__ float over_row(float v, float* slot) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
+  for (int off = (NT < 64 ? NT : 64) / 2; off >= 1; off >>= 1) {
     const float o = __shfl_xor(v, off, 64);
     v = MAX ? __builtin_elementwise_maximum(v, o) : v + o;
   }
@@ -42,226 +52,283 @@ __device__ __forceinline__ float over_row(float v, float* slot) {
   return v;
 }
 
-// Centres the row's values (layer norm) and returns what they are to be multiplied with.  Where the sums
-// leave float32 while the values are finite, values and eps are first brought down by a power of two.
+// Centres the row's values (layer norm; those behind its end are zeros and stay so) and returns what they are to be
+// multiplied with.  Where the sums leave float32 while the values are finite, values and eps are first brought down by a
+// power of two.
 template <int NT, int P>
 __device__ __forceinline__ float normalize(float (&v)[P][8], const bool (&in)[P], bool layer, float inv_k, float eps,
-                                           float (*slots)[NT / 64]) {
-  for (int pass = 0;; ++pass) {
-    float (*slot)[NT / 64] = slots + 3 * pass;
-    float mean = 0.f;
-    if (layer) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[i][e];
-      mean = over_row<NT, false>(s, slot[0]) * inv_k;
-    }
+                                           float (*slots)[kSlots<NT>]) {
+  auto squares = [&]() __attribute__((always_inline)) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = in[i] ? v[i][e] - mean : 0.f;
-        ss = __builtin_fmaf(d, d, ss);
-      }
-    ss = over_row<NT, false>(ss, slot[1]);
-    if (ss < __builtin_inff() || pass == 1) {
-      if (layer) {
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? v[i][e] - mean : 0.f;
-      }
-      return 1.0f / __builtin_sqrtf(__builtin_fmaf(ss, inv_k, eps));
-    }
-    float amax = 0.f;
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[i][e], v[i][e], ss);
+    return ss;
+  };
+  auto centre = [&](float* slot) __attribute__((always_inline)) {
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(v[i][e]));
-    amax = over_row<NT, true>(amax, slot[2]);
-    if (amax < __builtin_inff()) {
-      const int down = -__builtin_amdgcn_frexp_expf(amax);
+      for (int e = 0; e < 8; ++e) sum += v[i][e];
+    const float mean = over_row<NT, false>(sum, slot) * inv_k;
 #pragma unroll
-      for (int i = 0; i < P; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = __builtin_ldexpf(v[i][e], down);
-      eps = __builtin_ldexpf(eps, 2 * down);
-    }
+      for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? v[i][e] - mean : 0.f;
+    return mean;
+  };
+  if (!layer) {
+    const float ss = over_row<NT, false>(squares(), slots[0]);
+    if (ss < __builtin_inff()) return 1.0f / __builtin_sqrtf(__builtin_fmaf(ss, inv_k, eps));
   }
+  // layer norm, or squares beyond float32 (the values as they were)
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(v[i][e]));
+  amax = over_row<NT, true>(amax, slots[1]);
+  if (amax > 0x1p56f && amax < __builtin_inff()) {            // (2^15 squares of 2^56 stay inside)
+    const int down = -__builtin_amdgcn_frexp_expf(amax);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = __builtin_ldexpf(v[i][e], down);
+    eps = __builtin_ldexpf(eps, 2 * down);
+  }
+  if (layer) centre(slots[2]);
+  const float ss = over_row<NT, false>(squares(), slots[3]);
+  return 1.0f / __builtin_sqrtf(__builtin_fmaf(ss, inv_k, eps));
 }
 
-template <int T, bool R32, int NT, int P>
+// v *= f * (offset + weight), without a weight f alone.
+template <int T>
+__device__ __forceinline__ void scale_by(float (&v)[8], float f, bool weighted, float offset, const u32x4& raw) {
+  if (!weighted) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    return;
+  }
+  float w[8];
+  unpack8<T>(raw, w);
+  if (offset != 0.0f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] += offset;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * f * w[e];
+}
+
+// Takes the 16 bytes as new ones, so that what is made of them is not kept in (four times as many) registers over a loop.
+__device__ __forceinline__ void opaque(u32x4& v) { asm volatile("" : "+v"(v)); }
+
+// A thread's pieces of a row, as they lie in memory.
+template <int P, bool R32>
+struct RawRow {
+  u32x4 y[P], gate[P], res[P][R32 ? 2 : 1];
+};
+
+// KEEP: rows in turn, see above; else one row, and the shared rows read where they are used.
+template <int T, bool R32, int NT, int P, bool KEEP>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_rows_kernel(NormArgs a) {
   constexpr int RPB = NT < 256 ? 256 / NT : 1;                // rows per workgroup
-  __shared__ float slots[13][NT / 64];
+  __shared__ float slots[2][9][kSlots<NT>];                   // one row's sums while another's are still read
   const int tid = threadIdx.x % NT;
-  const int64_t r = a.row0 + (int64_t)blockIdx.x * RPB + threadIdx.x / NT;
-  if (r >= a.rows) return;                                    // NT = 64: whole waves leave together
   const int per_row = (int)(a.k >> 3);
   const float inv_k = 1.0f / (float)a.k;
   bool in[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) in[i] = tid + NT * i < per_row;
-
-  float u[P][8];
-#pragma unroll
-  for (int i = 0; i < P; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[i][e] = 0.f;
-  if (a.y) {
-    const uint16_t* row = (const uint16_t*)a.y + r * a.y_stride;
+  auto piece = [&](const void* p, int i) __attribute__((always_inline)) {
+    return ldg16((const uint16_t*)p + 8 * (tid + NT * i));
+  };
+  // what all rows share
+  u32x4 wp[P], w[P], b[P], g[P];
+  if constexpr (KEEP) {
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      if (in[i]) unpack8<T>(ldg16(row + 8 * (tid + NT * i)), u[i]);
+      if (in[i]) {
+        if (a.post_weight) wp[i] = piece(a.post_weight, i);
+        if (a.weight) w[i] = piece(a.weight, i);
+        if (a.bias) b[i] = piece(a.bias, i);
+        if (a.gate && a.gate_stride == 0) g[i] = piece(a.gate, i);
+      }
   }
-  float res[P][8];
-  if (a.res) {
+  RawRow<P, R32> raw;
+  auto load = [&](int64_t r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (in[i]) {
+        if (a.y) raw.y[i] = piece((const uint16_t*)a.y + r * a.y_stride, i);
+        if (a.res) {
+          if constexpr (R32) {
+            const float* const at = (const float*)a.res + r * a.res_stride + 8 * (tid + NT * i);
+            raw.res[i][0] = ldg16(at);
+            raw.res[i][1] = ldg16(at + 4);
+          } else {
+            raw.res[i][0] = piece((const uint16_t*)a.res + r * a.res_stride, i);
+          }
+        }
+        if (KEEP && a.gate && a.gate_stride != 0) raw.gate[i] = piece((const uint16_t*)a.gate + r * a.gate_stride, i);
+      }
+  };
+
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / NT;
+  if (r >= a.rows) return;                                    // NT <= 64: a row's lanes leave together
+  load(r);
+  for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
+    if (!KEEP && r >= step) load(r);                          // (more rows than a launch has workgroups)
+    float (*const slot)[kSlots<NT>] = slots[turn];
+    float u[P][8], res[P][8];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int64_t at = r * a.res_stride + 8 * (tid + NT * i);
+      if constexpr (KEEP) {
+        opaque(wp[i]);
+        opaque(w[i]);
+        opaque(b[i]);
+        opaque(g[i]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[i][e] = 0.f;
       if (!in[i]) continue;
-      if constexpr (R32) {
-        *(f32x4*)res[i] = *(const f32x4*)((const float*)a.res + at);
-        *(f32x4*)(res[i] + 4) = *(const f32x4*)((const float*)a.res + at + 4);
-      } else {
-        unpack8<T>(ldg16((const uint16_t*)a.res + at), res[i]);
-      }
-    }
-  }
-  if (a.post != 0) {
-    const float f = normalize<NT, P>(u, in, a.post == kNormLayer, inv_k, a.eps, slots);
+      if (a.y) unpack8<T>(raw.y[i], u[i]);
+      if (a.res) {
+        if constexpr (R32) {
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (in[i]) {
-        float w[8];
-        if (a.post_weight) unpack8<T>(ldg16((const uint16_t*)a.post_weight + 8 * (tid + NT * i)), w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[i][e] *= f * (a.post_weight ? a.weight_offset + w[e] : 1.0f);
-      }
-  }
-  if (a.y) {
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (in[i]) {
-        if (a.gate) {
-          float g[8];
-          unpack8<T>(ldg16((const uint16_t*)a.gate + r * a.gate_stride + 8 * (tid + NT * i)), g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[i][e] *= g[e];
+          for (int e = 0; e < 8; ++e) res[i][e] = __uint_as_float(raw.res[i][e >> 2][e & 3]);
+        } else {
+          unpack8<T>(raw.res[i][0], res[i]);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[i][e] = a.res ? __builtin_fmaf(a.res_scale, u[i][e], res[i][e]) : a.res_scale * u[i][e];
       }
-  } else {
+      if (KEEP && a.gate && a.gate_stride != 0) g[i] = raw.gate[i];
+    }
+    if (KEEP && r + step < a.rows) load(r + step);             // the next row's, on their way during this one's sums
+    if (a.post != 0) {
+      const float f = normalize<NT, P>(u, in, a.post == kNormLayer, inv_k, a.eps, slot);
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (in[i])
+      for (int i = 0; i < P; ++i)
+        if (in[i]) {
+          if (!KEEP && a.post_weight) wp[i] = piece(a.post_weight, i);
+          scale_by<T>(u[i], f, a.post_weight != nullptr, a.weight_offset, wp[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (!in[i]) continue;
+      if (a.y) {
+        if (a.gate) {
+          if (!KEEP) g[i] = piece((const uint16_t*)a.gate + r * a.gate_stride, i);
+          float v[8];
+          unpack8<T>(g[i], v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[i][e] *= v[e];
+        }
+        if (a.res) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[i][e] = __builtin_fmaf(a.res_scale, u[i][e], res[i][e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[i][e] *= a.res_scale;
+        }
+      } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[i][e] = res[i][e];
-  }
-  if (a.res_out) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int64_t at = r * a.res_stride + 8 * (tid + NT * i);
-      if (!in[i]) continue;
-      if constexpr (R32) {
-        *(f32x4*)((float*)a.res_out + at) = *(const f32x4*)u[i];
-        *(f32x4*)((float*)a.res_out + at + 4) = *(const f32x4*)(u[i] + 4);
-      } else {
-        *(u32x4*)((uint16_t*)a.res_out + at) = pack8<T>(u[i]);
+      }
+      if (a.res_out) {
+        const int64_t at = r * a.res_stride + 8 * (tid + NT * i);
+        if constexpr (R32) {
+          *(f32x4*)((float*)a.res_out + at) = f32x4{u[i][0], u[i][1], u[i][2], u[i][3]};
+          *(f32x4*)((float*)a.res_out + at + 4) = f32x4{u[i][4], u[i][5], u[i][6], u[i][7]};
+        } else {
+          *(u32x4*)((uint16_t*)a.res_out + at) = pack8<T>(u[i]);
+        }
       }
     }
-  }
-  if (a.norm == 0) return;
-  const float f = normalize<NT, P>(u, in, a.norm == kNormLayer, inv_k, a.eps, slots + 6);
-#pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (in[i]) {
-      float w[8], b[8];
-      if (a.weight) unpack8<T>(ldg16((const uint16_t*)a.weight + 8 * (tid + NT * i)), w);
-      if (a.bias) unpack8<T>(ldg16((const uint16_t*)a.bias + 8 * (tid + NT * i)), b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = u[i][e] * f;
-        u[i][e] = __builtin_fmaf(n, a.weight ? a.weight_offset + w[e] : 1.0f, a.bias ? b[e] : 0.0f);
-      }
-    }
-  if (a.out) {
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (in[i]) *(u32x4*)((uint16_t*)a.out + r * a.out_stride + 8 * (tid + NT * i)) = pack8<T>(u[i]);
-  }
-  if (a.code == A_FP4) {
-    // a block of 32 lies in four neighbouring threads
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(u[i][e]));
-      amax = __builtin_elementwise_maximum(amax, neighbour<0xB1>(amax));
-      amax = __builtin_elementwise_maximum(amax, neighbour<0x4E>(amax));
-      uint32_t codes;
-      const uint32_t e8 = mxfp4_encode8(u[i], amax, codes);
-      if (in[i]) {
-        const int c8 = tid + NT * i;
-        *(uint32_t*)((uint8_t*)a.codes + r * (a.k >> 1) + 4 * c8) = codes;
-        if ((c8 & 3) == 0) ((uint8_t*)a.scale)[r * (a.k >> 5) + (c8 >> 2)] = (uint8_t)e8;
-      }
-    }
-  } else if (a.code != 0) {
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, in[i] ? fabsf(u[i][e]) : 0.f);
-    amax = over_row<NT, true>(amax, slots[12]);
-    float sc = amax / (a.code == A_FP8 ? 448.0f : 127.0f);    // correctly rounded division
-    if (sc == 0.0f) sc = 1.0f;
-    if (!(amax < __builtin_inff())) sc = __builtin_nanf("");
-    if (tid == 0) ((float*)a.scale)[r] = sc;
-    const bool direct = !(sc >= 0x1p-100f && sc <= 0x1p100f);
-    const float inv = 1.0f / sc;
+    if (a.norm == 0) continue;
+    const float f = normalize<NT, P>(u, in, a.norm == kNormLayer, inv_k, a.eps, slot + 4);
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (in[i]) {
-        u32x2 o;
-        if (a.code == A_FP8)
-          o = direct ? u32x2{e4m3_codes_divided(u[i], sc), e4m3_codes_divided(u[i] + 4, sc)}
-                     : u32x2{e4m3_codes(u[i], sc, inv), e4m3_codes(u[i] + 4, sc, inv)};
-        else
-          o = direct ? u32x2{int8_codes_divided(u[i], sc), int8_codes_divided(u[i] + 4, sc)}
-                     : u32x2{int8_codes(u[i], sc, inv), int8_codes(u[i] + 4, sc, inv)};
-        *(u32x2*)((uint8_t*)a.codes + r * a.k + 8 * (tid + NT * i)) = o;
+        if (!KEEP && a.weight) w[i] = piece(a.weight, i);
+        scale_by<T>(u[i], f, a.weight != nullptr, a.weight_offset, w[i]);
+        if (a.bias) {
+          if (!KEEP) b[i] = piece(a.bias, i);
+          float v[8];
+          unpack8<T>(b[i], v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[i][e] += v[e];
+        }
+        if (a.out) *(u32x4*)((uint16_t*)a.out + r * a.out_stride + 8 * (tid + NT * i)) = pack8<T>(u[i]);
       }
+    if (a.code == A_FP4) {
+      // a block of 32 lies in four neighbouring threads
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        float most = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = __builtin_elementwise_maximum(most, fabsf(u[i][e]));
+        most = __builtin_elementwise_maximum(most, neighbour<0xB1>(most));
+        most = __builtin_elementwise_maximum(most, neighbour<0x4E>(most));
+        uint32_t codes;
+        const uint32_t e8 = mxfp4_encode8(u[i], most, codes);
+        if (in[i]) {
+          const int c8 = tid + NT * i;
+          *(uint32_t*)((uint8_t*)a.codes + r * (a.k >> 1) + 4 * c8) = codes;
+          if ((c8 & 3) == 0) ((uint8_t*)a.scale)[r * (a.k >> 5) + (c8 >> 2)] = (uint8_t)e8;
+        }
+      }
+    } else if (a.code != 0) {
+      float amax = 0.f;                                       // (zeros behind the row's end)
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(u[i][e]));
+      amax = over_row<NT, true>(amax, slot[8]);
+      float sc = amax / (a.code == A_FP8 ? 448.0f : 127.0f);  // correctly rounded division
+      if (sc == 0.0f) sc = 1.0f;
+      if (!(amax < __builtin_inff())) sc = __builtin_nanf("");
+      if (tid == 0) ((float*)a.scale)[r] = sc;
+      const bool direct = !(sc >= 0x1p-100f && sc <= 0x1p100f);
+      const float inv = 1.0f / sc;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (in[i]) {
+          u32x2 o;
+          if (a.code == A_FP8)
+            o = direct ? u32x2{e4m3_codes_divided(u[i], sc), e4m3_codes_divided(u[i] + 4, sc)}
+                       : u32x2{e4m3_codes(u[i], sc, inv), e4m3_codes(u[i] + 4, sc, inv)};
+          else
+            o = direct ? u32x2{int8_codes_divided(u[i], sc), int8_codes_divided(u[i] + 4, sc)}
+                       : u32x2{int8_codes(u[i], sc, inv), int8_codes(u[i] + 4, sc, inv)};
+          *(u32x2*)((uint8_t*)a.codes + r * a.k + 8 * (tid + NT * i)) = o;
+        }
+    }
   }
 }
 
-constexpr int64_t kNormRowsPerLaunch = 1 << 21;   // a launch takes fewer than 2^32 threads
-
-template <int T, bool R32, int NT, int P>
-void launch_one(NormArgs a, hipStream_t st) {
+// Workgroups: with KEEP four waves' worth on every SIMD at most, each taking rows in turn.
+template <int T, bool R32, int NT, int P, bool KEEP>
+void launch_one(const NormArgs& a, hipStream_t st) {
   constexpr int RPB = NT < 256 ? 256 / NT : 1;
-  const int64_t rows = a.rows;
-  for (a.row0 = 0; a.row0 < rows; a.row0 += kNormRowsPerLaunch) {
-    a.rows = rows - a.row0 < kNormRowsPerLaunch ? rows : a.row0 + kNormRowsPerLaunch;
-    const unsigned grid = (unsigned)((a.rows - a.row0 + RPB - 1) / RPB);
-    hipLaunchKernelGGL((norm_rows_kernel<T, R32, NT, P>), dim3(grid), dim3(NT * RPB), 0, st, a);
-  }
+  const int64_t groups = (a.rows + RPB - 1) / RPB, most = KEEP ? 256 * (1024 / (NT * RPB)) : (int64_t)1 << 21;
+  const dim3 grid((unsigned)(groups < most ? groups : most));
+  hipLaunchKernelGGL((norm_rows_kernel<T, R32, NT, P, KEEP>), grid, dim3(NT * RPB), 0, st, a);
 }
 
 template <int T, bool R32>
 void launch_shape(const NormArgs& a, hipStream_t st) {
   const int64_t k = a.k;
-  if (k <= 512) launch_one<T, R32, 64, 1>(a, st);
-  else if (k <= 1024) launch_one<T, R32, 64, 2>(a, st);
-  else if (k <= 2048) launch_one<T, R32, 256, 1>(a, st);
-  else if (k <= 4096) launch_one<T, R32, 256, 2>(a, st);
-  else if (k <= 8192) launch_one<T, R32, 256, 4>(a, st);
-  else if (k <= 16384) launch_one<T, R32, 1024, 2>(a, st);
-  else launch_one<T, R32, 1024, 4>(a, st);
+  if (k <= 128) launch_one<T, R32, 16, 1, false>(a, st);
+  else if (k <= 512) launch_one<T, R32, 64, 1, false>(a, st);
+  else if (k <= 1024) launch_one<T, R32, 64, 2, false>(a, st);
+  else if (k <= 2048) launch_one<T, R32, 256, 1, true>(a, st);
+  else if (k <= 4096) launch_one<T, R32, 256, 2, true>(a, st);
+  else if (k <= 8192) launch_one<T, R32, 512, 2, true>(a, st);
+  else if (k <= 16384) launch_one<T, R32, 1024, 2, false>(a, st);
+  else launch_one<T, R32, 1024, 4, false>(a, st);
 }
 
 }  // namespace

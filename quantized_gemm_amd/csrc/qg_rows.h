@@ -60,8 +60,9 @@ __device__ __forceinline__ uint32_t int8_codes_divided(const float* v, float sc)
   return w;
 }
 
-// e4m3 codes of four values of a row, likewise; |quotient| <= 448 to a unit in the last place, which the conversion
-// (nearest even) takes to 448.  A row that is not finite has scale NaN and codes 0.
+// e4m3 codes of four values of a row.  One correction: a quotient that lies halfway between two codes is a float32 number,
+// which it gives exactly, and of the others one is a unit in the last place off at most.  |quotient| <= 448 to such a unit,
+// which the conversion (nearest even) takes to 448.  A row that is not finite has scale NaN and codes 0.
 __device__ __forceinline__ uint32_t e4m3_of(const float* q) {
   int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);   // bytes 0, 1
   v = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], v, true);        // bytes 2, 3
@@ -72,7 +73,6 @@ __device__ __forceinline__ uint32_t e4m3_codes(const float* v, float sc, float i
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     q[e] = v[e] * inv;
-    q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], sc, v[e]), inv, q[e]);
     q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], sc, v[e]), inv, q[e]);
   }
   return e4m3_of(q);
