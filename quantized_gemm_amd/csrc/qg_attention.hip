@@ -14,7 +14,7 @@
 //
 // so that no score or weight leaves its lane.  Codes times their power of two are exact in bf16, whatever the
 // queries' type.  bf16 queries multiply as they are and weights are rounded to bf16 (their sum, taken in float32
-// before, is not): an error of at most 2^-9 of each weight, of the size of the output's own rounding.  f16 has
+// before, is not): an error of at most 2^-8 of each weight, of the size of the output's own rounding.  f16 has
 // three bits more, so f16 queries and weights are taken as a high and a low bf16 part, which hold all of them.
 //
 // The maximum only moves when a score is more than 2^8 times above it: weights stay below 2^8 and the exchange
@@ -72,6 +72,11 @@ __device__ __forceinline__ int over_group(int row, const AttnArgs& a) {
   return a.group == 1 ? row : (int)__umulhi((uint32_t)row, a.group_inv);
 }
 
+// The sequence of workgroup (., y, z).  Workgroups go to the eight dies and on each to its four shader engines in turn, whatever
+// work they hold: were y the sequence itself, all of a sequence would go to one of them in batches of 4, 8, ... (4
+// sequences of 1152 to 4608 tokens, 512 queries each: 202 us, and 155 turned; decoding of equal ones alike).
+__device__ __forceinline__ int turned(uint32_t y, uint32_t z, uint32_t batch) { return (int)((y + z + (z >> 2)) % batch); }
+
 // Values d .. d + N - 1 of a row (a query and its head), and with the first of them its sum of weights and maximum: the
 // outputs, or one part's.
 template <int T, int D, int N>
@@ -115,12 +120,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
 
   // ---- the tile: sequence, key head, rows, tokens -------------------------------------
   // (key heads and sequences fastest: tiles that read the same keys run on the same XCD where their number allows)
-  const int hk = blockIdx.x, b = blockIdx.y;
-  int split = 0, tile = blockIdx.z;
-  if (a.nsplit > 1) {
-    tile = (int)blockIdx.z / a.nsplit;
-    split = (int)blockIdx.z - tile * a.nsplit;
-  }
+  const int hk = blockIdx.x, b = turned(blockIdx.y, blockIdx.z, gridDim.y);
+  const int split = blockIdx.z;
   int64_t q0 = b;
   int nq = 1;
   if (a.q_offsets) {
@@ -129,8 +130,8 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
     nq = min(nq, a.max_q);
   }
   const int row_count = nq * a.group;
-  const int row0 = tile * 16;
-  if (row0 >= row_count) return;
+  constexpr int row0 = 0;                           // (all rows are in one tile)
+  if (row_count <= 0) return;
   const int len = max(0, min(a.lens[b], a.max_len));
   int sees[RT], qrow[RT];                           // tokens that row 16 t + r sees; its query
 #pragma unroll
@@ -424,7 +425,9 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
 // order that lanes read (1 KiB per operand, 16 bytes per lane side by side), two images in turn, one barrier per 32
 // tokens.  Converted by every wave for itself the operands cost as many instructions as the softmax of 64 rows (RT = 4, 2048
 // rows, D = 128: 281 us).  RT is what leaves room for two waves per SIMD, one multiplying while the other
-// takes exponentials: those bound it, about as much as the products do.
+// takes exponentials: those bound it, about as much as the products do.  Products go before other waves' exponentials
+// (s_setprio: 5%), and the scheduler mixes a step's conversion into the products of the step before (10 to 15%).  D = 128,
+// bf16: a prompt of 4608 tokens (32 query heads over 8) 208 us, 836 TFLOP/s.
 template <int T, int D, int RT>
 __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(2))) void attention_rows_kernel(AttnArgs a) {
   constexpr bool HILO = T == O_F16;
@@ -434,14 +437,9 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, c = lane >> 4;
-  const int hk = blockIdx.x, b = blockIdx.y;
-  // (the last queries first: they see the most tokens)
-  int split = 0, tile = (int)(gridDim.z - 1 - blockIdx.z);
-  if (a.nsplit > 1) {
-    const int tiles = (int)gridDim.z / a.nsplit, z = (int)blockIdx.z / a.nsplit;
-    tile = tiles - 1 - z;
-    split = (int)blockIdx.z - z * a.nsplit;
-  }
+  const int hk = blockIdx.x, b = turned(blockIdx.y, blockIdx.z, gridDim.y);
+  // (the last queries first: they see the most tokens; and the first parts, which are whole)
+  const int tiles = (int)gridDim.z / a.nsplit, split = (int)blockIdx.z / tiles, tile = tiles - 1 - ((int)blockIdx.z - split * tiles);
   int64_t q0 = b;
   int nq = 1;
   if (a.q_offsets) {
@@ -521,17 +519,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   auto odd_value = [&](int step, const Odd& o, int h, int i) __attribute__((always_inline)) {
     return ((o.vs[h] >> (8 * i)) & 0xFFu) == 0xFFu && o.ok[h] && 32 * step + 16 * h + 4 * c + i < all_most;
   };
-  auto convert = [&](int step, const Raw& s, u32x4 (*to)[64], Odd& odd) __attribute__((always_inline)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < KQ; ++i) {
-        const int j = KQ * part + i;                // (D = 256: words 0-3 are of the first block)
-        const float p = __uint_as_float(D == 256 ? ((s.ks[h] >> (part >= 2 ? 8 : 0)) & 0xFFu) << 23 : power_bits(s.ks[h], 0));
-        if (D != 64 || wave < 2)
-          to[h * KW + j][lane] = u32x4{cvt_pair<0>(s.k[h][i], p), cvt_pair<1>(s.k[h][i], p), cvt_pair<2>(s.k[h][i], p), cvt_pair<3>(s.k[h][i], p)};
-      }
-    uint32_t vp[2][4];
+  auto powers = [&](int step, const Raw& s, uint32_t (&vp)[2][4], Odd& odd) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       odd.vs[h] = s.vs[h];
@@ -552,6 +540,17 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
         }
       odd.any = __any(bad);
     }
+  };
+  auto emit = [&](const Raw& s, const uint32_t (&vp)[2][4], u32x4 (*to)[64]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < KQ; ++i) {
+        const int j = KQ * part + i;                // (D = 256: words 0-3 are of the first block)
+        const float p = __uint_as_float(D == 256 ? ((s.ks[h] >> (part >= 2 ? 8 : 0)) & 0xFFu) << 23 : power_bits(s.ks[h], 0));
+        if (D != 64 || wave < 2)
+          to[h * KW + j][lane] = u32x4{cvt_pair<0>(s.k[h][i], p), cvt_pair<1>(s.k[h][i], p), cvt_pair<2>(s.k[h][i], p), cvt_pair<3>(s.k[h][i], p)};
+      }
 #pragma unroll
     for (int i = 0; i < VQ; ++i) {
       // pair `part` of the word (D = 64: of its half; D = 256: two pairs of the word that part / 2 names)
@@ -584,24 +583,33 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  auto compute = [&](int step, const u32x4 (*from)[64], const Odd& odd) __attribute__((always_inline)) {
+  auto compute = [&](int step, const u32x4 (*from)[64], const Odd& odd, auto&& beside) __attribute__((always_inline)) {
     // operands are read AHEAD of the products that take them
     constexpr int AHEAD = 3, NK = 2 * KW;
     u32x4 ring[AHEAD + 1];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) ring[i] = from[i][lane];
     f32x4 sc[RT][2];
+    __builtin_amdgcn_s_setprio(1);
+    beside();
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       const int h = i / KW, j = i % KW;
       ring[(i + AHEAD) % (AHEAD + 1)] = from[i + AHEAD][lane];     // (the first ones of the values at the end)
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         sc[t][h] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], qf[t][j], j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sc[t][h]);
         if constexpr (HILO) sc[t][h] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], ql[t][j], sc[t][h]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+#pragma unroll
+      for (int t = 0; t < RT * (HILO ? 2 : 1); ++t) {
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
     if (32 * step + 32 > least || !odd.ok[0] || !odd.ok[1]) {
 #pragma unroll
       for (int t = 0; t < RT; ++t)
@@ -644,6 +652,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
       pf[t] = bf16_high(p);
       if constexpr (HILO) pl[t] = bf16_low(p, pf[t]);
     }
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int i = NK + j;
@@ -655,6 +664,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
         if constexpr (HILO) acc[t][j] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], pl[t], acc[t][j]);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     if (odd.any) {
       u32x4 nan = {0, 0, 0, 0};
 #pragma unroll
@@ -674,25 +684,28 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
       }
     }
   };
-  // step n's image is made while step n - 1 is multiplied, from codes loaded a step earlier still
+  // step n's image is made among step n - 1's first products, from codes loaded a step earlier still
   if (begin < end) {
     Raw raw;
     Odd odd, odd_next;
+    uint32_t vp[2][4];
     load_ids(begin);
     load(begin, raw);
-    convert(begin, raw, image[0], odd);
+    powers(begin, raw, vp, odd);
+    emit(raw, vp, image[0]);
     load(min(begin + 1, end - 1), raw);
-    odd_next = odd;
     __syncthreads();
     for (int step = begin; step < end; ++step) {
       const int at = (step - begin) & 1;
-      if (step + 1 < end) {
-        convert(step + 1, raw, image[at ^ 1], odd_next);
-        const int later = min(step + 2, end - 1);
-        if (later - ids0 >= 32) load_ids(later);
+      const int next = min(step + 1, end - 1), later = min(step + 2, end - 1);      // (the last ones are made again, for nothing)
+      powers(next, raw, vp, odd_next);
+      if (later - ids0 >= 32) load_ids(later);
+      auto beside = [&]() __attribute__((always_inline)) {
+        emit(raw, vp, image[at ^ 1]);
         load(later, raw);
-      }
-      if (32 * step < most) compute(step, image[at], odd);
+      };
+      if (32 * step < most) compute(step, image[at], odd, beside);
+      else beside();
       odd = odd_next;
       __syncthreads();
     }
@@ -835,8 +848,8 @@ void launch_one(AttnArgs a, hipStream_t st) {
 
 // Parts of 32 * chunk tokens: of equal work whatever the sequences' lengths.  Decoding: as many as fill the GPU if all
 // sequences had the maximum, none shorter than 512 tokens (what a part costs beside its tokens).  Many rows: only while a
-// workgroup per tile leaves CUs without two (a prompt of 4608 tokens, 768 tiles: whole 255 us, in parts 424; 4
-// sequences with 512 new tokens each, 352 tiles: whole 270 us, in parts 225 and 18 to join them).
+// workgroup per tile leaves CUs without two (a prompt of 4608 tokens, 768 tiles: whole 210 us, in parts 222 and 15 to join
+// them; 4 sequences of up to 4608 tokens with 512 new ones each, 352 tiles: whole 203 us, in parts 155 and 18).
 AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
   const int64_t rows = max_q * (q_heads / kv_heads);
   const bool share = shares_rows(rows);
