@@ -547,6 +547,7 @@ qg_status qg_kv_read(const qg_kv_desc* desc, const void* cache, const int32_t* s
  *   tokens       rows of q and out.  Rows that belong to no sequence are neither read nor written.
  *   ws           qg_attention_workspace_bytes(...) bytes (0: none needed)
  * q_heads is a multiple of kv_heads, at most 256 times it; batch and max_q <= 65535.
+ * scale is finite, in powers of two too (below 2.3e38).
  * The result depends on batch, max_q and max_len (which set how the tokens are split) in its last bits only.
  */
 size_t qg_attention_workspace_bytes(const qg_kv_desc* desc, int32_t q_heads, int64_t batch, int64_t max_q, int64_t tokens,

@@ -14,7 +14,9 @@ using namespace qg;
 namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 32;
+constexpr int64_t kLoraMaxTokens = (int64_t)1 << 24;
 constexpr int kCUs = 256;
+constexpr float kLog2e = 1.44269504088896f;
 
 int log2_of(int v) {
   int s = 0;
@@ -75,7 +77,7 @@ qg_status check_kv(const qg_kv_desc* d) {
   if (!type16(d->type) || d->kv_heads <= 0 || d->num_pages <= 0 || d->page_tokens <= 0) return QG_ERR_INVALID_ARG;
   if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return QG_ERR_UNSUPPORTED;
   if (d->page_tokens < 16 || d->page_tokens > 256 || (d->page_tokens & (d->page_tokens - 1)) != 0) return QG_ERR_UNSUPPORTED;
-  if (d->kv_heads > 1024 || d->num_pages * d->page_tokens > ((int64_t)1 << 31) - 1) return QG_ERR_UNSUPPORTED;
+  if (d->kv_heads > 1024 || d->num_pages > (((int64_t)1 << 31) - 1) / d->page_tokens) return QG_ERR_UNSUPPORTED;
   return QG_OK;
 }
 
@@ -158,7 +160,7 @@ static size_t lora_workspace(const qg_lora_desc* d, int64_t tokens, int32_t bloc
 }
 
 size_t qg_lora_workspace_bytes(const qg_lora_desc* d, int64_t tokens, int32_t block_m) {
-  if (check_lora(d) != QG_OK || tokens <= 0 || !lora_block(block_m)) return 0;
+  if (check_lora(d) != QG_OK || tokens <= 0 || tokens > kLoraMaxTokens || !lora_block(block_m)) return 0;
   return lora_workspace(d, tokens, block_m, nullptr);
 }
 
@@ -169,7 +171,7 @@ qg_status qg_lora(const qg_lora_desc* d, const void* x, const void* a_weight, co
   if (s != QG_OK) return s;
   if (tokens < 0) return QG_ERR_INVALID_ARG;
   if (!lora_block(block_m)) return QG_ERR_UNSUPPORTED;
-  if (tokens > (int64_t)1 << 24) return QG_ERR_UNSUPPORTED;
+  if (tokens > kLoraMaxTokens) return QG_ERR_UNSUPPORTED;
   if (tokens == 0) return QG_OK;
   if (!x || !a_weight || !b_weight || !sorted_ids || !expert_ids || !num_post_pad || !base || !y) return QG_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(a_weight) || !aligned16(b_weight) || !aligned16(base) || !aligned16(y) ||
@@ -266,9 +268,9 @@ qg_status qg_attention(const qg_kv_desc* d, const void* q, int64_t q_stride, int
   if (s != QG_OK) return s;
   AttnArgs a{};
   const int64_t width = (int64_t)q_heads * d->head_dim;
-  if (!finite(scale) || !stride_of(q_stride, width, &a.q_stride) || !stride_of(out_stride, width, &a.out_stride))
+  if (!finite(scale * kLog2e) || !stride_of(q_stride, width, &a.q_stride) || !stride_of(out_stride, width, &a.out_stride))
     return QG_ERR_INVALID_ARG;
-  if (table_stride < 0 || table_stride * d->page_tokens < max_len) return QG_ERR_INVALID_ARG;
+  if (table_stride < 0 || table_stride > kMaxStride || table_stride * d->page_tokens < max_len) return QG_ERR_INVALID_ARG;
   if (!q_offsets && (max_q != 1 || tokens != batch)) return QG_ERR_INVALID_ARG;
   if (batch == 0 || tokens == 0) return QG_OK;
   if (!q || !out || !cache || !seq_lens || (!block_table && max_len > 0)) return QG_ERR_INVALID_ARG;
@@ -294,7 +296,8 @@ qg_status qg_attention(const qg_kv_desc* d, const void* q, int64_t q_stride, int
   a.table_stride = table_stride; a.num_pages = d->num_pages; a.tokens = tokens; a.rows = tokens * q_heads;
   a.batch = (int)batch; a.q_heads = q_heads; a.kv_heads = d->kv_heads; a.dim = d->head_dim;
   a.page_shift = log2_of(d->page_tokens); a.max_q = (int)max_q; a.max_len = (int)max_len;
-  a.scale_log2 = fabsf(scale) * 1.44269504088896f;
+  // (scores of tokens that are not seen are -infinity, before the scale: times 0 they would be NaN)
+  a.scale_log2 = std::max(fabsf(scale) * kLog2e, 0x1p-149f);
   a.q_sign = scale < 0 ? 0x80008000u : 0;
   QG_LOG("attention batch=%lld heads=%d/%d dim=%d max_q=%lld max_len=%lld -> splits=%d", (long long)batch, q_heads,
          d->kv_heads, d->head_dim, (long long)max_q, (long long)max_len, a.nsplit);

@@ -3,13 +3,15 @@
 //   t[m][s] = x[m] A[a, s]^T over the adapter's rank rows,  y[m][n] = base[m][n] + scale[a] sum_r t[m][s(n)][r] B[a, n, r]
 //
 // for the adapter a of token m and the slice s(n) of column n.  Tokens come in blocks of BM rows of one adapter
-// (qg_moe_align's map).  Two launches: the first makes t in float32 (partial sums over `ksplit` parts of K, each
-// in a place of its own, so that no order is left to chance), the second adds the parts and multiplies by B.
+// (qg_moe_align's map).  The first product makes t in float32, partial sums over `ksplit` parts of K, each
+// in a place of its own, so that no order is left to chance.  Few tokens (blocks of 16): the second one adds the parts
+// itself, two launches in all, which bound them (1 token, 7168 to 7168, rank 16: 4.2 + 4.3 us).  Many: a launch between
+// adds them once, and both products pass their operands through LDS.  Bound by bytes, of which the second product's
+// outputs, read and written, are most (8192 tokens, 4096 to 2 x 2816, rank 128, 252 MB: 43 + 10 + 65 us).
 //
 // Both products run on 16x16x32 MFMAs with the adapter's rows as first operand, so that a lane's sums belong to
 // one token: four ranks side by side of t, and, with the columns of two tiles interleaved, eight columns
-// side by side of y.  Operands go from memory to registers: an adapter's rows are read by one workgroup (few
-// tokens) or stay in the caches (many).
+// side by side of y.
 //
 // t is split into two 16-bit numbers, high and low part, which together carry at least 16 (bf16) or 22 (f16) bits
 // of it: one number alone would cost the last bit of y.  f16 parts are taken from t over a power of two of the

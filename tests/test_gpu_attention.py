@@ -245,6 +245,14 @@ def test_tokens_on_pages_outside_the_cache_are_not_seen():
     Case([30], 4, 1, 128, 32, bad_pages=[(0, 0)]).run().check()      # nothing is seen: zeros
 
 
+@pytest.mark.parametrize("counts", [[1, 1, 1], [9, 40, 3]])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-45, -0.25])
+def test_scales_of_nothing_and_below(scale, counts):
+    c = Case([33, 70, 517], 16, 2, 64, 16, counts=counts)
+    c.scale = scale
+    c.run().check()
+
+
 def test_large_scores():
     # softmax close to a choice: scores of a hundred and more; weights that vanish
     c = Case([500, 33], 4, 2, 128, 16, sigma=6.0)

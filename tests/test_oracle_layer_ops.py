@@ -179,3 +179,23 @@ def test_attention_workspace_holds_whole_splits(batch, max_q, max_len):
         need = qg.attention_workspace_bytes(d, 8, batch, max_q, batch * max_q, max_len)
         one = batch * max_q * 8 * (dim + 2) * 4
         assert need % one == 0 and need // one != 1
+
+
+def test_sizes_beyond_64_bits_are_refused():
+    lib = qg.lib()
+    far = qg.make_kv_desc(qg.O_BF16, 1, 64, 256, 1 << 60)
+    assert qg.kv_cache_bytes(far) == 0
+    assert lib.qg_kv_append(ctypes.byref(far), FAKE, 0, FAKE, 0, FAKE, 4, FAKE, None) == 2
+    d = qg.make_kv_desc(qg.O_BF16, 1, 64, 16, 4)
+
+    def attn(table_stride, scale):
+        return lib.qg_attention(ctypes.byref(d), FAKE, 0, 1, FAKE, FAKE, table_stride, FAKE, None, 1, 1, 1, 64, scale, FAKE, 0, FAKE,
+                                1 << 30, None)
+
+    assert attn((1 << 60) + 4, 1.0) == 1                            # rows of the table that 64 bits of bytes do not hold
+    assert attn(4, 3e38) == 1 and attn(4, -3e38) == 1               # (infinite in powers of two)
+    lora = qg.make_lora_desc(qg.O_BF16, 2, 16, 64, [64])
+    assert qg.lora_workspace_bytes(lora, 1 << 24, 16) > 0
+    assert qg.lora_workspace_bytes(lora, (1 << 24) + 1, 16) == 0 and qg.lora_workspace_bytes(lora, 1 << 62, 64) == 0
+    assert lib.qg_lora(ctypes.byref(lora), FAKE, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, 1 << 62, 16, FAKE, FAKE, FAKE, 1 << 62,
+                       None) == 2
