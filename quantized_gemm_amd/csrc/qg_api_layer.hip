@@ -89,6 +89,7 @@ KvArgs kv_args(const qg_kv_desc* d, const int32_t* slots, int64_t tokens, const 
   a.num_slots = d->num_pages * d->page_tokens;
   a.heads = d->kv_heads;
   a.dim = d->head_dim;
+  a.dim_shift = log2_of(d->head_dim);
   a.page_shift = log2_of(d->page_tokens);
   return a;
 }

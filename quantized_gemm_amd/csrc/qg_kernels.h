@@ -174,7 +174,7 @@ struct KvArgs {
   uint8_t* cache;
   const int32_t* slots;
   int64_t tokens, k_stride, v_stride, num_slots;
-  int heads, dim, page_shift;
+  int heads, dim, dim_shift, page_shift;
 };
 void launch_kv_append(const KvArgs& a, int type, hipStream_t st);
 void launch_kv_read(const KvArgs& a, int type, hipStream_t st);
