@@ -4,8 +4,9 @@
  * What it computes: Y = X . dequant(Wq, scales, zeros)^T with low-bit weights
  * (int4 / uint4 + zero points, FP4 e2m1 with UE8M0 block scales, FP8 e4m3 with
  * channel scales, int8 with channel scales) and f16 / bf16 / FP8 e4m3 / int8 activations,
- * as a dense layer and as an MoE grouped GEMM over routed tokens.  Sources: the web pages on the Humming
- * quantized-GEMM library -- "Humming" (README), "Key Features" and "Support Matrix"
+ * as a dense layer and as an MoE grouped GEMM over routed tokens; the rest of an MoE layer; and what stands around a
+ * decoder layer's products (qg_norm_rows, qg_lora, qg_kv_append and qg_kv_read, qg_attention).
+ * Sources: the web pages on the Humming quantized-GEMM library -- "Humming" (README), "Key Features" and "Support Matrix"
  * (weight, activation and scale types; dense and MoE GEMM); "Humming: Fast,
  * Flexible Kernels for Quantized Inference" (the standard format of weights,
  * scales and zero points; preprocessing that repacks tensors into the kernel's
@@ -32,7 +33,7 @@
  *   buffer of at least that size; its contents need no initialisation (a call writes
  *   every byte it reads).  Calls that share one workspace must not run concurrently
  *   (use one per stream).
- * - Shape rules: n % 64 == 0, k % 128 == 0, k % group_k == 0.
+ * - Shape rules of the products: n % 64 == 0, k % 128 == 0, k % group_k == 0.  (The other entry points name theirs.)
  */
 #ifndef QG_H_
 #define QG_H_
