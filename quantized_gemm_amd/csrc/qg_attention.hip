@@ -849,7 +849,8 @@ void launch_one(AttnArgs a, hipStream_t st) {
 // Parts of 32 * chunk tokens: of equal work whatever the sequences' lengths.  Decoding: as many as fill the GPU if all
 // sequences had the maximum, none shorter than 512 tokens (what a part costs beside its tokens).  Many rows: only while a
 // workgroup per tile leaves CUs without two (a prompt of 4608 tokens, 768 tiles: whole 210 us, in parts 222 and 15 to join
-// them; 4 sequences of up to 4608 tokens with 512 new ones each, 352 tiles: whole 203 us, in parts 155 and 18).
+// them; 4 sequences of up to 4608 tokens with 512 new ones each, 352 tiles: whole 203 us, in three parts 158
+// and 18, in two 160 and 12; one sequence of 8192 with 2048 new ones, 344 tiles: three 321 and 21, two 358 and 15).
 AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
   const int64_t rows = max_q * (q_heads / kv_heads);
   const bool share = shares_rows(rows);
