@@ -41,7 +41,7 @@ def _dev(rng, *shape, scale=1.0, mean=0.0):
 
 
 class Block:
-    def __init__(self, counts, held, seed):
+    def __init__(self, counts, held, seed, ws=None):
         """counts: new tokens of each sequence; held: tokens that its cache holds already."""
         rng = np.random.default_rng(seed)
         self.rng, self.counts, self.held = rng, list(counts), list(held)
@@ -87,7 +87,8 @@ class Block:
         need = max(qg.lora_workspace_bytes(self.lora, t, self.block),
                    qg.attention_workspace_bytes(self.kv, HEADS, b, self.max_q, t, self.max_len),
                    *(qg.workspace_bytes(p, t) for p, _ in self.p))
-        self.ws = by(max(1, need))                                 # one for all: they run in turn
+        self.ws = by(max(1, need)) if ws is None else ws           # one for all: they run in turn
+        assert self.ws.numel() >= need
 
     def slots(self, i, begin, end):
         at = np.arange(begin, end)
@@ -183,3 +184,42 @@ def test_a_block(counts, held):
         c.fill(ids(turn))
         graph.replay()
         c.check()
+
+
+IDS = [0, -1, 2, 1, 7]
+
+
+def test_two_graphs_share_a_workspace():
+    ws = torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda")
+    blocks = [Block([1, 1, 1], [90, 0, 47], 7, ws), Block([30, 1, 9], [2, 64, 15], 8, ws)]
+    graphs = []
+    for c in blocks:
+        c.fill([IDS[i % 5] for i in range(c.t)])
+        c.run()
+        c.check()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.run()
+        graphs.append(graph)
+    for turn in range(1, 4):
+        for c in blocks:
+            c.fill([IDS[(i + turn) % 5] for i in range(c.t)])
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        for c in blocks:
+            c.check()
+
+
+def test_two_streams_at_once():
+    blocks = [Block([1, 1, 1, 1], [90, 0, 47, 15], 9), Block([30, 1, 9], [2, 64, 15], 10)]
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for turn in range(3):
+        for c in blocks:
+            c.fill([IDS[(i + turn) % 5] for i in range(c.t)])
+        torch.cuda.synchronize()
+        for c, stream in zip(blocks, streams):
+            with torch.cuda.stream(stream):
+                c.run()
+        for c in blocks:
+            c.check()
