@@ -24,7 +24,8 @@ namespace qg {
 
 namespace {
 
-// The value of the lane whose place in its four neighbours is this one's, XOR 1 (M = 0xB1) or XOR 2 (0x4E).
+// The value of another lane of its 16: M = 0xB1 and 0x4E the one whose place is this one's XOR 1 or 2, 0x141 and 0x140 its
+// mirror image in eight and in sixteen.
 template <int M>
 __device__ __forceinline__ float neighbour(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), M, 0xF, 0xF, true));
@@ -37,17 +38,26 @@ constexpr int kSlots = NT > 64 ? NT / 64 : 1;
 // A sum or a NaN-keeping maximum over the NT threads of a row; `slot`: NT / 64 words of LDS of its own.
 template <int NT, bool MAX>
 __device__ __forceinline__ float over_row(float v, float* slot) {
-#pragma unroll
-  for (int off = (NT < 64 ? NT : 64) / 2; off >= 1; off >>= 1) {
-    const float o = __shfl_xor(v, off, 64);
-    v = MAX ? __builtin_elementwise_maximum(v, o) : v + o;
+  auto with = [](float x, float y) __attribute__((always_inline)) { return MAX ? __builtin_elementwise_maximum(x, y) : x + y; };
+  // (in the vector unit: exchanges through LDS take several times as long)
+  v = with(v, neighbour<0xB1>(v));
+  v = with(v, neighbour<0x4E>(v));
+  v = with(v, neighbour<0x141>(v));
+  v = with(v, neighbour<0x140>(v));
+  if constexpr (NT >= 64) {
+    const uint32_t w = __float_as_uint(v);
+    const auto rows = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    v = with(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
+    const uint32_t h = __float_as_uint(v);
+    const auto halves = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    v = with(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
   }
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slot[0];
 #pragma unroll
-    for (int w = 1; w < NT / 64; ++w) v = MAX ? __builtin_elementwise_maximum(v, slot[w]) : v + slot[w];
+    for (int w = 1; w < NT / 64; ++w) v = with(v, slot[w]);
   }
   return v;
 }
