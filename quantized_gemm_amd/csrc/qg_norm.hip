@@ -13,9 +13,10 @@
 // 8192 values are taken in turn by a workgroup (KEEP), the next one's loads on their way during one's sums, and weights and
 // a shared gate stay in registers.  Longer rows lack the registers for it (2048 rows of 16384 values: 57 us, in turn 150),
 // and shorter ones need no barrier to wait at (65536 rows of 512: 47 us, in turn 53); those are one to a workgroup or part
-// of it, and read the weights again.  Measured: 16384 rows of 4096, both norms, gate and residual, 135 us (3.5 TB/s; 155
-// with a workgroup per row); 4096 rows of 7168 to e4m3 53 us (68); one row of 7168 to e4m3 4.7 us (6.7); 65536 rows of 128
-// 14 us (29 with a whole wave to a row).
+// of it, and read the weights again.  Workgroups that are no more than the GPU holds at once: 16384 rows of 4096 in 768
+// workgroups 95 us, in 1024 115.  Measured: those (both norms, gate, residual, to e4m3) 95 us, 4.9 TB/s (155 with a
+// workgroup per row, 137 with sums exchanged through LDS); 4096 rows of 7168 to e4m3 45 us; one 4.3 us; 65536 rows of 128 13
+// us (29 with a whole wave to a row).
 #include "qg_device.h"
 #include "qg_kernels.h"
 #include "qg_rows.h"
@@ -319,11 +320,12 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_rows_kernel(NormArgs
   }
 }
 
-// Workgroups: with KEEP four waves' worth on every SIMD at most, each taking rows in turn.
+// Workgroups: with KEEP as many as the GPU holds at once, each taking rows in turn (4 waves per SIMD with one piece per thread,
+// 3 with two).
 template <int T, bool R32, int NT, int P, bool KEEP>
 void launch_one(const NormArgs& a, hipStream_t st) {
-  constexpr int RPB = NT < 256 ? 256 / NT : 1;
-  const int64_t groups = (a.rows + RPB - 1) / RPB, most = KEEP ? 256 * (1024 / (NT * RPB)) : (int64_t)1 << 21;
+  constexpr int RPB = NT < 256 ? 256 / NT : 1, WAVES = P == 1 ? 16 : 12;
+  const int64_t groups = (a.rows + RPB - 1) / RPB, most = KEEP ? 256 * (WAVES / (NT * RPB / 64)) : (int64_t)1 << 21;
   const dim3 grid((unsigned)(groups < most ? groups : most));
   hipLaunchKernelGGL((norm_rows_kernel<T, R32, NT, P, KEEP>), grid, dim3(NT * RPB), 0, st, a);
 }
