@@ -761,13 +761,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   // every wave: maximum and sum of all parts (64 or fewer, one per lane)
   const float ms = lane * a.chunk < steps ? ml[(int64_t)lane * a.rows * 2] : kNegInf;
   const float ls = lane * a.chunk < steps ? ml[(int64_t)lane * a.rows * 2 + 1] : 0.f;
-  float top = ms;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  const float top = over_lanes<64>(ms, [](float x, float y) { return fmaxf(x, y); });
   const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - top);
-  float sum = ls * f;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  const float sum = over_lanes<64>(ls * f, [](float x, float y) { return x + y; });
   if (tid < 64) weight[lane] = f;
   __syncthreads();
   const int g = tid / LPR, d = (tid % LPR) * 4;

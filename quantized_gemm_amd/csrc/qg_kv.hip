@@ -15,11 +15,6 @@ namespace qg {
 
 namespace {
 
-template <int M>
-__device__ __forceinline__ float neighbour(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), M, 0xF, 0xF, true));
-}
-
 // Where 8 values (word w) of a token's head are: codes and exponent byte.
 struct KvPlace { uint8_t *codes, *scale; };
 __device__ __forceinline__ KvPlace place_of(const KvArgs& a, bool value, int64_t slot, int head, int w) {

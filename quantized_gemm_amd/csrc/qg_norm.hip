@@ -25,13 +25,6 @@ namespace qg {
 
 namespace {
 
-// The value of another lane of its 16: M = 0xB1 and 0x4E the one whose place is this one's XOR 1 or 2, 0x141 and 0x140 its
-// mirror image in eight and in sixteen.
-template <int M>
-__device__ __forceinline__ float neighbour(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), M, 0xF, 0xF, true));
-}
-
 // Words that the waves of a row leave their sums in.
 template <int NT>
 constexpr int kSlots = NT > 64 ? NT / 64 : 1;
@@ -40,19 +33,7 @@ constexpr int kSlots = NT > 64 ? NT / 64 : 1;
 template <int NT, bool MAX>
 __device__ __forceinline__ float over_row(float v, float* slot) {
   auto with = [](float x, float y) __attribute__((always_inline)) { return MAX ? __builtin_elementwise_maximum(x, y) : x + y; };
-  // (in the vector unit: exchanges through LDS take several times as long)
-  v = with(v, neighbour<0xB1>(v));
-  v = with(v, neighbour<0x4E>(v));
-  v = with(v, neighbour<0x141>(v));
-  v = with(v, neighbour<0x140>(v));
-  if constexpr (NT >= 64) {
-    const uint32_t w = __float_as_uint(v);
-    const auto rows = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-    v = with(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
-    const uint32_t h = __float_as_uint(v);
-    const auto halves = __builtin_amdgcn_permlane32_swap(h, h, false, false);
-    v = with(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
-  }
+  v = over_lanes<(NT < 64 ? NT : 64)>(v, with);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
     __syncthreads();

@@ -105,4 +105,31 @@ __device__ __forceinline__ uint32_t mxfp4_encode8(const float* v, float amax, ui
   return (uint32_t)(e + 127);
 }
 
+// The value of another lane of its 16: M = 0xB1 and 0x4E the one whose place is this one's XOR 1 or 2, 0x141 and 0x140 its
+// mirror image in eight and in sixteen.
+template <int M>
+__device__ __forceinline__ float neighbour(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), M, 0xF, 0xF, true));
+}
+
+// A symmetric operation over 16 or all 64 lanes, the same bits in each.  (in the vector unit: exchanges through LDS take several
+// times as long)
+template <int N, typename F>
+__device__ __forceinline__ float over_lanes(float v, F with) {
+  static_assert(N == 16 || N == 64, "rows of lanes or a wave");
+  v = with(v, neighbour<0xB1>(v));
+  v = with(v, neighbour<0x4E>(v));
+  v = with(v, neighbour<0x141>(v));
+  v = with(v, neighbour<0x140>(v));
+  if constexpr (N == 64) {
+    const uint32_t w = __float_as_uint(v);
+    const auto rows = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    v = with(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
+    const uint32_t h = __float_as_uint(v);
+    const auto halves = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    v = with(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
+  }
+  return v;
+}
+
 }  // namespace qg
