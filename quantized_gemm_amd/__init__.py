@@ -405,11 +405,23 @@ def attention_workspace_bytes(desc: KvDesc, q_heads: int, batch: int, max_q: int
     return lib().qg_attention_workspace_bytes(ctypes.byref(desc), q_heads, batch, max_q, tokens, max_len)
 
 
+def _table(table, page_tokens: int, max_len: int):
+    """Address of a block table and the distance of its rows, as its tensor has them (a slice of a wider one, too)."""
+    if table is None:
+        return None, 0
+    width = table.shape[-1]
+    if width * page_tokens < max_len or (width > 1 and table.stride(-1) != 1) or (table.dim() > 2 and not table.is_contiguous()):
+        raise QGError(1, "qg_attention")
+    return table.data_ptr(), table.stride(0) if table.dim() == 2 and table.shape[0] > 1 else width
+
+
 def attention(desc: KvDesc, q, q_heads: int, cache, block_table, seq_lens, batch: int, max_len: int, scale: float, out, ws=None,
               q_offsets=None, max_q: int = 1, tokens: int | None = None, q_stride: int = 0, out_stride: int = 0, stream=None):
     """Causal attention of each sequence's newest queries over its tokens in the MXFP4 cache; block_table [batch][pages]
-    int32; tokens: rows of q (default: its first dimension)."""
-    st = lib().qg_attention(ctypes.byref(desc), _ptr(q), q_stride, q_heads, _ptr(cache), _ptr(block_table), block_table.shape[-1],
+    int32, its rows as far apart as its stride says (None: no sequence has tokens, max_len 0); tokens: rows of q (default:
+    its first dimension)."""
+    table, table_stride = _table(block_table, desc.page_tokens, max_len)
+    st = lib().qg_attention(ctypes.byref(desc), _ptr(q), q_stride, q_heads, _ptr(cache), table, table_stride,
                             _ptr(seq_lens), _ptr(q_offsets), batch, max_q, q.shape[0] if tokens is None else tokens, max_len,
                             scale, _ptr(out), out_stride, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                             _stream(stream))
