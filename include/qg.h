@@ -544,7 +544,8 @@ qg_status qg_kv_read(const qg_kv_desc* desc, const void* cache, const int32_t* s
  *                holds its tokens j * page_tokens and on.  Tokens of a page outside [0, num_pages) are not seen.
  *   seq_lens     device int32 [batch], taken into [0, max_len]
  *   q_offsets    device int32 [batch + 1]: sequence b's queries are rows q_offsets[b] .. q_offsets[b + 1] - 1 of q and
- *                out, at most max_q of them; NULL: one query per sequence (max_q 1, tokens == batch)
+ *                out, at most max_q of them (offsets are taken into [0, tokens]; none where they descend); NULL: one query
+ *                per sequence (max_q 1, tokens == batch)
  *   tokens       rows of q and out.  Rows that belong to no sequence are neither read nor written.
  *   ws           qg_attention_workspace_bytes(...) bytes (0: none needed)
  * q_heads is a multiple of kv_heads, at most 256 times it; batch and max_q <= 65535.

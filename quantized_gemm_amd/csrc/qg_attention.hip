@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "qg_attention_rows.h"
 #include "qg_device.h"
 #include "qg_kernels.h"
 #include "qg_rows.h"
@@ -70,6 +71,12 @@ struct Step {
 // row / group for rows below 2^24 and groups of at most 256: group_inv = ceil(2^32 / group)
 __device__ __forceinline__ int over_group(int row, const AttnArgs& a) {
   return a.group == 1 ? row : (int)__umulhi((uint32_t)row, a.group_inv);
+}
+
+// A sequence's rows of queries and outputs.
+__device__ __forceinline__ Queries queries_of(const AttnArgs& a, int b) {
+  if (!a.q_offsets) return Queries{b, 1};
+  return sequence_queries(a.q_offsets[b], a.q_offsets[b + 1], a.tokens, a.max_q);
 }
 
 // The sequence of workgroup (., y, z).  Workgroups go to the eight dies and on each to its four shader engines in turn, whatever
@@ -122,13 +129,9 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   // (key heads and sequences fastest: tiles that read the same keys run on the same XCD where their number allows)
   const int hk = blockIdx.x, b = turned(blockIdx.y, blockIdx.z, gridDim.y);
   const int split = blockIdx.z;
-  int64_t q0 = b;
-  int nq = 1;
-  if (a.q_offsets) {
-    q0 = max(0, a.q_offsets[b]);
-    nq = (int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0);
-    nq = min(nq, a.max_q);
-  }
+  const Queries rows = queries_of(a, b);
+  const int64_t q0 = rows.first;
+  const int nq = rows.count;
   const int row_count = nq * a.group;
   constexpr int row0 = 0;                           // (all rows are in one tile)
   if (row_count <= 0) return;
@@ -440,13 +443,9 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
   const int hk = blockIdx.x, b = turned(blockIdx.y, blockIdx.z, gridDim.y);
   // (the last queries first: they see the most tokens; and the first parts, which are whole)
   const int tiles = (int)gridDim.z / a.nsplit, split = (int)blockIdx.z / tiles, tile = tiles - 1 - ((int)blockIdx.z - split * tiles);
-  int64_t q0 = b;
-  int nq = 1;
-  if (a.q_offsets) {
-    q0 = max(0, a.q_offsets[b]);
-    nq = (int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0);
-    nq = min(nq, a.max_q);
-  }
+  const Queries rows = queries_of(a, b);
+  const int64_t q0 = rows.first;
+  const int nq = rows.count;
   constexpr int ROWS = 16 * RT * kAttnWaves;
   const int row_count = nq * a.group, tile0 = tile * ROWS, row0 = tile0 + wave * 16 * RT;
   if (tile0 >= row_count) return;
@@ -746,12 +745,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   __shared__ float weight[kMaxParts];
   __shared__ __attribute__((aligned(16))) float sums[GROUPS][D];
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
-  int64_t q0 = b;
-  int nq = 1;
-  if (a.q_offsets) {
-    q0 = max(0, a.q_offsets[b]);
-    nq = min((int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0), a.max_q);
-  }
+  const Queries rows = queries_of(a, b);
+  const int64_t q0 = rows.first;
+  const int nq = rows.count;
   const int head = blockIdx.x, qi = blockIdx.z;
   if (qi >= nq) return;
   const int steps = steps_of(a, b, nq, qi, head);
@@ -786,12 +782,9 @@ template <int T, int D>
 __global__ __launch_bounds__(256) void attention_join_rows_kernel(AttnArgs a) {
   constexpr int LPR = D / 4, RPB = 256 / LPR;
   const int b = blockIdx.y, qi = blockIdx.z;
-  int64_t q0 = b;
-  int nq = 1;
-  if (a.q_offsets) {
-    q0 = max(0, a.q_offsets[b]);
-    nq = min((int)(min((int64_t)a.q_offsets[b + 1], a.tokens) - q0), a.max_q);
-  }
+  const Queries rows = queries_of(a, b);
+  const int64_t q0 = rows.first;
+  const int nq = rows.count;
   const int head = (int)blockIdx.x * RPB + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
   if (qi >= nq || head >= a.q_heads) return;
   const int steps = steps_of(a, b, nq, qi, head);

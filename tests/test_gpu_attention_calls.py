@@ -29,3 +29,24 @@ def test_a_table_cut_from_a_wider_one(counts):
     c.run().check()
     c.table = torch.cat([table, torch.full_like(table, -1)], 0)[:3]
     c.run().check()
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_malformed_offsets_take_rows_that_there_are(many):
+    # offsets outside the rows, descending, and far enough apart that their difference leaves 32 bits: the rows between them
+    # that exist, max_q at most (below zero is the first row), and no others
+    n = 90 if many else 3
+    c = Case([100, 700, 31, 9], 8, 2, 128, 16, counts=[n, 2, 0, 0])
+    low, high = -2 ** 31, 2 ** 31 - 1
+    used = c.used
+    for offsets in ([high, low, 0, 0, 0], [used + 3, 1 << 24, high, high, high], [low, -7, low, -1, 0], [used, high, low, high, low]):
+        c.offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+        c.out.fill_(float("nan"))
+        c.run()
+        torch.cuda.synchronize()
+        taken = {row for b, e in zip(offsets, offsets[1:]) for row in list(range(max(0, b), min(e, used)))[:c.max_q]}
+        written = [row for row in range(used) if not torch.isnan(c.out[row]).any()]
+        assert written == sorted(taken), offsets
+        assert torch.isnan(c.out).any(1).sum() == torch.isnan(c.out).all(1).sum()
+    c.offsets.copy_(torch.tensor([0, n, used, high, low], dtype=torch.int32))          # the first two as they should be
+    c.run().check()
