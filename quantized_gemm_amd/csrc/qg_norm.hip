@@ -88,7 +88,8 @@ __device__ __forceinline__ float normalize(float (&v)[P][8], const bool (&in)[P]
     for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = __builtin_ldexpf(v[i][e], down);
-    eps = __builtin_ldexpf(eps, 2 * down);
+    // (a row of one value has no variance left: not over zero, which would make its zeros NaN)
+    eps = fmaxf(__builtin_ldexpf(eps, 2 * down), 0x1p-126f);
   }
   if (layer) centre(slots[2]);
   const float ss = over_row<NT, false>(squares(), slots[3]);
