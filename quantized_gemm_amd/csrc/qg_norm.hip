@@ -6,7 +6,8 @@
 //
 // Everything between the loads and the stores is float32: u goes into the second norm, and z into the codes,
 // without being rounded to 16 bits in between.  The mean square is taken from the values less their mean (a
-// second sum over registers), which loses nothing where the mean is far from zero.
+// second sum over registers), which loses nothing where the mean is far from zero.  The mean is kept between the row's
+// least and largest value: of a row whose values are all alike zeros are left, not a last bit of them over sqrt(eps).
 //
 // Bound by bytes.  A row stays in registers between the sums (P pieces of 8 values per thread), so that each
 // input is read once; NT threads share a row, and a sum over them is a wave's exchange plus one barrier.  Rows of 1025 to
@@ -29,20 +30,34 @@ namespace {
 template <int NT>
 constexpr int kSlots = NT > 64 ? NT / 64 : 1;
 
-// A sum or a NaN-keeping maximum over the NT threads of a row; `slot`: NT / 64 words of LDS of its own.
-template <int NT, bool MAX>
-__device__ __forceinline__ float over_row(float v, float* slot) {
+// Sums or NaN-keeping maxima of N values over the NT threads of a row; `slots`: NT / 64 words of LDS for each.
+template <int NT, bool MAX, int N>
+__device__ __forceinline__ void over_row(float (&v)[N], float (*slots)[kSlots<NT>]) {
   auto with = [](float x, float y) __attribute__((always_inline)) { return MAX ? __builtin_elementwise_maximum(x, y) : x + y; };
-  v = over_lanes<(NT < 64 ? NT : 64)>(v, with);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = slot[0];
 #pragma unroll
-    for (int w = 1; w < NT / 64; ++w) v = with(v, slot[w]);
+  for (int n = 0; n < N; ++n) v[n] = over_lanes<(NT < 64 ? NT : 64)>(v[n], with);
+  if constexpr (NT > 64) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if ((threadIdx.x & 63) == 0) slots[n][threadIdx.x >> 6] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      v[n] = slots[n][0];
+#pragma unroll
+      for (int w = 1; w < NT / 64; ++w) v[n] = with(v[n], slots[n][w]);
+    }
   }
-  return v;
 }
+template <int NT, bool MAX>
+__device__ __forceinline__ float over_row(float v, float (*slots)[kSlots<NT>]) {
+  float one[1] = {v};
+  over_row<NT, MAX>(one, slots);
+  return one[0];
+}
+
+// Sums of a row that one norm takes.
+constexpr int kNormSums = 5;
 
 // Centres the row's values (layer norm; those behind its end are zeros and stay so) and returns what they are to be
 // multiplied with.  Where the sums leave float32 while the values are finite, values and eps are first brought down by a
@@ -58,41 +73,46 @@ __device__ __forceinline__ float normalize(float (&v)[P][8], const bool (&in)[P]
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[i][e], v[i][e], ss);
     return ss;
   };
-  auto centre = [&](float* slot) __attribute__((always_inline)) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += v[i][e];
-    const float mean = over_row<NT, false>(sum, slot) * inv_k;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? v[i][e] - mean : 0.f;
-    return mean;
-  };
   if (!layer) {
-    const float ss = over_row<NT, false>(squares(), slots[0]);
+    const float ss = over_row<NT, false>(squares(), slots);
     if (ss < __builtin_inff()) return 1.0f / __builtin_sqrtf(__builtin_fmaf(ss, inv_k, eps));
   }
   // layer norm, or squares beyond float32 (the values as they were)
-  float amax = 0.f;
+  float ends[2] = {-__builtin_inff(), -__builtin_inff()};     // the largest value, and less the least
 #pragma unroll
   for (int i = 0; i < P; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(v[i][e]));
-  amax = over_row<NT, true>(amax, slots[1]);
+    for (int e = 0; e < 8; ++e) {
+      if (!in[i]) continue;
+      ends[0] = __builtin_elementwise_maximum(ends[0], v[i][e]);
+      ends[1] = __builtin_elementwise_maximum(ends[1], -v[i][e]);
+    }
+  over_row<NT, true>(ends, slots + 1);
+  const float amax = __builtin_elementwise_maximum(ends[0], ends[1]);
   if (amax > 0x1p56f && amax < __builtin_inff()) {            // (2^15 squares of 2^56 stay inside)
     const int down = -__builtin_amdgcn_frexp_expf(amax);
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = __builtin_ldexpf(v[i][e], down);
+    for (float& v : ends) v = __builtin_ldexpf(v, down);
     // (a row of one value has no variance left: not over zero, which would make its zeros NaN)
     eps = fmaxf(__builtin_ldexpf(eps, 2 * down), 0x1p-126f);
   }
-  if (layer) centre(slots[2]);
-  const float ss = over_row<NT, false>(squares(), slots[3]);
+  if (layer) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += v[i][e];
+    // (values that are not finite make the squares NaN, whatever the mean)
+    const float mean = fmaxf(fminf(over_row<NT, false>(sum, slots + 3) * inv_k, ends[0]), -ends[1]);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = in[i] ? v[i][e] - mean : 0.f;
+  }
+  const float ss = over_row<NT, false>(squares(), slots + 4);
   return 1.0f / __builtin_sqrtf(__builtin_fmaf(ss, inv_k, eps));
 }
 
@@ -127,7 +147,7 @@ struct RawRow {
 template <int T, bool R32, int NT, int P, bool KEEP>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_rows_kernel(NormArgs a) {
   constexpr int RPB = NT < 256 ? 256 / NT : 1;                // rows per workgroup
-  __shared__ float slots[2][9][kSlots<NT>];                   // one row's sums while another's are still read
+  __shared__ float slots[2][2 * kNormSums + 1][kSlots<NT>];   // one row's sums while another's are still read
   const int tid = threadIdx.x % NT;
   const int per_row = (int)(a.k >> 3);
   const float inv_k = 1.0f / (float)a.k;
@@ -241,7 +261,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_rows_kernel(NormArgs
       }
     }
     if (a.norm == 0) continue;
-    const float f = normalize<NT, P>(u, in, a.norm == kNormLayer, inv_k, a.eps, slot + 4);
+    const float f = normalize<NT, P>(u, in, a.norm == kNormLayer, inv_k, a.eps, slot + kNormSums);
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (in[i]) {
@@ -279,7 +299,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_rows_kernel(NormArgs
       for (int i = 0; i < P; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = __builtin_elementwise_maximum(amax, fabsf(u[i][e]));
-      amax = over_row<NT, true>(amax, slot[8]);
+      amax = over_row<NT, true>(amax, slot + 2 * kNormSums);
       float sc = amax / (a.code == A_FP8 ? 448.0f : 127.0f);  // correctly rounded division
       if (sc == 0.0f) sc = 1.0f;
       if (!(amax < __builtin_inff())) sc = __builtin_nanf("");

@@ -48,3 +48,46 @@ def test_constants_beyond_the_range_of_squares(k, post):
     for dtype, res in (("bf16", "bf16"), ("bf16", "f32")):
         out, want, _, _ = _run(k, values, dtype, res, post=post)
         assert torch.equal(out.float(), want.float().expand_as(out))
+
+
+KS = [8, 40, 128, 136, 512, 1000, 1416, 4096, 5120, 8192, 8200, 20000, 32768]
+VALUES = [1.0, -600.0, 1e-3, 12345.0, 0.1, 3e4]
+
+
+@pytest.mark.parametrize("k", KS)
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+def test_any_constant(k, dtype, res):
+    values = VALUES + ([1e30, -3e38, 1e-30] if res != "f16" else [])
+    out, want, _, _ = _run(k, values, dtype, res)
+    assert torch.equal(out.float(), want.float().expand_as(out))
+    out, _, _, _ = _run(k, VALUES, dtype, res, post=True)
+    assert not out.any()
+    for code in (qg.A_FP8_E4M3, qg.A_INT8):
+        _, _, codes, scale = _run(k, values, dtype, res, code)
+        assert not (codes & (0x7F if code == qg.A_FP8_E4M3 else 0xFF)).any() and (scale == 1).all()   # (e4m3 has a zero below 0)
+
+
+@pytest.mark.parametrize("k", [40, 1416, 5120, 20000])
+def test_rows_of_one_value_but_one(k):
+    # one value beside the others, its place first, last or between: the mean is the others', but for its share
+    for at in (0, k // 2, k - 1):
+        x = torch.full((3, k), 50.0, device="cuda")
+        x[:, at] += torch.tensor([1.0, 1000.0, -7.0], device="cuda")
+        out = torch.full((3, k), float("nan"), dtype=torch.bfloat16, device="cuda")
+        qg.norm_rows(qg.make_norm_desc(qg.N_LAYER, qg.O_BF16, k, 1e-6, res_type=qg.L_F32), 3, None, x, None, out)
+        d = x.double() - x.double().mean(1, keepdim=True)
+        z = d / torch.sqrt((d * d).mean(1, keepdim=True) + 1e-6)
+        # of z, half a step of bf16 and a few roundings; of the mean, 64 roundings of 2^-24 of its terms, over the deviation
+        noise = 2.0 ** -18 * x.double().abs().mean(1, keepdim=True) / torch.sqrt((d * d).mean(1, keepdim=True) + 1e-6)
+        assert ((out.double() - z).abs() <= (2.0 ** -8 + 2.0 ** -16) * z.abs() + noise).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("k", [40, 520, 1416, 9000])
+def test_constants_beside_values_that_are_not_finite(value, k):
+    for at in (0, k - 1):
+        x = torch.full((3, k), 5.0, dtype=torch.bfloat16, device="cuda")
+        x[1, at] = value
+        out = torch.zeros((3, k), dtype=torch.bfloat16, device="cuda")
+        qg.norm_rows(qg.make_norm_desc(qg.N_LAYER, qg.O_BF16, k, 1e-6), 3, None, x, None, out)
+        assert torch.isnan(out[1]).all() and not out[[0, 2]].any()
