@@ -444,7 +444,8 @@ qg_status qg_moe_combine(const void* y, const float* weights, const int32_t* top
  *   res, res_out device rows of k of res_type (`type`'s, or QG_L_F32), res_stride apart; res_out may be res
  *   gate         device [k] of `type` (gate_stride 0) or rows of k gate_stride apart, or NULL (1)
  *   post_weight, weight, bias   device [k] of `type`, or NULL
- *   out          device rows of k of `type`, out_stride apart, or NULL; may be y (with the same stride)
+ *   out          device rows of k of `type`, out_stride apart, or NULL; may be y, or res where that is not res_out
+ *                (an output in an input's place has its type and stride, else QG_ERR_INVALID_ARG)
  *   codes, scale with code_type (else both NULL; contiguous rows):
  *     QG_A_FP8_E4M3, QG_A_INT8   uint8 / int8 [rows][k], float32 [rows]: as qg_quantize_e4m3_rows and
  *                qg_quantize_int8_rows (scale max|z| / 448 or / 127, 1 for a row of zeros); a row that holds a NaN

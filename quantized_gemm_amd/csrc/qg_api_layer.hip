@@ -128,6 +128,10 @@ qg_status qg_norm_rows(const qg_norm_desc* d, int64_t rows, const void* y, const
   for (const void* p : {y, res, (const void*)res_out, gate, post_weight, weight, bias, (const void*)out, (const void*)codes})
     if (!aligned16(p)) return QG_ERR_INVALID_ARG;
   if (d->code_type != QG_A_FP4_E2M1 && ((uintptr_t)scale & 3u) != 0) return QG_ERR_INVALID_ARG;
+  // an output in an input's place: row by row, or rows are overwritten before they are read
+  if (out && (out == res_out || (out == y && a.out_stride != a.y_stride) || (out == res && (res32 || a.out_stride != a.res_stride))))
+    return QG_ERR_INVALID_ARG;
+  if (res_out && res_out == y && (res32 || a.res_stride != a.y_stride)) return QG_ERR_INVALID_ARG;
   qg_status s = check_arch();
   if (s != QG_OK) return s;
   a.y = y; a.res = res; a.gate = gate; a.post_weight = post_weight; a.weight = weight; a.bias = bias;

@@ -1,0 +1,44 @@
+"""Outputs in an input's place give the same bits as beside it, for rows that a workgroup takes in turn too."""
+import pytest
+import torch
+
+import quantized_gemm_amd as qg
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    qg.lib()
+    yield
+
+
+def _wide(rows, k, pad, dtype):
+    return torch.randn((rows, k + pad), device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("rows,k", [(5, 64), (3100, 1416), (2100, 4096), (700, 8192), (40, 16384)])
+@pytest.mark.parametrize("pad", [0, 24])
+def test_norm(rows, k, pad):
+    torch.manual_seed(rows)
+    y, r, r32 = _wide(rows, k, pad, torch.bfloat16), _wide(rows, k, pad, torch.bfloat16), _wide(rows, k, pad, torch.float32)
+    w = torch.randn(k, device="cuda").to(torch.bfloat16)
+    one = dict(y_stride=k + pad, res_stride=k + pad, out_stride=k + pad)
+
+    def both(res, res_type, y, where):
+        d = qg.make_norm_desc(qg.N_RMS, qg.O_BF16, k, 1e-6, res_type=res_type, **one)
+        beside = torch.full_like(res, float("nan")), torch.full_like(r, float("nan"))
+        qg.norm_rows(d, rows, y, res, beside[0] if "res" in where or y is not None else None, beside[1], weight=w)
+        y2, res2 = None if y is None else y.clone(), res.clone()
+        inside = res2 if "res" in where else None, {"y": y2, "residual": res2, "": torch.empty_like(r)}[where["out"]]
+        qg.norm_rows(d, rows, y2, res2, inside[0], inside[1], weight=w)
+        torch.cuda.synchronize()
+        if inside[0] is not None:
+            assert torch.equal(inside[0][:, :k], beside[0][:, :k]) and torch.equal(inside[0][:, k:], res[:, k:])
+        assert torch.equal(inside[1][:, :k], beside[1][:, :k])
+
+    both(r, qg.L_BF16, y, dict(res=1, out="y"))
+    both(r32, qg.L_F32, y, dict(res=1, out="y"))
+    both(r, qg.L_BF16, y, dict(out="y"))
+    both(r, qg.L_BF16, None, dict(out="residual"))
