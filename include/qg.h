@@ -487,6 +487,7 @@ qg_status qg_norm_rows(const qg_norm_desc* desc, int64_t rows, const void* y, co
  *              token (topk 1, num_experts = num_adapters, block_m); the same map serves every product of a step.
  *              Tokens whose id is outside [0, num_adapters) have no adapter: their rows of y are not written.
  *   base, y    device rows of n, base_stride and y_stride apart: the shared product's output; y may be base
+ *              (with the same stride, else QG_ERR_INVALID_ARG)
  *   block_m    16, 64 or 128; qg_lora_block_m gives the best for a batch
  *   ws         qg_lora_workspace_bytes(desc, tokens, block_m) bytes
  * The result does not depend on where in the batch a token stands; it does, in its last bits, on the batch's size,

@@ -184,13 +184,14 @@ qg_status qg_lora(const qg_lora_desc* d, const void* x, const void* a_weight, co
     return QG_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws) || ws_bytes < qg_lora_workspace_bytes(d, tokens, block_m)) return QG_ERR_WORKSPACE;
   LoraArgs a{};
+  stride_of(d->x_stride, d->k, &a.x_stride);
+  stride_of(d->base_stride, d->n, &a.base_stride);
+  stride_of(d->y_stride, d->n, &a.y_stride);
+  if (y == base && a.y_stride != a.base_stride) return QG_ERR_INVALID_ARG;   // (rows overwritten before they are read)
   const int64_t blocks = block_capacity(tokens, d->num_adapters, block_m, &a.cap_rows);
   if (blocks * std::max(1, block_m / 64) * (d->n / 128 + d->num_slices) >= (int64_t)1 << 23) return QG_ERR_UNSUPPORTED;   // a launch takes fewer than 2^32 threads
   s = check_arch();
   if (s != QG_OK) return s;
-  stride_of(d->x_stride, d->k, &a.x_stride);
-  stride_of(d->base_stride, d->n, &a.base_stride);
-  stride_of(d->y_stride, d->n, &a.y_stride);
   a.x = x; a.a = a_weight; a.b = b_weight; a.base = base; a.y = y;
   a.ranks = ranks; a.scales = scales; a.sorted_ids = sorted_ids; a.expert_ids = expert_ids; a.num_post_pad = num_post_pad;
   a.part = (float*)ws;

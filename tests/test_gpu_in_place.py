@@ -42,3 +42,24 @@ def test_norm(rows, k, pad):
     both(r32, qg.L_F32, y, dict(res=1, out="y"))
     both(r, qg.L_BF16, y, dict(out="y"))
     both(r, qg.L_BF16, None, dict(out="residual"))
+
+
+@pytest.mark.parametrize("tokens,n,block", [(50, 136, 16), (300, 1864, 64), (700, 4096, 128), (3000, 5632, 128)])
+@pytest.mark.parametrize("rank", [16, 64, 128])
+def test_adapters(tokens, n, block, rank):
+    torch.manual_seed(tokens)
+    k, e, pad = 264, 3, 8
+    x, base = _wide(tokens, k, 0, torch.bfloat16), _wide(tokens, n, pad, torch.bfloat16)
+    a, b = torch.randn((e, 1, rank, k), device="cuda").to(torch.bfloat16), torch.randn((e, n, rank), device="cuda").to(torch.bfloat16)
+    ids = torch.randint(-1, e, (tokens,), dtype=torch.int32, device="cuda")
+    rows, blocks = qg.moe_capacity(tokens, 1, e, block)
+    at = [torch.empty(z, dtype=torch.int32, device="cuda") for z in (rows, blocks, 1)]
+    qg.moe_align(ids, tokens, 1, e, block, *at)
+    d = qg.make_lora_desc(qg.O_BF16, e, rank, k, [n], base_stride=n + pad, y_stride=n + pad)
+    ws = torch.empty(qg.lora_workspace_bytes(d, tokens, block), dtype=torch.uint8, device="cuda")
+    beside, inside = base.clone(), base.clone()
+    qg.lora(d, x, a, b, *at, tokens, block, base, beside, ws)
+    qg.lora(d, x, a, b, *at, tokens, block, inside, inside, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(beside, inside) and torch.equal(inside[:, n:], base[:, n:])
+    assert torch.equal(inside[ids < 0], base[ids < 0]) and not torch.equal(inside[ids >= 0], base[ids >= 0])

@@ -17,3 +17,10 @@ def test_norm_in_place_has_the_inputs_rows():
                      ((None, B, None, B), dict(out_stride=128)), ((None, B, None, B), dict(res_type=qg.L_F32)),
                      ((A, B, A, None), dict(res_type=qg.L_F32)), ((A, B, A, None), dict(y_stride=128)), ((A, B, C, C), {})):
         assert _norm(*args, **kw) == 1, (args, kw)
+
+
+def test_adapters_in_place_have_the_bases_rows():
+    for kw in (dict(base_stride=72), dict(y_stride=72), dict(base_stride=128, y_stride=72)):
+        d = qg.make_lora_desc(qg.O_BF16, 3, 16, 64, [64], **kw)
+        for block in (16, 64):
+            assert qg.lib().qg_lora(ctypes.byref(d), A, A, A, None, None, A, A, A, 4, block, B, B, C, 1 << 30, None) == 1
