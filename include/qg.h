@@ -539,8 +539,8 @@ qg_status qg_kv_read(const qg_kv_desc* desc, const void* cache, const int32_t* s
  * among them; its n queries stand at its last n places, and each sees the tokens up to its own place:
  *   out[i] = sum_t w_t V[t] / sum_t w_t,  w_t = exp(scale * q[i] . K[t]),  t <= seq_lens[b] - n + i
  * per query head; query head h reads key head h / (q_heads / kv_heads).  A query that sees no token gives zeros.
- * Softmax and sums are float32; bf16 weights are rounded to bf16 before they multiply the values, f16 ones keep
- * 16 bits and more.
+ * Softmax and sums are float32; bf16 weights are rounded to bf16 before they multiply the values (and are summed as
+ * rounded), f16 ones keep 16 bits and more.
  *   q, out       device rows of q_heads * head_dim of `type`, q_stride and out_stride apart (0: contiguous)
  *   block_table  device int32, rows of table_stride >= max_len / page_tokens pages (rounded up): page j of sequence b
  *                holds its tokens j * page_tokens and on.  Tokens of a page outside [0, num_pages) are not seen.

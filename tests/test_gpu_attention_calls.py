@@ -50,3 +50,22 @@ def test_malformed_offsets_take_rows_that_there_are(many):
         assert torch.isnan(c.out).any(1).sum() == torch.isnan(c.out).all(1).sum()
     c.offsets.copy_(torch.tensor([0, n, used, high, low], dtype=torch.int32))          # the first two as they should be
     c.run().check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("counts,lens", [([1, 1, 1], [40, 700, 3000]), ([12, 60, 200], [40, 90, 200]), ([3, 150, 2], [3000, 900, 33])])
+def test_weights_add_up_to_one(dtype, dim, counts, lens):
+    # values of one everywhere: the outputs are one, whatever the weights; scores up to ten powers of two apart, one token's
+    # weight above the others'.  Sums of float32 are off by 2^-13 at most, a quarter of the smallest step beside one and less.
+    c = Case(lens, 8, 2, dim, 16, counts=counts, dtype=dtype, sigma=2.0)
+    rng = np.random.default_rng(5)
+    width = 2 * dim
+    for i, n in enumerate(lens):
+        k = torch.from_numpy(rng.standard_normal((n, width)).astype(np.float32) * 2).to(c.q.dtype).cuda()
+        t = np.arange(n)
+        slots = c.table[i].cpu().numpy()[t // 16] * 16 + t % 16
+        qg.kv_append(c.desc, k, torch.ones_like(k), torch.from_numpy(slots.astype(np.int32)).cuda(), n, c.cache)
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, torch.ones_like(c.out))
