@@ -96,3 +96,40 @@ def attention(q, k, v, lens, counts, scale, seen=None):
                     mag[at + i, h] = (w * (1.0 + terms)) @ np.abs(vv) + (w @ terms) * np.abs(out[at + i, h])
         at += n
     return out, mag
+
+
+def attention_terms(q, k, v, lens, counts, scale, seen=None):
+    """attention() with what its roundings are bounded against kept apart, per output: a dict of
+    out;  wv: sum_t w_t |V_t|;  dev: a bound of sum_t w_t |V_t - out|;  dev2: sum_t (w_t (V_t - out))^2;
+    terms: a bound of sum_t w_t T_t |V_t - out|, T_t = |scale| sum |k q| of the score's terms, plus |score|.
+    An error e_t of the weights, relative to each and the same in their sum, moves an output by sum_t w_t e_t (V_t - out)
+    to first order: |e_t| <= e gives e * dev, independent errors of root mean square e give e * sqrt(dev2).
+    (The bounds are Cauchy's: sum w T |d| <= sqrt(sum w T^2) sqrt(sum w d^2).)"""
+    heads, dim = q.shape[1:]
+    r = {name: np.zeros(q.shape) for name in ("out", "wv", "dev", "dev2", "terms")}
+    at = 0
+    for b, n in enumerate(counts):
+        if n == 0:
+            continue
+        kv = k[b].shape[1]
+        places = lens[b] - n + np.arange(n)
+        vis = np.arange(lens[b])[None, :] <= places[:, None]
+        if seen is not None:
+            vis = vis & seen[b][None, :]
+        some = vis.any(axis=1)
+        for h in range(heads):
+            kk, vv = k[b][:, h // (heads // kv)], v[b][:, h // (heads // kv)]
+            qq = q[at:at + n, h]
+            s = np.where(vis, scale * (qq @ kk.T), -np.inf)
+            w = np.exp(s - np.where(some, s.max(axis=1, initial=-np.inf), 0.0)[:, None])
+            w /= np.where(some, w.sum(axis=1), 1.0)[:, None]
+            t = abs(scale) * (np.abs(qq) @ np.abs(kk).T) + np.where(vis, np.abs(s), 0.0)
+            out, w2 = w @ vv, w * w
+            dev = np.sqrt(np.maximum(w @ (vv * vv) - out * out * w.sum(axis=1)[:, None], 0.0))
+            r["out"][at:at + n, h] = out
+            r["wv"][at:at + n, h] = w @ np.abs(vv)
+            r["dev"][at:at + n, h] = dev
+            r["dev2"][at:at + n, h] = np.maximum(w2 @ (vv * vv) - 2 * out * (w2 @ vv) + out * out * w2.sum(axis=1)[:, None], 0.0)
+            r["terms"][at:at + n, h] = np.sqrt((w * t * t).sum(axis=1))[:, None] * dev
+        at += n
+    return r
