@@ -228,7 +228,7 @@ def prepare_lora(s):
     qg.moe_align(s["ids"], m, 1, e, s["block"], *s["map"])
     s["ws"] = torch.empty(qg.lora_workspace_bytes(s["desc"], m, s["block"]), dtype=torch.uint8, device="cuda")
     s["y"] = torch.empty((m, width), dtype=DT[s["dtype"]], device="cuda")[:, :s["n"]]
-    s["y"].copy_(s["base"])   # rows without an adapter are not written
+    s["some_without"] = bool((s["ids"] < 0).any())
 
 
 def prepare_kv(s):
@@ -301,7 +301,10 @@ def own_norm(s):
 
 def own_lora(s):
     import quantized_gemm_amd as qg
-    qg.lora(s["desc"], s["x"], s["a"], s["b"], *s["map"], s["tokens"], s["block"], s["base"], s["y"], s["ws"],
+    base = s["base"]
+    if s["some_without"]:   # the rows of tokens without an adapter are not written: y in base's place
+        base = s["y"].copy_(base)
+    qg.lora(s["desc"], s["x"], s["a"], s["b"], *s["map"], s["tokens"], s["block"], base, s["y"], s["ws"],
             ranks=s["ranks"], scales=s["scales"])
     return s["y"]
 
