@@ -124,7 +124,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int hk, int split, 
 template <int T, int D>
 __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(2))) void attention_kernel(AttnArgs a) {
   constexpr bool HILO = T == O_F16;
-  constexpr int RT = 1;
+  constexpr int RT = 1;                             // row tiles (the same without the loops over them is 1 to 3% slower)
   constexpr int KW = D / 32, NJ = D / 16;           // MFMAs of a score tile; tiles of 16 output values
   constexpr int OP = D + 4;
   __shared__ __attribute__((aligned(16))) float so[kAttnWaves * 16 * OP];
@@ -612,12 +612,6 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
       for (int t = 0; t < RT; ++t) {
         sc[t][h] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], qf[t][j], j == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sc[t][h]);
         if constexpr (HILO) sc[t][h] = mfma16x16x32<A_BF16>(ring[i % (AHEAD + 1)], ql[t][j], sc[t][h]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-#pragma unroll
-      for (int t = 0; t < RT * (HILO ? 2 : 1); ++t) {
       }
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -189,7 +189,7 @@ struct AttnArgs {
   int64_t table_stride, q_stride, out_stride, num_pages, tokens, rows;   // rows: tokens * q_heads
   int batch, q_heads, kv_heads, group, dim, page_shift, max_q, max_len;
   int nsplit, chunk;         // parts at most, and steps of 32 tokens of a part
-  int tile_rows;             // rows of a wave
+  int tile_rows;             // rows of a workgroup
   uint32_t group_inv;        // ceil(2^32 / group)
   float scale_log2;          // |scale| * log2(e)
   uint32_t q_sign;           // 0x80008000 where scale is negative: turned into the queries

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a) {
 
 // a launch takes fewer than 2^32 threads
 template <typename F>
-static void in_parts(const KvArgs& all, int type, F one) {
+static void in_parts(const KvArgs& all, F one) {
   const int64_t per = (int64_t)2 * all.heads * (all.dim / 8), most = ((int64_t)1 << 31) / per;
   for (int64_t t = 0; t < all.tokens; t += most) {
     KvArgs a = all;
@@ -104,14 +104,14 @@ static void in_parts(const KvArgs& all, int type, F one) {
 }
 
 void launch_kv_append(const KvArgs& a, int type, hipStream_t st) {
-  in_parts(a, type, [&](const KvArgs& p, dim3 grid) {
+  in_parts(a, [&](const KvArgs& p, dim3 grid) {
     if (type == O_BF16) hipLaunchKernelGGL(kv_append_kernel<O_BF16>, grid, dim3(256), 0, st, p);
     else hipLaunchKernelGGL(kv_append_kernel<O_F16>, grid, dim3(256), 0, st, p);
   });
 }
 
 void launch_kv_read(const KvArgs& a, int type, hipStream_t st) {
-  in_parts(a, type, [&](const KvArgs& p, dim3 grid) {
+  in_parts(a, [&](const KvArgs& p, dim3 grid) {
     if (type == O_BF16) hipLaunchKernelGGL(kv_read_kernel<O_BF16>, grid, dim3(256), 0, st, p);
     else hipLaunchKernelGGL(kv_read_kernel<O_F16>, grid, dim3(256), 0, st, p);
   });
