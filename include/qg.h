@@ -492,7 +492,8 @@ qg_status qg_norm_rows(const qg_norm_desc* desc, int64_t rows, const void* y, co
  *   ws         qg_lora_workspace_bytes(desc, tokens, block_m) bytes
  * The result does not depend on where in the batch a token stands; it does, in its last bits, on the batch's size,
  * which sets how K is split.  max_rank <= 256 and a multiple of 8, num_adapters <= 512, num_slices <= 8, n % 8 == 0,
- * k % 8 == 0, slice ends ascending to n, all but the last multiples of 32.
+ * k % 8 == 0, slice ends ascending to n, all but the last multiples of 32; tokens, n and k <= 2^24, and blocks (of 64
+ * tokens where block_m is 128) times n / 128 + num_slices below 2^23.
  */
 typedef struct {
   int32_t type;          /* QG_O_* of x, a, b, base and y                    */
@@ -519,7 +520,7 @@ qg_status qg_lora(const qg_lora_desc* desc, const void* x, const void* a, const 
  *                 call's slots are distinct: one given twice holds any mix of its rows.
  *   qg_kv_read    writes the slots' keys and values back as contiguous rows of `type` (f16: values above 65504 are
  *                 infinite; zeros for a slot outside the cache)
- * head_dim 64, 128 or 256; page_tokens a power of two from 16 to 256; num_pages * page_tokens < 2^31.
+ * head_dim 64, 128 or 256; kv_heads <= 1024; page_tokens a power of two from 16 to 256; num_pages * page_tokens < 2^31.
  */
 typedef struct {
   int32_t type;          /* QG_O_* of the rows, and of queries and outputs   */
@@ -550,9 +551,12 @@ qg_status qg_kv_read(const qg_kv_desc* desc, const void* cache, const int32_t* s
  *                per sequence (max_q 1, tokens == batch)
  *   tokens       rows of q and out.  Rows that belong to no sequence are neither read nor written.
  *   ws           qg_attention_workspace_bytes(...) bytes (0: none needed)
- * q_heads is a multiple of kv_heads, at most 256 times it; batch and max_q <= 65535.
- * scale is finite, in powers of two too (below 2.3e38).
+ * q_heads is a multiple of kv_heads, at most 256 times it; batch and max_q <= 65535, tokens <= 2^24, max_len <= 2^30, and
+ * max_q * q_heads / kv_heads rows in 65535 tiles (of 64 rows and more) of all parts, else QG_ERR_UNSUPPORTED.
+ * scale is finite, in powers of two too (below 2.3e38).  A query whose scores all lie below float32's range gives zeros.
  * The result depends on batch, max_q and max_len (which set how the tokens are split) in its last bits only.
+ * The split takes every sequence to have max_q queries: single tokens of long sequences and long chunks of prompts are
+ * faster in two calls than in one.
  */
 size_t qg_attention_workspace_bytes(const qg_kv_desc* desc, int32_t q_heads, int64_t batch, int64_t max_q, int64_t tokens,
                                     int64_t max_len);

@@ -443,7 +443,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
 // rows, D = 128: 281 us).  RT is what leaves room for two waves per SIMD, one multiplying while the other
 // takes exponentials: those bound it, about as much as the products do.  Products go before other waves' exponentials
 // (s_setprio: 5%), and the scheduler mixes a step's conversion into the products of the step before (10 to 15%).  D = 128,
-// bf16: a prompt of 4608 tokens (32 query heads over 8) 201 us, 865 TFLOP/s.
+// bf16: a prompt of 4608 tokens (32 query heads over 8) 201 to 220 us from card to card, 790 to 865 TFLOP/s.
 template <int T, int D, int RT>
 __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(2))) void attention_rows_kernel(AttnArgs a) {
   constexpr bool HILO = T == O_F16;
@@ -850,7 +850,11 @@ void launch_one(AttnArgs a, hipStream_t st) {
 // sequences had the maximum, none shorter than 512 tokens (what a part costs beside its tokens).  Many rows: only while a
 // workgroup per tile leaves CUs without two (a prompt of 4608 tokens, 768 tiles: whole 210 us, in parts 222 and 15 to join
 // them; 4 sequences of up to 4608 tokens with 512 new ones each, 352 tiles: whole 203 us, in three parts 158
-// and 18, in two 160 and 12; one sequence of 8192 with 2048 new ones, 344 tiles: three 321 and 21, two 358 and 15).
+// and 18, in two 160 and 12; one sequence of 8192 with 2048 new ones, 344 tiles: three 321 and 21, two 358 and 15: three
+// cost the first 4 us and save the second 31).  Every sequence counts as if it had max_q queries: single tokens of long
+// sequences beside a chunk are not split (one chunk of 512 among 63 single tokens of up to 32768, 64 heads over 8: 1272 us,
+// in two calls 134 and 225), and more than 16 rows per key head go to the many rows' kernel (3 queries of 64 sequences of up
+// to 8192, 24 rows: 324 us, one query 59 and 6).
 AttnSplit attn_split(int64_t batch, int q_heads, int kv_heads, int64_t max_q, int64_t max_len, int dim, int type) {
   const int64_t rows = max_q * (q_heads / kv_heads);
   const bool share = shares_rows(rows);

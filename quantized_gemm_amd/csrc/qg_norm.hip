@@ -9,15 +9,16 @@
 // second sum over registers), which loses nothing where the mean is far from zero.  The mean is kept between the row's
 // least and largest value: of a row whose values are all alike zeros are left, not a last bit of them over sqrt(eps).
 //
-// Bound by bytes.  A row stays in registers between the sums (P pieces of 8 values per thread), so that each
+// Bound by bytes.  A row stays in registers between the sums (P pieces of 8 values per thread; of rows above 16384 values
+// 63 to 99 registers' worth goes through scratch memory: 2048 rows of 32768 225 us, 2.4 TB/s), so that each
 // input is read once; NT threads share a row, and a sum over them is a wave's exchange plus one barrier.  Rows of 1025 to
 // 8192 values are taken in turn by a workgroup (KEEP), the next one's loads on their way during one's sums, and weights and
 // a shared gate stay in registers.  Longer rows lack the registers for it (2048 rows of 16384 values: 57 us, in turn 150),
 // and shorter ones need no barrier to wait at (65536 rows of 512: 47 us, in turn 53); those are one to a workgroup or part
 // of it, and read the weights again.  Workgroups that are no more than the GPU holds at once: 16384 rows of 4096 in 768
 // workgroups 95 us, in 1024 115.  Measured: those (both norms, gate, residual, to e4m3) 95 us, 4.9 TB/s (155 with a
-// workgroup per row, 137 with sums exchanged through LDS); 4096 rows of 7168 to e4m3 45 us; one 4.3 us; 65536 rows of 128 13
-// us (29 with a whole wave to a row).
+// workgroup per row, 137 with sums exchanged through LDS), to MXFP4 83; 4096 rows of 7168 to e4m3 45 us, to MXFP4 40; one
+// 4.3 us; 65536 rows of 128 13 us (29 with a whole wave to a row).
 #include "qg_device.h"
 #include "qg_kernels.h"
 #include "qg_rows.h"
