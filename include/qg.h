@@ -445,7 +445,7 @@ qg_status qg_moe_combine(const void* y, const float* weights, const int32_t* top
  *   gate         device [k] of `type` (gate_stride 0) or rows of k gate_stride apart, or NULL (1)
  *   post_weight, weight, bias   device [k] of `type`, or NULL
  *   out          device rows of k of `type`, out_stride apart, or NULL; may be y, or res where that is not res_out
- *                (an output in an input's place has its type and stride, else QG_ERR_INVALID_ARG)
+ *                (an output in an input's place has its type and, of more than one row, its stride, else QG_ERR_INVALID_ARG)
  *   codes, scale with code_type (else both NULL; contiguous rows):
  *     QG_A_FP8_E4M3, QG_A_INT8   uint8 / int8 [rows][k], float32 [rows]: as qg_quantize_e4m3_rows and
  *                qg_quantize_int8_rows (scale max|z| / 448 or / 127, 1 for a row of zeros); a row that holds a NaN
@@ -487,7 +487,7 @@ qg_status qg_norm_rows(const qg_norm_desc* desc, int64_t rows, const void* y, co
  *              token (topk 1, num_experts = num_adapters, block_m); the same map serves every product of a step.
  *              Tokens whose id is outside [0, num_adapters) have no adapter: their rows of y are not written.
  *   base, y    device rows of n, base_stride and y_stride apart: the shared product's output; y may be base
- *              (with the same stride, else QG_ERR_INVALID_ARG)
+ *              (of more than one token with the same stride, else QG_ERR_INVALID_ARG)
  *   block_m    16, 64 or 128; qg_lora_block_m gives the best for a batch
  *   ws         qg_lora_workspace_bytes(desc, tokens, block_m) bytes
  * The result does not depend on where in the batch a token stands; it does, in its last bits, on the batch's size,

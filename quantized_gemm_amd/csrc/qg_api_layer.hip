@@ -129,9 +129,11 @@ qg_status qg_norm_rows(const qg_norm_desc* d, int64_t rows, const void* y, const
     if (!aligned16(p)) return QG_ERR_INVALID_ARG;
   if (d->code_type != QG_A_FP4_E2M1 && ((uintptr_t)scale & 3u) != 0) return QG_ERR_INVALID_ARG;
   // an output in an input's place: row by row, or rows are overwritten before they are read
-  if (out && (out == res_out || (out == y && a.out_stride != a.y_stride) || (out == res && (res32 || a.out_stride != a.res_stride))))
+  auto apart = [&](int64_t s, int64_t t) { return rows > 1 && s != t; };
+  if (out && (out == res_out || (out == y && apart(a.out_stride, a.y_stride)) ||
+              (out == res && (res32 || apart(a.out_stride, a.res_stride)))))
     return QG_ERR_INVALID_ARG;
-  if (res_out && res_out == y && (res32 || a.res_stride != a.y_stride)) return QG_ERR_INVALID_ARG;
+  if (res_out && res_out == y && (res32 || apart(a.res_stride, a.y_stride))) return QG_ERR_INVALID_ARG;
   qg_status s = check_arch();
   if (s != QG_OK) return s;
   a.y = y; a.res = res; a.gate = gate; a.post_weight = post_weight; a.weight = weight; a.bias = bias;
@@ -187,7 +189,7 @@ qg_status qg_lora(const qg_lora_desc* d, const void* x, const void* a_weight, co
   stride_of(d->x_stride, d->k, &a.x_stride);
   stride_of(d->base_stride, d->n, &a.base_stride);
   stride_of(d->y_stride, d->n, &a.y_stride);
-  if (y == base && a.y_stride != a.base_stride) return QG_ERR_INVALID_ARG;   // (rows overwritten before they are read)
+  if (y == base && tokens > 1 && a.y_stride != a.base_stride) return QG_ERR_INVALID_ARG;   // (rows overwritten before they are read)
   const int64_t blocks = block_capacity(tokens, d->num_adapters, block_m, &a.cap_rows);
   if (blocks * std::max(1, block_m / 64) * (d->n / 128 + d->num_slices) >= (int64_t)1 << 23) return QG_ERR_UNSUPPORTED;   // a launch takes fewer than 2^32 threads
   s = check_arch();

@@ -63,3 +63,24 @@ def test_adapters(tokens, n, block, rank):
     torch.cuda.synchronize()
     assert torch.equal(beside, inside) and torch.equal(inside[:, n:], base[:, n:])
     assert torch.equal(inside[ids < 0], base[ids < 0]) and not torch.equal(inside[ids >= 0], base[ids >= 0])
+
+
+def test_one_row_has_no_stride():
+    torch.manual_seed(1)
+    k = 4096
+    y, r = (torch.randn((1, k), device="cuda").to(torch.bfloat16) for _ in "yr")
+    w = torch.randn(k, device="cuda").to(torch.bfloat16)
+    beside, inside = torch.empty_like(y), y.clone()
+    for out, src in ((beside, y), (inside, inside)):
+        qg.norm_rows(qg.make_norm_desc(qg.N_RMS, qg.O_BF16, k, 1e-6, y_stride=8 * k), 1, src, r, None, out, weight=w)
+    a, b = torch.randn((1, 1, 16, k), device="cuda").to(torch.bfloat16), torch.randn((1, k, 16), device="cuda").to(torch.bfloat16)
+    rows, blocks = qg.moe_capacity(1, 1, 1, 16)
+    at = [torch.empty(z, dtype=torch.int32, device="cuda") for z in (rows, blocks, 1)]
+    qg.moe_align(torch.zeros(1, dtype=torch.int32, device="cuda"), 1, 1, 1, 16, *at)
+    d = qg.make_lora_desc(qg.O_BF16, 1, 16, k, [k], base_stride=8 * k)
+    ws = torch.empty(qg.lora_workspace_bytes(d, 1, 16), dtype=torch.uint8, device="cuda")
+    far, near = torch.empty_like(y), r.clone()
+    qg.lora(d, y, a, b, *at, 1, 16, r, far, ws)
+    qg.lora(d, y, a, b, *at, 1, 16, near, near, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(beside, inside) and torch.equal(far, near) and not torch.equal(near, r)
