@@ -84,7 +84,7 @@ __device__ __forceinline__ int over_group(int row, const AttnArgs& a) {
 // A sequence's rows of queries and outputs.
 __device__ __forceinline__ Queries queries_of(const AttnArgs& a, int b) {
   if (!a.q_offsets) return Queries{b, 1};
-  return sequence_queries(a.q_offsets[b], a.q_offsets[b + 1], a.tokens, a.max_q);
+  return sequence_queries(a.q_offsets[b], a.q_offsets[b + 1], (int)a.tokens, a.max_q);   // (at most 2^24)
 }
 
 // The sequence of workgroup (., y, z).  Workgroups go to the eight dies and on each to its four shader engines in turn, whatever
