@@ -409,10 +409,11 @@ def _table(table, page_tokens: int, max_len: int):
     """Address of a block table and the distance of its rows, as its tensor has them (a slice of a wider one, too)."""
     if table is None:
         return None, 0
-    width = table.shape[-1]
-    if width * page_tokens < max_len or (width > 1 and table.stride(-1) != 1) or (table.dim() > 2 and not table.is_contiguous()):
+    shape, stride = table.shape, table.stride()      # (each asked for once: the host's time of a small call)
+    width = shape[-1]
+    if width * page_tokens < max_len or (stride[-1] != 1 and width > 1) or (len(shape) > 2 and not table.is_contiguous()):
         raise QGError(1, "qg_attention")
-    return table.data_ptr(), table.stride(0) if table.dim() == 2 and table.shape[0] > 1 else width
+    return table.data_ptr(), stride[0] if len(shape) == 2 and shape[0] > 1 else width
 
 
 def attention(desc: KvDesc, q, q_heads: int, cache, block_table, seq_lens, batch: int, max_len: int, scale: float, out, ws=None,
