@@ -443,7 +443,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu
 // rows, D = 128: 281 us).  RT is what leaves room for two waves per SIMD, one multiplying while the other
 // takes exponentials: those bound it, about as much as the products do.  Products go before other waves' exponentials
 // (s_setprio: 5%), and the scheduler mixes a step's conversion into the products of the step before (10 to 15%).  D = 128,
-// bf16: a prompt of 4608 tokens (32 query heads over 8) 201 to 220 us from card to card, 790 to 865 TFLOP/s.
+// bf16: a prompt of 4608 tokens (32 query heads over 8) 195 to 220 us from card to card, 790 to 890 TFLOP/s.
 template <int T, int D, int RT>
 __global__ __launch_bounds__(64 * kAttnWaves) __attribute__((amdgpu_waves_per_eu(2))) void attention_rows_kernel(AttnArgs a) {
   constexpr bool HILO = T == O_F16;
